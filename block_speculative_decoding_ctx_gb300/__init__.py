@@ -66,6 +66,40 @@ class dflash_sampling(ctypes.Structure):
                 ("seeds", ctypes.c_void_p), ("step", ctypes.c_uint64)]
 
 
+DFLASH_TYPE_BF16, DFLASH_TYPE_F16, DFLASH_TYPE_F32 = 0, 1, 2
+DFLASH_CACHE_BF16, DFLASH_CACHE_F16, DFLASH_CACHE_E4M3 = 0, 1, 2
+
+_TYPES = {torch.bfloat16: DFLASH_TYPE_BF16, torch.float16: DFLASH_TYPE_F16,
+          torch.float32: DFLASH_TYPE_F32}
+_CACHES = {torch.bfloat16: DFLASH_CACHE_BF16, torch.float16: DFLASH_CACHE_F16,
+           torch.float8_e4m3fn: DFLASH_CACHE_E4M3, torch.uint8: DFLASH_CACHE_E4M3}
+
+
+class dflash_paged_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale")] + [
+        (n, ctypes.c_longlong) for n in ("k_page_stride", "v_page_stride")] + [
+        (n, ctypes.c_int) for n in ("n_pages", "n_kv_heads", "page_size", "head_dim", "format")]
+
+
+class dflash_paged_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("row_start", "kv_len", "page_table")] + [
+        ("table_stride", ctypes.c_longlong)] + [
+        (n, ctypes.c_int) for n in ("B", "max_pages", "rows")]
+
+
+class dflash_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
+class dflash_logit_rules(ctypes.Structure):
+    _fields_ = [("counts", ctypes.c_void_p), ("prompt_mask", ctypes.c_void_p),
+                ("req_slot", ctypes.c_void_p), ("slots", ctypes.c_int)] + [
+        (n, ctypes.c_void_p) for n in ("draft", "repetition", "frequency", "presence",
+                                       "bias_start", "bias_ids", "bias_vals")] + [
+        ("n_bias", ctypes.c_int), ("allow", ctypes.c_void_p)]
+
+
 class dflash_draft_out(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "topk_ids", "topk_vals", "lse", "logits", "q", "draft")]
@@ -110,6 +144,15 @@ def lib():
         "dflash_quantize_e4m3": (_I, [_P, _I, _I, _P, _P, _P]),
         "dflash_verify_noalloc": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, ctypes.c_uint64, _P, _P, _P,
                                        _P, _P]),
+        "dflash_paged_workspace_bytes": (_SZ, []),
+        "dflash_paged_append": (_I, [_P, _P, _I, _P, _P, _P, _SZ, _P]),
+        "dflash_paged_gather": (_I, [_P, _P, _I, _P, _P, _P, _SZ, _P]),
+        "dflash_paged_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+        "dflash_paged_attention": (_I, [_P, _P, _I, _I, _P, _P, _P, _I, ctypes.c_float, _I, _I, _P,
+                                        _SZ, _P]),
+        "dflash_logits_adjust_workspace_bytes": (_SZ, []),
+        "dflash_logits_adjust": (_I, [_I, _I, _I, _I, _P, ctypes.c_longlong, ctypes.c_longlong, _P,
+                                      ctypes.c_longlong, ctypes.c_longlong, _P, _P, _SZ, _P]),
         "dflash_profile_read": (_I, [_P, ctypes.POINTER(ctypes.c_float),
                                      ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I), _I,
                                      ctypes.POINTER(_I)]),
@@ -327,6 +370,172 @@ def dflash_quantize_e4m3(w, codes, scales, stream=None):
     rows, cols = w.shape
     _check(lib().dflash_quantize_e4m3(_ptr(w), rows, cols, _ptr(codes), _ptr(scales), _stream(stream)),
            "dflash_quantize_e4m3")
+
+
+# ------------------------------------------------- the target's side of a cycle
+
+class PagedCache:
+    """One layer's paged cache (see paged_cache); keeps its tensors alive."""
+
+    def __init__(self, struct, keep):
+        self.struct = struct
+        self.device = keep[0].device
+        self._keep = keep
+
+
+def _fit(name, t, dtype, shape, device):
+    """The tensor's address after checking its type, shape and device; it must
+    be contiguous.  None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _on_device(device):
+    if device.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None):
+    """A cache for the dflash_paged_* calls: pages [n_pages, n_kv_heads,
+    page_size, head_dim] of bfloat16, float16, or E4M3 codes (float8_e4m3fn or
+    uint8) with float32 scales [n_pages, n_kv_heads, page_size].  A page is
+    contiguous; pages may lie further apart (a slice of a larger tensor)."""
+    n, heads, size, hd = k_pages.shape
+    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
+        raise ValueError("k_pages and v_pages differ in shape, type or device")
+    if k_pages.dtype not in _CACHES:
+        raise ValueError(f"no cache of {k_pages.dtype}")
+    for t in (k_pages, v_pages):
+        if n and not t[0].is_contiguous():
+            raise ValueError("a page is not contiguous")
+    fmt = _CACHES[k_pages.dtype]
+    if (fmt == DFLASH_CACHE_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("E4M3 pages come with k_scale and v_scale, 16-bit pages without")
+    shape = (n, heads, size)
+    page = heads * size * hd
+    c = dflash_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(),
+                           _fit("k_scale", k_scale, torch.float32, shape, k_pages.device),
+                           _fit("v_scale", v_scale, torch.float32, shape, k_pages.device),
+                           k_pages.stride(0) if n > 1 else page, v_pages.stride(0) if n > 1 else page,
+                           n, heads, size, hd, fmt)
+    return PagedCache(c, (k_pages, v_pages, k_scale, v_scale))
+
+
+def _rows(name, t, device):
+    if t.dim() != 3 or t.device != device or (t.numel() and t.stride(2) != 1):
+        raise ValueError(f"{name}: expected [rows, heads, head_dim] on {device} with head_dim contiguous")
+    return dflash_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _paged_batch(row_start, kv_len, page_table, rows, device):
+    B = kv_len.shape[0]
+    _on_device(device)
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32 or \
+            page_table.device != device or (page_table.numel() and page_table.stride(1) != 1):
+        raise ValueError(f"page_table: expected int32 [{B}, max_pages] on {device}")
+    pages = page_table.shape[1]
+    return dflash_paged_batch(_fit("row_start", row_start, torch.int32, (B + 1,), device),
+                              _fit("kv_len", kv_len, torch.int64, (B,), device), page_table.data_ptr(),
+                              page_table.stride(0) if B > 1 else pages, B, pages, rows)
+
+
+def dflash_paged_workspace_bytes():
+    return int(lib().dflash_paged_workspace_bytes())
+
+
+def _paged_move(name, cache, k, v, row_start, kv_len, page_table, ws, stream):
+    c = cache.struct
+    if k.shape != v.shape or k.dtype != v.dtype or tuple(k.shape[1:]) != (c.n_kv_heads, c.head_dim):
+        raise ValueError(f"k and v: expected [rows, {c.n_kv_heads}, {c.head_dim}] of one type")
+    if k.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"no rows of {k.dtype}")
+    b = _paged_batch(row_start, kv_len, page_table, k.shape[0], cache.device)
+    rk, rv = _rows("k", k, cache.device), _rows("v", v, cache.device)
+    _check(getattr(lib(), name)(ctypes.byref(c), ctypes.byref(b), _TYPES[k.dtype], ctypes.byref(rk),
+                                ctypes.byref(rv), _ptr(ws), ws.numel(), _stream(stream)), name)
+
+
+def dflash_paged_append(cache, k, v, row_start, kv_len, page_table, ws, stream=None):
+    """Write rows k, v [rows, n_kv_heads, head_dim] into the cache; row_start
+    int32 [B + 1], kv_len int64 [B] (new rows counted), page_table int32
+    [B, max_pages]."""
+    _paged_move("dflash_paged_append", cache, k, v, row_start, kv_len, page_table, ws, stream)
+
+
+def dflash_paged_gather(cache, k, v, row_start, kv_len, page_table, ws, stream=None):
+    """Read the last row_start[b + 1] - row_start[b] positions of every request
+    back into k, v [rows, n_kv_heads, head_dim]."""
+    _paged_move("dflash_paged_gather", cache, k, v, row_start, kv_len, page_table, ws, stream)
+
+
+def dflash_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_rows):
+    return int(lib().dflash_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_rows))
+
+
+def dflash_paged_attention(cache, q, out, row_start, kv_len, page_table, max_rows, ws, lse=None,
+                           scale=None, causal=True, window=0, stream=None):
+    """q, out [rows, n_q_heads, head_dim]; lse float32 [rows, n_q_heads] or
+    None; scale None: 1 / sqrt(head_dim)."""
+    c = cache.struct
+    if q.shape != out.shape or q.dtype != out.dtype or q.dim() != 3 or q.shape[2] != c.head_dim:
+        raise ValueError(f"q and out: expected [rows, n_q_heads, {c.head_dim}] of one type")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"no rows of {q.dtype}")
+    b = _paged_batch(row_start, kv_len, page_table, q.shape[0], cache.device)
+    rq, ro = _rows("q", q, cache.device), _rows("out", out, cache.device)
+    _check(lib().dflash_paged_attention(
+        ctypes.byref(c), ctypes.byref(b), _TYPES[q.dtype], q.shape[1], ctypes.byref(rq), ctypes.byref(ro),
+        _fit("lse", lse, torch.float32, q.shape[:2], cache.device), int(max_rows),
+        c.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window), _ptr(ws),
+        ws.numel(), _stream(stream)), "dflash_paged_attention")
+
+
+def dflash_logits_adjust_workspace_bytes():
+    return int(lib().dflash_logits_adjust_workspace_bytes())
+
+
+def dflash_logits_adjust(logits, out, ws, counts=None, prompt_mask=None, req_slot=None, draft=None,
+                         repetition=None, frequency=None, presence=None, bias_start=None, bias_ids=None,
+                         bias_vals=None, allow=None, stream=None):
+    """logits [B, G, V] float32, bfloat16 or float16; out float32 [B, G, V]
+    (may be logits).  counts int32 [slots, V]; prompt_mask int32
+    [slots, ceil(V / 32)] bits; req_slot int32 [B]; draft int32 [B, G - 1];
+    repetition, frequency, presence float32 [B]; bias_start int32 [B + 1] with
+    bias_ids int32 and bias_vals float32 [n_bias]; allow int32
+    [B, G, ceil(V / 32)] bits."""
+    if logits.dim() != 3 or logits.dtype not in _TYPES or out.shape != logits.shape or \
+            out.dtype != torch.float32 or out.device != logits.device:
+        raise ValueError("logits and out: expected [B, G, V], out float32, on one device")
+    B, G, V = logits.shape
+    dev = logits.device
+    _on_device(dev)
+    if (V > 1 and (logits.stride(2) != 1 or out.stride(2) != 1)):
+        raise ValueError("the vocabulary is not contiguous")
+    words = (V + 31) // 32
+    slots = next((t.shape[0] for t in (counts, prompt_mask) if t is not None), 0)
+    n_bias = 0 if bias_ids is None else bias_ids.shape[0]
+    r = dflash_logit_rules(
+        _fit("counts", counts, torch.int32, (slots, V), dev),
+        _fit("prompt_mask", prompt_mask, torch.int32, (slots, words), dev),
+        _fit("req_slot", req_slot, torch.int32, (B,), dev), slots,
+        _fit("draft", draft, torch.int32, (B, G - 1), dev),
+        _fit("repetition", repetition, torch.float32, (B,), dev),
+        _fit("frequency", frequency, torch.float32, (B,), dev),
+        _fit("presence", presence, torch.float32, (B,), dev),
+        _fit("bias_start", bias_start, torch.int32, (B + 1,), dev),
+        _fit("bias_ids", bias_ids, torch.int32, (n_bias,), dev),
+        _fit("bias_vals", bias_vals, torch.float32, (n_bias,), dev), n_bias,
+        _fit("allow", allow, torch.int32, (B, G, words), dev))
+    _check(lib().dflash_logits_adjust(B, G, V, _TYPES[logits.dtype], _ptr(logits), logits.stride(0),
+                                      logits.stride(1), _ptr(out), out.stride(0), out.stride(1),
+                                      ctypes.byref(r), _ptr(ws), ws.numel(), _stream(stream)),
+           "dflash_logits_adjust")
 
 
 def quantize_weights_e4m3(weights, stream=None):

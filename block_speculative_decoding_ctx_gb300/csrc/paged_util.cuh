@@ -1,0 +1,47 @@
+// Device helpers shared by the paged-cache kernels.
+#pragma once
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace dfl {
+
+// Rows and length of request b; false (nothing of it is touched) if they do
+// not fit the call: row_start decreasing or past `rows`, kv_len negative or
+// longer than the page table.
+struct RequestSpan {
+  int s0, n;  // first row, rows
+  int len;    // kv_len
+};
+__device__ __forceinline__ bool request_span(const PagedBatch& p, int b, RequestSpan* r) {
+  const int s0 = __ldg(p.row_start + b), s1 = __ldg(p.row_start + b + 1);
+  const long long len = __ldg(reinterpret_cast<const long long*>(p.kv_len) + b);
+  r->s0 = s0;
+  r->n = s1 - s0;
+  r->len = (int)len;
+  return s0 >= 0 && s1 >= s0 && s1 <= p.rows && len >= 0 && len <= ((long long)p.max_pages << p.page_shift);
+}
+
+// Two E4M3 codes (low byte first) as two fp16 values: exact, NaN codes as NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (BF16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+}  // namespace dfl

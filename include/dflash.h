@@ -58,7 +58,8 @@
  * create/destroy are asynchronous on the given stream, never synchronise the
  * host, and may be captured into a CUDA graph.
  *
- * Workspace.  draft_block, ctx_append, probs and verify take a caller-owned
+ * Workspace.  draft_block, ctx_append, probs, verify and the target-side calls
+ * (paged_append, paged_gather, paged_attention, logits_adjust) take a caller-owned
  * device workspace of at least the size the matching *_workspace_bytes
  * function returns, 256-byte aligned, ZERO-FILLED BEFORE ITS FIRST USE.  The
  * library leaves the workspace's counter region zeroed after every call, so
@@ -363,6 +364,157 @@ int dflash_verify_noalloc(int mode, int B, int gamma, int vocab, const float* ta
  *   scales  float32 [rows] out
  * Asynchronous on the stream; allocates nothing. */
 int dflash_quantize_e4m3(const void* w, int rows, int cols, void* codes, float* scales,
+                         dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The target's side of a cycle: the model that verifies a block keeps its own
+ * keys and values in a paged cache, attends from the block's rows (or a chunk
+ * of a prompt) over it, and its logits are adjusted before dflash_probs /
+ * dflash_verify ("Speculative decoding" product doc, section "How it works":
+ * the target scores the whole block in one pass; the pages leave the target's
+ * kernels to the serving stack, so formats and rules here are the library's).
+ *
+ * Paged cache.  Position s of request b lives in row s % page_size of page
+ * page_table[b][s / page_size].  Pages may be shared between requests and lie
+ * in any order.  Formats:
+ *   BF16, F16  the rows as they are;
+ *   E4M3       8-bit codes (as DFLASH_WEIGHTS_E4M3) with one float32 scale
+ *              per (page, KV head, row): value = code * scale,
+ *              scale = max|row| / 448 (1 for a row of zeros; NaN for a row
+ *              that holds a NaN or an infinity, which then reads back as NaN),
+ *              code = value / scale rounded to nearest, ties to even.
+ *
+ * Rows.  q, k, v and the outputs hold the new rows of all requests one after
+ * another: request b owns rows row_start[b] .. row_start[b + 1] - 1, and its
+ * row j is position kv_len[b] - n_b + j with n_b = row_start[b + 1] -
+ * row_start[b] (kv_len counts the new rows).  n_b = 0 is allowed.  Rows at and
+ * after row_start[B] are neither read nor written.
+ *
+ * Device status (dflash_read_status) of these calls: DFLASH_ERR_SHAPE if
+ * row_start decreases or passes `rows`, kv_len[b] is negative or needs more
+ * than max_pages pages, or (attention) n_b > max_rows: that request is left
+ * out, its outputs stay as they were; also if a row to be written or read
+ * back would lie before position 0 (it is skipped; read back as zeros).
+ * DFLASH_ERR_ARG if a page id that is needed is outside [0, n_pages): such
+ * rows are not written, and read as zeros.
+ */
+enum { DFLASH_TYPE_BF16 = 0, DFLASH_TYPE_F16 = 1, DFLASH_TYPE_F32 = 2 };
+enum { DFLASH_CACHE_BF16 = 0, DFLASH_CACHE_F16 = 1, DFLASH_CACHE_E4M3 = 2 };
+
+/* One layer's cache (host struct).  Constraints: page_size 16, 32, 64 or 128;
+ * head_dim 64 or 128; pages 16-byte aligned; page strides multiples of 16
+ * bytes and at least n_kv_heads * page_size * head_dim elements. */
+typedef struct dflash_paged_cache {
+  void* k_pages;           /* [n_pages][n_kv_heads, page_size, head_dim], pages k_page_stride apart */
+  void* v_pages;
+  float* k_scale;          /* E4M3 only: float32 [n_pages, n_kv_heads, page_size]; else NULL */
+  float* v_scale;
+  long long k_page_stride; /* elements from one page to the next */
+  long long v_page_stride;
+  int n_pages;
+  int n_kv_heads;
+  int page_size;
+  int head_dim;
+  int format;              /* DFLASH_CACHE_* */
+} dflash_paged_cache;
+
+/* The requests of a call (host struct of device pointers). */
+typedef struct dflash_paged_batch {
+  const int32_t* row_start;  /* [B + 1] */
+  const int64_t* kv_len;     /* [B] */
+  const int32_t* page_table; /* [B, max_pages], rows table_stride apart */
+  long long table_stride;    /* elements, >= max_pages */
+  int B;
+  int max_pages;             /* max_pages * page_size < 2^30 */
+  int rows;                  /* rows the row tensors hold */
+} dflash_paged_batch;
+
+/* A tensor of rows (host struct): [rows, heads, head_dim], head_dim
+ * contiguous; 16-byte aligned, strides (in elements) multiples of 8. */
+typedef struct dflash_rows {
+  void* ptr;
+  long long row_stride;
+  long long head_stride;
+} dflash_rows;
+
+size_t dflash_paged_workspace_bytes(void); /* for append and gather */
+
+/* Write the new rows' keys and values into the cache, quantised if it is E4M3.
+ *   type  DFLASH_TYPE_BF16 or _F16, the type of k and v; a 16-bit cache has
+ *         the same type.
+ * Two rows of one call must not share a (page, row): which one stays would be
+ * undefined. */
+int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_batch* batch, int type,
+                        const dflash_rows* k, const dflash_rows* v, void* workspace,
+                        size_t ws_bytes, dflash_stream_t stream);
+
+/* Read the same positions back: k and v (written here) get rows
+ * kv_len[b] - n_b .. kv_len[b] - 1 of every request, code * scale rounded to
+ * `type`; a 16-bit cache has the type of k and v. */
+int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batch* batch, int type,
+                        const dflash_rows* k, const dflash_rows* v, void* workspace,
+                        size_t ws_bytes, dflash_stream_t stream);
+
+/* Attention of the new rows over the cache (which already holds them).  Query
+ * head h reads KV head h / (n_q_heads / n_kv_heads).  Row j of request b, at
+ * position P = kv_len[b] - n_b + j, sees position s iff s < kv_len[b], and
+ * s <= P if causal, and s > P - window if window > 0:
+ *   out = sum_s softmax_s(scale q . k_s) v_s,   lse = log sum_s exp(scale q . k_s).
+ * A row that sees nothing gets out = 0 and lse = -infinity.
+ *   type      DFLASH_TYPE_BF16 or _F16: q and out; a 16-bit cache has the same
+ *   lse       float32 [rows, n_q_heads] or NULL
+ *   max_rows  no request has more new rows than this
+ *   scale     finite and > 0;  causal 0 or 1;  window >= 0, 0 = none
+ * n_q_heads is a multiple of n_kv_heads.  Cache rows that no row of a request
+ * sees (behind its length, before its window, in pages it does not list) may
+ * hold anything, NaN included.  A visible row that is not finite makes the
+ * outputs of that request and KV head undefined, no other's. */
+size_t dflash_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim,
+                                              int max_rows);
+int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_batch* batch,
+                           int type, int n_q_heads, const dflash_rows* q, const dflash_rows* out,
+                           float* lse, int max_rows, float scale, int causal, int window,
+                           void* workspace, size_t ws_bytes, dflash_stream_t stream);
+
+/* What dflash_logits_adjust applies (host struct of device pointers; NULL =
+ * that rule is off). */
+typedef struct dflash_logit_rules {
+  const int32_t* counts;      /* [slots, V] times each token was produced so far */
+  const int32_t* prompt_mask; /* [slots, ceil(V/32)] bit v % 32 of word v / 32: token v is in the prompt */
+  const int32_t* req_slot;    /* [B] row of counts and prompt_mask, NULL: slot(b) = b */
+  int slots;                  /* rows of counts and prompt_mask */
+  const int32_t* draft;       /* [B, G - 1] the block's drafts; ids outside [0, V) count for nothing */
+  const float* repetition;    /* [B] r > 0 */
+  const float* frequency;     /* [B] f */
+  const float* presence;      /* [B] p */
+  const int32_t* bias_start;  /* [B + 1] request b's biases: entries bias_start[b] .. bias_start[b + 1] - 1 */
+  const int32_t* bias_ids;    /* [n_bias]; an id may come twice, its values add up in order */
+  const float* bias_vals;     /* [n_bias] */
+  int n_bias;
+  const int32_t* allow;       /* [B, G, ceil(V/32)] bit set: token allowed at that position */
+} dflash_logit_rules;
+
+/* Penalties, biases and token masks on the logits of a block, for greedy
+ * verification or dflash_probs.  Position i of request b counts the drafts
+ * before it as produced, as they are if position i is reached:
+ *   c  = counts[slot][v] + #{j < i : draft[b][j] = v}
+ *   l1 = l / r if l > 0 else l * r, where c > 0 or v is in the prompt; else l
+ *   l2 = l1 - (f * c + (c > 0 ? p : 0))
+ *   l3 = l2 + the request's biases of v
+ *   out[b, i, v] = l3 if allowed, else -infinity
+ * in float32.  A position whose mask allows nothing is all -infinity (greedy
+ * verification then takes id 0; dflash_probs has no distribution to return).
+ *   type     DFLASH_TYPE_F32, _BF16 or _F16: logits [B, G, V] with strides
+ *            l_b and l_i between requests and positions, V contiguous
+ *   out      float32 [B, G, V], strides o_b and o_i; out may be logits itself
+ *            (float32, equal strides) and may not overlap it otherwise
+ * Device status: DFLASH_ERR_ARG if a slot is outside [0, slots) (its counts and
+ * prompt are taken as empty), a bias range is outside [0, n_bias] or decreases
+ * (ignored) or a bias id is outside [0, V) (ignored). */
+size_t dflash_logits_adjust_workspace_bytes(void);
+int dflash_logits_adjust(int B, int G, int vocab, int type, const void* logits, long long l_b,
+                         long long l_i, float* out, long long o_b, long long o_i,
+                         const dflash_logit_rules* rules, void* workspace, size_t ws_bytes,
                          dflash_stream_t stream);
 
 /* Copy the workspace status word to the host (synchronises the stream). */

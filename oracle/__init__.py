@@ -30,6 +30,11 @@ What it computes, and where each step comes from:
                 "Conditioning on the target model"; model card
                 "Beam-1.0-501B-A23B-DFlash2", section "Model").
 
+* ``target``    the verifying model's side: rows of a paged cache (16-bit or
+                E4M3), attention of new rows over it, penalties, biases and
+                token masks on logits (the library's own rules; the pages
+                leave the target's kernels to the serving stack).
+
 Floating point is accumulated in float64 throughout.  Integer decisions
 (argmax, accept, inverse-CDF index) are taken exactly as the function
 docstrings state so that a second implementation can match them bit for bit.
@@ -39,4 +44,4 @@ parity with these readings): RoPE placement and base, the pre-norm layer
 layout, the RMSNorm epsilon, the MASK token id, and the Philox counter layout.
 """
 
-from . import philox, fixedpoint, sampling, verify, model, quant  # noqa: F401
+from . import philox, fixedpoint, sampling, verify, model, quant, target  # noqa: F401
