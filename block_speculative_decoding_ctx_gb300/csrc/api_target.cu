@@ -176,7 +176,7 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_b
   a.group = group;
   a.max_rows = max_rows;
   a.causal = causal;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 0;  // longer than any position: none
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = static_cast<int*>(workspace);
   return launch_paged_attention(a, cache->head_dim, cache->format, type, workspace,

@@ -1,103 +1,997 @@
 // Attention of new rows over a paged cache (dflash_paged_attention; the rules
-// are in include/dflash.h): one warp per (row, query head), the keys one after
-// another with a running maximum and sum.
+// are in include/dflash.h), on the 5th-generation tensor cores.
+//
+//   z_s = scale q . k_s over the visible s;  out = sum 2^(z' - m) v_s / l,
+//   m a running reference of z' = z log2(e), l = sum 2^(z' - m), one pass.
+//
+// Work.  The rows of one request that read one KV head, n_b x group of them
+// (packed row = new row x group + query head of the group), are cut into items
+// of at most 256; an item runs over the key tiles (128 positions) that any of
+// its rows sees.  All key tiles of all items, in order, are one line that is
+// cut into equal parts, one for each CTA (one CTA per SM): unequal lengths,
+// causal triangles and single long requests all balance.  A CTA that holds a
+// whole item writes its result; an item cut between CTAs leaves partial (O, m,
+// l) in the workspace, which a second kernel joins in CTA order.  The cut
+// depends on the lengths alone, so results are the same on every run.
+//
+// Inside a CTA two streams of jobs (Q tile of 128 rows x key tile) run side by
+// side, each with its own S and O in tensor memory and its own softmax
+// warpgroup, so that one's softmax runs under the other's products:
+//   an item of more than 128 rows: its two Q tiles, both over every key tile
+//     (each K/V byte feeds 256 rows);
+//   a smaller one: even and odd key tiles of its one Q tile, joined at the end.
+// Roles (384 threads, 168 registers each):
+//   warp 0      page table and TMA: K and V tiles into a ring of slots
+//   warp 1      lane 0 issues S = Q K^T (both from shared memory) and
+//               O += P V (P from tensor memory, V MN-major as TMA left it)
+//   warps 2-3   zero the V rows that no row of the item sees (a weight of 0
+//               times whatever lies there must not become NaN); E4M3: widen
+//               each tile to fp16 (exact) between the TMA ring and the slots
+//   warps 4-7   softmax of stream 0, one query row per thread; warps 8-11
+//               stream 1.  P overwrites S in place.  O is rescaled only when a
+//               row's reference grows by more than a headroom, a few times a
+//               row.
+// Tensor memory: S0 | S1 | O0 | O1, 128 columns each, all 512 of it; the
+// shared memory of a CTA keeps any other off its SM.
+//
+// E4M3 caches: the codes are fp16 values exactly, so both products run in
+// fp16; bf16 queries become fp16 by a power of two per row (exact but for
+// parts 2^-28 below the row's largest).  The key scale multiplies the score
+// and the value scale the weight, both in float32; the weight is taken
+// relative to the largest value scale so far and times 2^8, which keeps it a
+// normal fp16 down to 2^-22 of the largest.
+//
+// All waits are bounded (mbar_wait_bounded).  When one gives up, the softmax
+// and widening warps run on without waiting (their barriers stay matched,
+// results are void, the status word says so) and the CTA ends as usual.
+#include <atomic>
+#include <cstddef>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "attention_util.cuh"
 #include "paged_util.cuh"
 
 namespace dfl {
 namespace {
 
-template <int HD, bool E4M3, bool BF16>
-__global__ void __launch_bounds__(256) paged_attention_kernel(const PagedAttnArgs a) {
-  pdl_enter();
-  const PagedBatch& p = a.batch;
-  const int lane = threadIdx.x & 31, head = blockIdx.y, b = blockIdx.z;
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
-  RequestSpan r;
-  if (!request_span(p, b, &r) || r.n > a.max_rows) {
-    if (threadIdx.x == 0) report_status(a.status, DFLASH_ERR_SHAPE);
-    return;
-  }
-  if (j >= r.n) return;
-  constexpr int kE = HD / 32;  // values per lane
-  const size_t row = r.s0 + j;
-  const int kv = head / a.group;
-  float q[kE], o[kE], m = -INFINITY, l = 0.0f;
-  auto load = [&](const uint8_t* x, float (&f)[kE]) {  // kE 16-bit values
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
-#pragma unroll
-    for (int i = 0; i < kE / 2; ++i) {
-      const float2 t = unpack16<BF16>(__ldg(w + i));
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
+using namespace attn;
+
+constexpr int kKT = 128;           // keys per tile
+constexpr int kMT = 128;           // rows of a Q tile
+constexpr int kThreads = 384;
+constexpr int kMaxCtas = 160;      // the workspace has room for so many
+constexpr int kMaxSlots = 12, kMaxRaw = 8;
+constexpr int kCtrlBytes = 3072;
+constexpr int kSmem = 227 * 1024;  // all that a CTA may have
+constexpr uint32_t kColO = 256;    // O of stream 0; S of stream s at 128 s
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kVShift = 256.0f;  // E4M3: factor on the weights
+
+struct Ctrl {
+  uint64_t full[kMaxSlots], empty[kMaxSlots], raw_full[kMaxRaw], raw_empty[kMaxRaw];
+  uint64_t s_full[2], p_full[2], q_full[2], o_full, fix, fixed, fin;
+  unsigned long long scan[34];
+  long long start_off;
+  int start_pair, abort_flag;
+  uint32_t tmem;
+  float vmax[2][4];
+  float vfac[2];
+  alignas(16) float x[2][256];  // per warpgroup: key and value scales; (m, l) of the join; row scales of Q
+};
+static_assert(sizeof(Ctrl) <= kCtrlBytes && offsetof(Ctrl, x) % 16 == 0, "control block");
+
+// Where an item that this CTA starts but does not finish continues.
+struct Rec {
+  int pair, head, slot, last_cta;  // pair < 0: none
+};
+
+struct KernelArgs {
+  PagedAttnArgs a;
+  float* part;    // [CTA][2][part_rows][HD]
+  float2* ml;     // [CTA][2][part_rows]
+  Rec* rec;       // [CTA]
+  int rts;        // items per request at most
+  int part_rows;  // 128 or 256
+  int slots, raw; // slots of the 16-bit ring and of the E4M3 ring
+  int q_tiles;    // Q tiles in shared memory
+};
+
+// ------------------------------------------------------------------- items
+
+struct Item {
+  int b, s0, n, len;     // request
+  int row0, rows;        // packed rows
+  int lo, hi;            // positions that some row sees
+  int t_lo, tiles;       // key tiles
+  int units;             // length on the line: a CTA's turn for an empty item, too
+};
+
+__device__ __forceinline__ bool item_rows(const PagedAttnArgs& a, int b, RequestSpan* r) {
+  return request_span(a.batch, b, r) && r->n <= a.max_rows;
+}
+
+__device__ __forceinline__ Item make_item(const PagedAttnArgs& a, const RequestSpan& r, int b, int rt) {
+  Item it;
+  it.b = b;
+  it.s0 = r.s0;
+  it.n = r.n;
+  it.len = r.len;
+  it.row0 = rt * (2 * kMT);
+  it.rows = min(2 * kMT, r.n * a.group - it.row0);
+  const int p0 = r.len - r.n + it.row0 / a.group;
+  const int p1 = r.len - r.n + (it.row0 + it.rows - 1) / a.group;
+  it.hi = a.causal ? min(r.len, p1 + 1) : r.len;
+  it.lo = a.window ? max(0, p0 - a.window + 1) : 0;
+  it.t_lo = it.lo / kKT;
+  it.tiles = it.hi > it.lo ? (it.hi + kKT - 1) / kKT - it.t_lo : 0;
+  it.units = max(it.tiles, 1);
+  return it;
+}
+
+// First item at or after pair (request x rts + item) on the line; pair moves
+// to it.  False past the last request.
+__device__ __forceinline__ bool find_item(const KernelArgs& k, int* pair, int end, Item* it) {
+  while (*pair < end) {
+    const int b = *pair / k.rts, rt = *pair - b * k.rts;
+    RequestSpan r;
+    if (item_rows(k.a, b, &r) && rt * (2 * kMT) < r.n * k.a.group) {
+      *it = make_item(k.a, r, b, rt);
+      return true;
     }
-  };
-  load(a.q + (row * a.q_row + (size_t)head * a.q_head + lane * kE) * 2, q);
-#pragma unroll
-  for (int i = 0; i < kE; ++i) o[i] = 0.0f;
-  const int pos = r.len - r.n + j;
-  const int hi = a.causal ? min(r.len, pos + 1) : r.len;
-  const int lo = a.window ? max(0, pos - a.window + 1) : 0;
-  for (int s = lo; s < hi; ++s) {
-    const int page = __ldg(p.table + b * p.table_stride + (s >> p.page_shift));
-    const bool there = page >= 0 && page < p.n_pages;
-    if (!there) report_status(a.status, DFLASH_ERR_ARG);
-    const size_t at = ((size_t)kv << p.page_shift) + (s & ((1 << p.page_shift) - 1));
-    float k[kE] = {}, v[kE] = {};
-    if (there) {
-      const size_t ko = (size_t)page * a.k_page_stride + at * HD + lane * kE;
-      const size_t vo = (size_t)page * a.v_page_stride + at * HD + lane * kE;
-      if (E4M3) {
-        const size_t so = (((size_t)page * a.n_kv) << p.page_shift) + at;
-        const float ks = __ldg(a.k_scale + so), vs = __ldg(a.v_scale + so);
-#pragma unroll
-        for (int i = 0; i < kE; i += 2) {
-          const float2 kf = unpack16<false>(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(a.k_pages + ko + i)));
-          const float2 vf = unpack16<false>(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(a.v_pages + vo + i)));
-          k[i] = kf.x * ks;
-          k[i + 1] = kf.y * ks;
-          v[i] = vf.x * vs;
-          v[i + 1] = vf.y * vs;
-        }
-      } else {
-        load(a.k_pages + ko * 2, k);
-        load(a.v_pages + vo * 2, v);
-      }
-    }
-    float z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) z = fmaf(q[i], k[i], z);
-    z = warp_sum(z) * a.scale_log2;
-    const float mn = fmaxf(m, z);
-    const float f = m == -INFINITY ? 0.0f : exp2f(m - mn), w = exp2f(z - mn);
-    m = mn;
-    l = l * f + w;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) o[i] = fmaf(o[i], f, w * v[i]);
+    *pair = (b + 1) * k.rts;
   }
-  const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (row * a.o_row + (size_t)head * a.o_head + lane * kE) * 2);
+  return false;
+}
+
+// The CTA's part of the line as segments of items.
+struct Seg {
+  Item it;
+  int head;        // KV head
+  int t0, nt;      // key tiles
+  bool split;      // one Q tile, streams take every other key tile
+  bool first, last;
+  int slot;        // partial slot
+  int pair;
+  long long before;  // units of this CTA before it
+};
+
+struct Walk {
+  const KernelArgs& k;
+  long long left, total;
+  int pair, head, off, end;
+  Item it;
+  bool loaded;
+  __device__ Walk(const KernelArgs& kk, const Ctrl* c, long long n)
+      : k(kk), left(n), total(n), pair(c->start_pair), end(kk.a.batch.B * kk.rts), loaded(false) {
+    Item i;
+    (void)find_item(k, &pair, end, &i);
+    it = i;
+    loaded = true;
+    head = (int)(c->start_off / it.units);
+    off = (int)(c->start_off - (long long)head * it.units);
+  }
+  __device__ bool next(Seg* s) {
+    if (left <= 0) return false;
+    if (!loaded) {
+      if (!find_item(k, &pair, end, &it)) return false;
+      loaded = true;
+    }
+    const int take = (int)min(left, (long long)(it.units - off));
+    s->it = it;
+    s->head = head;
+    s->t0 = it.t_lo + off;
+    s->nt = max(0, min(take, it.tiles - off));
+    s->split = it.rows <= kMT;
+    s->first = off == 0;
+    s->last = off + take == it.units;
+    s->slot = left == total ? 0 : 1;
+    s->pair = pair;
+    s->before = total - left;
+    left -= take;
+    off = 0;
+    if (++head == k.a.n_kv) {
+      head = 0;
+      ++pair;
+      loaded = false;
+    }
+    return true;
+  }
+};
+
+// -------------------------------------------------------------- PTX helpers
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
-  for (int i = 0; i < kE / 2; ++i) out[i] = pack16<BF16>(o[2 * i] * inv, o[2 * i + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row * a.n_q + head] = (m + log2f(l)) * 0.693147180559945309f;
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Matrix descriptor of V as TMA writes it with the 128-byte swizzle: rows
+// along K of 128 bytes (64 values along N), 8-row atoms 1024 bytes apart,
+// further blocks of 64 values along N kKT x 128 bytes apart.
+__device__ __forceinline__ uint64_t v_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((kKT * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
 }
 
 template <int HD, bool E4M3, bool BF16>
-int launch(const PagedAttnArgs& a, cudaStream_t s) {
-  return launch_pdl(paged_attention_kernel<HD, E4M3, BF16>, dim3(ceil_div(a.max_rows, 8), a.n_q, a.batch.B), dim3(256), 0, s, a);
+struct Cfg {
+  static constexpr int kTile = kKT * HD * 2;              // 16-bit tile of K, V or Q
+  static constexpr int kRaw = kKT * HD;                   // E4M3 tile
+  static constexpr bool kMmaBF = BF16 && !E4M3;
+  static constexpr float kHeadroom = E4M3 ? 4.0f : 8.0f;  // growth of a reference (log2) before O is rescaled
+};
+
+// ------------------------------------------------------------------ Q tile
+
+// Rows [row0, row0 + 128) of the item's packed rows into a swizzled tile, by
+// the 128 threads of a warpgroup; rows past the item's are zero.  E4M3 with
+// bf16: fp16 by a power of two per row, its inverse in row_scale.
+template <int HD, bool E4M3, bool BF16>
+__device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, int head, int row0, uint8_t* q_s,
+                                       float* row_scale, int t, int r_begin, int r_end) {
+  constexpr int kCh = HD / 8;  // 16-byte chunks of a row
+  for (int idx = r_begin * kCh + t; idx < r_end * kCh; idx += 128) {
+    const int r = idx / kCh, ch = idx % kCh, pr = row0 + r;
+    const bool ok = pr < it.rows;
+    const int packed = it.row0 + (ok ? pr : 0);
+    const int tok = packed / a.group, g = packed - tok * a.group;
+    const uint8_t* src = a.q + ((size_t)(it.s0 + tok) * a.q_row + (size_t)(head * a.group + g) * a.q_head + ch * 8) * 2;
+    uint8_t* dst = q_s + (ch >> 3) * (kMT * 128) + swz(r, (ch & 7) * 8);
+    if (!(E4M3 && BF16)) {
+      cp_async16(dst, src, ok);
+    } else {
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (ok) w = __ldg(reinterpret_cast<const uint4*>(src));
+      uint32_t v[4] = {w.x, w.y, w.z, w.w}, m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+#pragma unroll
+      for (int o = kCh / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = max(m & 0xFFFFu, m >> 16);
+      int e = max((int)(m >> 7), 15);   // largest exponent field of the row
+      const bool fin = e < 255;
+      const float f = fin ? __uint_as_float((uint32_t)(268 - e) << 23) : 1.0f;   // largest into [2^14, 2^15)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = unpack16<true>(v[i]);
+        v[i] = pack_f16(y.x * f, y.y * f);
+      }
+      *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+      if (ch == 0) row_scale[r] = fin ? __uint_as_float((uint32_t)(e - 14) << 23) : 1.0f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <int HD, bool E4M3, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                           const KernelArgs k) {
+  using C = Cfg<HD, E4M3, BF16>;
+  pdl_enter();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const PagedAttnArgs& a = k.a;
+  uint8_t* ring_s = smem;
+  uint8_t* q_s = ring_s + k.slots * C::kTile;
+  uint8_t* raw_s = q_s + k.q_tiles * C::kTile;
+  Ctrl* c = reinterpret_cast<Ctrl*>(smem + kSmem - kCtrlBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023) {  // the swizzled tiles want 1024-byte atoms
+    if (tid == 0) {
+      report_status(a.status, DFLASH_ERR_UNSUPPORTED);
+      k.rec[blockIdx.x].pair = -1;
+    }
+    return;
+  }
+
+  // ---- the line's length and this CTA's part of it
+  const int pairs = a.batch.B * k.rts;
+  const int per = (pairs + kThreads - 1) / kThreads;
+  const int p0 = min(pairs, tid * per), p1 = min(pairs, p0 + per);
+  unsigned long long mine = 0;
+  for (int p = p0; p < p1;) {
+    const int b = p / k.rts;
+    int rt = p - b * k.rts;
+    RequestSpan r;
+    if (!item_rows(a, b, &r)) {
+      if (blockIdx.x == 0) report_status(a.status, DFLASH_ERR_SHAPE);
+      p = (b + 1) * k.rts;
+      continue;
+    }
+    const int items = (r.n * a.group + 2 * kMT - 1) / (2 * kMT);
+    for (; rt < items && p < p1; ++rt, ++p) mine += make_item(a, r, b, rt).units;
+    if (rt >= items) p = (b + 1) * k.rts;
+  }
+  unsigned long long total;
+  const unsigned long long excl = block_exclusive_scan(mine, c->scan, &total);
+  const long long W = (long long)total * a.n_kv;
+  const int ctas = (int)min((long long)gridDim.x, W);
+  const int cta = blockIdx.x;
+  if (cta >= ctas) {
+    if (tid == 0) k.rec[cta].pair = -1;
+    return;
+  }
+  const long long w0 = W * cta / ctas, w1 = W * (cta + 1) / ctas;
+  if ((long long)excl * a.n_kv <= w0 && w0 < (long long)(excl + mine) * a.n_kv) {
+    long long at = (long long)excl * a.n_kv;
+    int p = p0;
+    Item it;
+    while (find_item(k, &p, pairs, &it)) {
+      const long long n = (long long)it.units * a.n_kv;
+      if (w0 < at + n) break;
+      at += n;
+      ++p;
+    }
+    c->start_pair = p;
+    c->start_off = w0 - at;
+  }
+
+  if (tid == 0) {
+    for (int s = 0; s < k.slots; ++s) {
+      mbar_init(&c->full[s], E4M3 ? 2 : 1);
+      mbar_init(&c->empty[s], 1);
+    }
+    for (int s = 0; s < k.raw; ++s) {
+      mbar_init(&c->raw_full[s], 1);
+      mbar_init(&c->raw_empty[s], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->s_full[i], 1);
+      mbar_init(&c->p_full[i], 4);
+      mbar_init(&c->q_full[i], 1);
+    }
+    mbar_init(&c->o_full, 1);
+    mbar_init(&c->fix, 1);
+    mbar_init(&c->fixed, 2);
+    mbar_init(&c->fin, 1);
+    c->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&c->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem;
+  volatile int* stop = &c->abort_flag;
+  Walk walk(k, c, w1 - w0);
+  Seg s;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
+    uint8_t* dst0 = E4M3 ? raw_s : ring_s;
+    uint64_t* full = E4M3 ? c->raw_full : c->full;
+    uint64_t* empty = E4M3 ? c->raw_empty : c->empty;
+    const int ring = E4M3 ? k.raw : k.slots;
+    constexpr int kBytes = E4M3 ? C::kRaw : C::kTile;
+    int slot = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok && walk.next(&s)) {
+      const int32_t* table = a.batch.table + s.it.b * a.batch.table_stride;
+      int ids = 0, ids_at = -1;  // page ids of 32 pages from ids_at on, one per lane
+      for (int t = s.t0; ok && t < s.t0 + s.nt; ++t) {
+        const int first = t * per_tile;
+        // pages of the tile that hold a visible position
+        const int g0 = max(first, s.it.lo >> shift), g1 = min(first + per_tile, ((s.it.hi - 1) >> shift) + 1);
+        if (ids_at < 0 || first + per_tile > ids_at + 32) {
+          ids_at = first;
+          const int g = first + lane;
+          int id = -1;
+          if (g >= (s.it.lo >> shift) && g <= (s.it.hi - 1) >> shift) {
+            id = __ldg(table + g);
+            if (id < 0 || id >= a.batch.n_pages) {
+              report_status(a.status, DFLASH_ERR_ARG);
+              id = a.batch.n_pages;  // outside the tensor: TMA fills zeros
+            }
+          }
+          ids = id;
+        }
+        for (int side = 0; side < 2; ++side) {
+          bool got = true;
+          if (lane == 0) got = mbar_wait_bounded(&empty[slot], phase ^ 1u, stop, a.status);
+          ok = __shfl_sync(0xffffffffu, got, 0);
+          if (!ok) break;
+          uint8_t* dst = dst0 + slot * kBytes;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)((g1 - g0) << shift) * (E4M3 ? HD : HD * 2));
+          for (int g = g0; g < g1; ++g) {
+            const int id = __shfl_sync(0xffffffffu, ids, g - ids_at);
+            if (lane == 0) {
+              const int row = (g - first) << shift;
+              const void* map = side ? &tmV : &tmK;
+              if (E4M3) {
+                tma_load_3d(dst + row * HD, map, &full[slot], 0, s.head * page_rows, id);
+              } else {
+#pragma unroll
+                for (int h = 0; h < HD / 64; ++h)
+                  tma_load_3d(dst + h * (kKT * 128) + row * 128, map, &full[slot], h * 64, s.head * page_rows, id);
+              }
+            }
+          }
+          ++issued;
+          if (++slot == ring) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      // a wait gave up: let the copies in flight land before the CTA leaves
+      int dummy = 0;
+      for (int j = issued > ring ? issued - ring : 0; j < issued; ++j)
+        (void)mbar_wait_bounded(&full[j % ring], (uint32_t)(j / ring) & 1u, &dummy, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_f32acc(kMT, kKT, C::kMmaBF);
+      constexpr uint32_t id_pv = idesc_f32acc(kMT, HD, C::kMmaBF) | (1u << 16);  // V is MN-major
+      const uint32_t ring_a = smem_u32(ring_s), q_a = smem_u32(q_s);
+      uint32_t base = 0, seg = 0, fixes = 0;  // ring index of the segment's first K tile
+      uint32_t jobs_p[2] = {0, 0};
+      bool ok = true;
+      while (ok && walk.next(&s)) {
+        const int jobs = s.split ? s.nt : 2 * s.nt;
+        ok = mbar_wait_bounded(&c->q_full[0], seg & 1u, stop, a.status) &&
+             mbar_wait_bounded(&c->q_full[1], seg & 1u, stop, a.status);
+        ++seg;
+        tc_fence_after();
+        auto qk = [&](int j) -> bool {
+          const int st = j & 1, t = s.split ? j : j >> 1;
+          const uint32_t r = base + 2 * t, slot = r % k.slots;
+          if (s.split || st == 0) {
+            if (!mbar_wait_bounded(&c->full[slot], (r / k.slots) & 1u, stop, a.status)) return false;
+            tc_fence_after();
+          }
+          const uint32_t ka = ring_a + slot * C::kTile, qa = q_a + (s.split ? 0 : st) * C::kTile;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kKT * 128) + (kk & 3) * 32;
+            tc_mma_f16(tmem + st * kKT, smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id_qk, kk > 0);
+          }
+          tc_commit(&c->s_full[st]);
+          if (s.split || st == 1) tc_commit(&c->empty[slot]);
+          return true;
+        };
+        auto pv = [&](int j) -> bool {
+          const int st = j & 1, t = s.split ? j : j >> 1;
+          const uint32_t r = base + 2 * t + 1, slot = r % k.slots;
+          bool edge = false;  // V rows of the tile are out of sight: have them zeroed
+          if (s.split || st == 0) {
+            if (!mbar_wait_bounded(&c->full[slot], (r / k.slots) & 1u, stop, a.status)) return false;
+            const int k0 = (s.t0 + t) * kKT;
+            edge = !E4M3 && (k0 < s.it.lo || k0 + kKT > s.it.hi);
+            if (edge) mbar_arrive(&c->fix);
+          }
+          if (!mbar_wait_bounded(&c->p_full[st], jobs_p[st]++ & 1u, stop, a.status)) return false;
+          if (edge && !mbar_wait_bounded(&c->fixed, fixes++ & 1u, stop, a.status)) return false;
+          tc_fence_after();
+          const uint32_t va = ring_a + slot * C::kTile;
+          const bool fresh = s.split ? j < 2 : t == 0;
+#pragma unroll
+          for (int kk = 0; kk < kKT / 16; ++kk)
+            tc_mma_f16_ta(tmem + kColO + st * 128, tmem + st * kKT + kk * 8, v_desc(va + kk * 2048), id_pv,
+                          !fresh || kk > 0);
+          if (s.split || st == 1) tc_commit(&c->empty[slot]);
+          return true;
+        };
+        if (ok && jobs > 0) ok = qk(0);
+        if (ok && jobs > 1) ok = qk(1);
+        for (int j = 0; ok && j < jobs; ++j) {
+          ok = pv(j);
+          // P of a job overwrites its S: the next scores of the stream follow
+          // its P V in the tensor pipe's order
+          if (ok && j + 2 < jobs) ok = qk(j + 2);
+        }
+        tc_commit(&c->o_full);
+        base += 2 * s.nt;
+      }
+      tc_commit(&c->fin);  // every MMA this thread issued
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------- V rows out of sight; E4M3: widening
+    const int ct = tid - 64;  // 0..63
+    uint32_t r = 0, fixes = 0;
+    while (walk.next(&s)) {
+      for (int t = s.t0; t < s.t0 + s.nt; ++t) {
+        const int k0 = t * kKT;
+        const int v0 = max(0, s.it.lo - k0), v1 = min(kKT, s.it.hi - k0);  // rows in sight
+        if (!E4M3) {
+          if (v0 > 0 || v1 < kKT) {
+            const uint32_t rv = r + 1, slot = rv % k.slots;
+            (void)warp_wait(&c->fix, fixes++ & 1u, stop, a.status);  // the tile is there
+            uint8_t* v = ring_s + slot * C::kTile;
+            for (int idx = ct; idx < kKT * (HD / 8); idx += 64) {
+              const int row = idx / (HD / 8), ch = idx % (HD / 8);
+              if (row < v0 || row >= v1)
+                *reinterpret_cast<uint4*>(v + (ch >> 3) * (kKT * 128) + row * 128 + (ch & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->fixed);
+          }
+        } else {
+          for (int side = 0; side < 2; ++side) {
+            const uint32_t rs = r + side, raw = rs % k.raw, slot = rs % k.slots;
+            (void)warp_wait(&c->raw_full[raw], (rs / k.raw) & 1u, stop, a.status);
+            (void)warp_wait(&c->empty[slot], ((rs / k.slots) & 1u) ^ 1u, stop, a.status);
+            const uint4* src = reinterpret_cast<const uint4*>(raw_s + raw * C::kRaw);
+            uint8_t* dst = ring_s + slot * C::kTile;
+            constexpr int kCh = HD / 16;  // 16-code chunks of a row
+#pragma unroll 4
+            for (int i = 0; i < kKT * kCh / 64; ++i) {
+              const int idx = ct + i * 64, row = idx / kCh, ch = idx % kCh;
+              uint4 w = src[idx];
+              if (side && (row < v0 || row >= v1)) w = make_uint4(0u, 0u, 0u, 0u);
+              const uint4 lo = make_uint4(e4m3x2_to_f16x2((uint16_t)w.x), e4m3x2_to_f16x2((uint16_t)(w.x >> 16)),
+                                          e4m3x2_to_f16x2((uint16_t)w.y), e4m3x2_to_f16x2((uint16_t)(w.y >> 16)));
+              const uint4 hi = make_uint4(e4m3x2_to_f16x2((uint16_t)w.z), e4m3x2_to_f16x2((uint16_t)(w.z >> 16)),
+                                          e4m3x2_to_f16x2((uint16_t)w.w), e4m3x2_to_f16x2((uint16_t)(w.w >> 16)));
+              uint8_t* base = dst + (ch >> 2) * (kKT * 128) + row * 128;
+              const int c0 = (ch & 3) * 2;
+              // the upper half's chunks go in the other order: the eight
+              // threads of a row then hit eight different 16-byte banks
+              const bool swap = (ch >> 2) & 1;
+              *reinterpret_cast<uint4*>(base + (((c0 + swap) ^ row) & 7) * 16) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(base + (((c0 + !swap) ^ row) & 7) * 16) = swap ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&c->raw_empty[raw]);
+              mbar_arrive(&c->full[slot]);
+            }
+          }
+        }
+        r += 2;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int wg = (warp >> 2) - 1, t = tid & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + wg * kKT, tO = tmem + lane_off + kColO;
+    float* x = c->x[wg];
+    uint32_t jobs = 0, seg = 0;
+    Rec rec = {-1, 0, 0, 0};
+    while (walk.next(&s)) {
+      const Item& it = s.it;
+      // ---- queries of this stream (a split item's one tile: half by each
+      // warpgroup, or all by both where the row scales are needed by both)
+      if (s.split) {
+        constexpr bool kAll = E4M3 && BF16;
+        load_q<HD, E4M3, BF16>(a, it, s.head, 0, q_s, x, t, kAll ? 0 : 64 * wg, kAll ? kMT : 64 * wg + 64);
+      } else {
+        load_q<HD, E4M3, BF16>(a, it, s.head, kMT * wg, q_s + wg * C::kTile, x, t, 0, kMT);
+      }
+      if (!(E4M3 && BF16)) cp_async_wait_all();
+      fence_proxy_async_smem();
+      named_sync(1 + wg, 128);
+      if (t == 0) mbar_arrive(&c->q_full[wg]);
+      const int pr = (s.split ? 0 : kMT * wg) + t;   // row of the item
+      const bool real = pr < it.rows;
+      const bool live = __any_sync(0xffffffffu, real);
+      const int packed = it.row0 + (real ? pr : 0);
+      const int tok = packed / a.group, g = packed - tok * a.group;
+      const int pos = it.len - it.n + tok;
+      // rows past the item's see everything: their scores are zero
+      const int hi = !real ? 1 << 30 : a.causal ? min(it.len, pos + 1) : it.len;
+      const int lo = real && a.window ? pos - a.window + 1 : -(1 << 30);
+      const float cs = a.scale_log2 * (E4M3 && BF16 ? x[t] : 1.0f);
+
+      float m_ref = -INFINITY, l = 0.0f, vref = 0.0f;
+      const int step = s.split ? 2 : 1, j0 = s.split ? wg : 0;
+      float nks = 0.0f, nvs = 0.0f;  // scales of key t of the next tile
+      auto fetch = [&](int tile) {
+        const int key = tile * kKT + t;
+        nks = nvs = 0.0f;
+        if (key >= it.lo && key < it.hi) {
+          const int id = __ldg(a.batch.table + it.b * a.batch.table_stride + (key >> a.batch.page_shift));
+          if (id >= 0 && id < a.batch.n_pages) {
+            const size_t o = (((size_t)id * a.n_kv + s.head) << a.batch.page_shift) + (key & ((1 << a.batch.page_shift) - 1));
+            nks = __ldg(a.k_scale + o);
+            nvs = __ldg(a.v_scale + o);
+          }
+        }
+      };
+      if (E4M3 && j0 < s.nt) fetch(s.t0 + j0);
+      for (int j = j0; j < s.nt; j += step) {
+        float fv = 1.0f;  // E4M3: change of the value reference
+        float cv = 0.0f;
+        if (E4M3) {
+          named_sync(1 + wg, 128);  // the last job's scales have been read
+          x[t] = nks;
+          x[128 + t] = nvs;
+          const float wm = warp_max_f(nvs);
+          if (lane == 0) c->vmax[wg][warp & 3] = wm;
+          named_sync(1 + wg, 128);
+          const float vm = fmaxf(fmaxf(c->vmax[wg][0], c->vmax[wg][1]), fmaxf(c->vmax[wg][2], c->vmax[wg][3]));
+          if (vm > 8.0f * vref || vref == 0.0f) {
+            const float nv = fmaxf(vm, 1e-30f);
+            fv = vref / nv;
+            vref = nv;
+          }
+          cv = kVShift / vref;
+          if (j + step < s.nt) fetch(s.t0 + j + step);
+        }
+        (void)warp_wait(&c->s_full[wg], jobs++ & 1u, stop, a.status);
+        tc_fence_after();
+        if (!live) {
+          // no query row in this warp's lanes: whatever their P holds only
+          // reaches lanes of O that nobody reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->p_full[wg]);
+          continue;
+        }
+        float sv[kKT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_x32(tS + i * 32, sv + i * 32);
+        tc_wait_ld();
+        if (E4M3) {
+#pragma unroll
+          for (int e = 0; e < kKT; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(x + e);
+            sv[e] *= f.x;
+            sv[e + 1] *= f.y;
+            sv[e + 2] *= f.z;
+            sv[e + 3] *= f.w;
+          }
+        }
+        const int k0 = (s.t0 + j) * kKT;
+        if (!__all_sync(0xffffffffu, k0 >= lo && k0 + kKT <= hi)) {
+          const int e0 = lo - k0, e1 = hi - k0;  // visible: e0 <= e < e1
+#pragma unroll
+          for (int e = 0; e < kKT; ++e)
+            if (e < e0 || e >= e1) sv[e] = -INFINITY;
+        }
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          mx[i] = sv[i];
+#pragma unroll
+          for (int e = i + 8; e < kKT; e += 8) mx[i] = fmaxf(mx[i], sv[e]);
+        }
+        const float m_tile =
+            fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * cs;
+        const bool grow = m_tile > m_ref + C::kHeadroom || (m_ref == -INFINITY && m_tile > -INFINITY);
+        if (__any_sync(0xffffffffu, grow || fv != 1.0f)) {
+          const float m_new = grow ? m_tile : m_ref;
+          const float f = grow ? ex2_approx(m_ref - m_new) : 1.0f;  // 0 while nothing was seen
+          if (j > j0) {
+            // O holds the stream's earlier jobs: their P V precede these
+            // scores in the tensor pipe, the next one waits for this P
+            const float fo = f * fv;
+            uint32_t r[16];
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+              const uint32_t oa = tO + wg * 128 + i * 16;
+              tmem_ld_x16(oa, r);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fo);
+              tmem_st_x16(oa, r);
+            }
+          }
+          l *= f;
+          m_ref = m_new;
+        }
+        const float nb = m_ref == -INFINITY ? 0.0f : -m_ref;
+        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              p[i] = ex2_approx(fmaf(sv[q * 32 + e + i], cs, nb));
+              ls[i] += p[i];
+            }
+            if (E4M3) {
+              const float4 f = *reinterpret_cast<const float4*>(x + 128 + q * 32 + e);
+              p[0] *= f.x * cv;
+              p[1] *= f.y * cv;
+              p[2] *= f.z * cv;
+              p[3] *= f.w * cv;
+            }
+            pw[e / 2] = pack16<C::kMmaBF>(p[0], p[1]);
+            pw[e / 2 + 1] = pack16<C::kMmaBF>(p[2], p[3]);
+          }
+          tmem_st_x16(tS + q * 16, pw);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->p_full[wg]);
+      }
+
+      // ---- end of the segment: O is final
+      (void)warp_wait(&c->o_full, seg++ & 1u, stop, a.status);
+      tc_fence_after();
+      const bool whole = s.first && s.last;
+      if (s.first && !s.last) {
+        const long long u = w0 + s.before + it.units - 1;  // the item's last unit
+        rec = {s.pair, s.head, s.slot, (int)(((u + 1) * ctas - 1) / W)};
+      }
+      float f0, f1 = 0.0f, M = m_ref, L = l;  // factors of O0 and O1 (a row-split item: of its own O)
+      f0 = E4M3 ? vref * (1.0f / kVShift) : 1.0f;
+      if (s.split) {
+        named_sync(1 + wg, 128);  // scales are no longer read
+        x[t] = m_ref;
+        x[128 + t] = l;
+        if (t == 0) c->vfac[wg] = f0;
+        named_sync(3, 256);
+        const float m0 = c->x[0][t], m1 = c->x[1][t];
+        M = fmaxf(m0, m1);
+        const float e0 = m0 == -INFINITY ? 0.0f : ex2_approx(m0 - M), e1 = m1 == -INFINITY ? 0.0f : ex2_approx(m1 - M);
+        L = c->x[0][128 + t] * e0 + c->x[1][128 + t] * e1;
+        f0 = e0 * c->vfac[0];
+        f1 = e1 * c->vfac[1];
+        named_sync(3, 256);  // read by all before the next segment's scales
+      }
+      const float inv = whole ? (L > 0.0f || L != L ? 1.0f / L : 0.0f) : 1.0f;
+      f0 *= inv;
+      f1 *= inv;
+      // columns: a split item's are shared out between the warpgroups
+      const int col0 = s.split ? wg * (HD / 2) : 0, cols = s.split ? HD / 2 : HD;
+      const bool have0 = s.nt > 0, have1 = s.split && s.nt > 1;
+      if (live) {
+        const size_t pi = (size_t)(cta * 2 + s.slot) * k.part_rows + pr;
+        uint8_t* out = a.out + ((size_t)(it.s0 + tok) * a.o_row + (size_t)(s.head * a.group + g) * a.o_head) * 2;
+        for (int i = 0; i < cols / 16; ++i) {
+          const int col = col0 + i * 16;
+          float o[16];
+          uint32_t r0[16], r1[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r0[e] = r1[e] = 0u;
+          if (have0) tmem_ld_x16(tO + (s.split ? 0 : wg * 128) + col, r0);
+          if (have1) tmem_ld_x16(tO + 128 + col, r1);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            o[e] = __uint_as_float(r0[e]) * f0;
+            if (have1) o[e] = fmaf(__uint_as_float(r1[e]), f1, o[e]);
+          }
+          if (!real) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(out + col * 2);
+            dst[0] = make_uint4(pack16<BF16>(o[0], o[1]), pack16<BF16>(o[2], o[3]), pack16<BF16>(o[4], o[5]),
+                                pack16<BF16>(o[6], o[7]));
+            dst[1] = make_uint4(pack16<BF16>(o[8], o[9]), pack16<BF16>(o[10], o[11]), pack16<BF16>(o[12], o[13]),
+                                pack16<BF16>(o[14], o[15]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(k.part + pi * HD + col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (real && (!s.split || wg == 0)) {
+          if (!whole)
+            k.ml[pi] = make_float2(M, L);
+          else if (a.lse)
+            a.lse[(size_t)(it.s0 + tok) * a.n_q + s.head * a.group + g] = (M + log2f(L)) * kLn2;
+        }
+      }
+      tc_fence_before();
+    }
+    if (warp == 4 && lane == 0) k.rec[cta] = rec;
+  }
+
+  // tensor memory is no longer read: free it once every MMA has completed
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    int dummy = 0;
+    if (lane == 0) (void)mbar_wait_bounded(&c->fin, 0, &dummy, nullptr, 100000000ull);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial results of the item that CTA blockIdx.x of the kernel
+// above started and did not finish: one warp per row, CTAs in order.
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(256) paged_join_kernel(const KernelArgs k) {
+  pdl_enter();
+  const int cta = blockIdx.x;
+  const Rec rec = k.rec[cta];
+  if (rec.pair < 0) return;
+  const PagedAttnArgs& a = k.a;
+  const int lane = threadIdx.x & 31, w = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int b = rec.pair / k.rts;
+  RequestSpan r;
+  if (!item_rows(a, b, &r)) return;
+  const Item it = make_item(a, r, b, rec.pair - b * k.rts);
+  const int n = rec.last_cta - cta + 1;
+  constexpr int kE = HD / 32;
+  for (int row = w; row < it.rows; row += 8 * gridDim.y) {
+    auto place = [&](int i) { return (size_t)((cta + i) * 2 + (i ? 0 : rec.slot)) * k.part_rows + row; };
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, k.ml[place(i)].x);
+    M = warp_max_f(M);
+    float L = 0.0f, o[kE] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float f = 0.0f;
+      if (i0 + lane < n) {
+        const float2 ml = k.ml[place(i0 + lane)];
+        f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+        L += f * ml.y;
+      }
+      const int m = min(32, n - i0);
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* p = k.part + place(i0 + i) * HD + lane * kE;
+#pragma unroll
+        for (int e = 0; e < kE; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(p + e);
+          o[e] = fmaf(fi, v.x, o[e]);
+          o[e + 1] = fmaf(fi, v.y, o[e + 1]);
+        }
+      }
+    }
+    L = warp_sum(L);
+    const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+    const int packed = it.row0 + row, tok = packed / a.group, g = packed - tok * a.group;
+    uint32_t* out = reinterpret_cast<uint32_t*>(
+        a.out + ((size_t)(it.s0 + tok) * a.o_row + (size_t)(rec.head * a.group + g) * a.o_head + lane * kE) * 2);
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) out[e / 2] = pack16<BF16>(o[e] * inv, o[e + 1] * inv);
+    if (a.lse && lane == 0)
+      a.lse[(size_t)(it.s0 + tok) * a.n_q + rec.head * a.group + g] = (M + log2f(L)) * kLn2;
+  }
+}
+
+// -------------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+// Tensor map of one side of the cache: [pages][heads x page rows][head_dim].
+int encode_pages(CUtensorMap* map, const void* ptr, const PagedAttnArgs& a, int hd, bool e4m3, bool bf16,
+                 long long page_stride) {
+  std::call_once(g_encode_once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return DFLASH_ERR_CUDA;
+  const int cell = e4m3 ? 1 : 2, page = 1 << a.batch.page_shift;
+  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)a.n_kv * page, (cuuint64_t)a.batch.n_pages};
+  cuuint64_t strides[2] = {(cuuint64_t)hd * cell, (cuuint64_t)page_stride * cell};
+  cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? hd : 64), (cuuint32_t)page, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = e4m3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUresult r = g_encode(map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+struct Layout {
+  float* part;
+  float2* ml;
+  Rec* rec;
+  size_t bytes;
+};
+
+int part_rows(int group, int max_rows) { return (long long)group * max_rows > kMT ? 2 * kMT : kMT; }
+
+Layout layout(void* ws, int group, int hd, int max_rows) {
+  Carve cv(ws, kWsHeader);
+  const size_t rows = (size_t)kMaxCtas * 2 * part_rows(group, max_rows);
+  Layout l;
+  l.rec = cv.take<Rec>(kMaxCtas);
+  l.ml = cv.take<float2>(rows);
+  l.part = cv.take<float>(rows * hd);
+  l.bytes = cv.off;
+  return l;
+}
+
+template <int HD, bool E4M3, bool BF16>
+int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
+  using C = Cfg<HD, E4M3, BF16>;
+  CUtensorMap tk, tv;
+  int rc = encode_pages(&tk, a.k_pages, a, HD, E4M3, BF16, a.k_page_stride);
+  if (rc) return rc;
+  if ((rc = encode_pages(&tv, a.v_pages, a, HD, E4M3, BF16, a.v_page_stride))) return rc;
+  auto kern = paged_attention_kernel<HD, E4M3, BF16>;
+  int dev = 0, sms = 0;
+  DFL_CUDA_TRY(cudaGetDevice(&dev));
+  static std::atomic<int> known[64];  // SMs of the devices the attribute is set on
+  if (dev < 64 && (sms = known[dev].load())) {
+  } else {
+    DFL_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    DFL_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    if (dev < 64) known[dev].store(sms);
+  }
+  KernelArgs k;
+  k.a = a;
+  const Layout l = layout(ws, a.group, HD, a.max_rows);
+  k.part = l.part;
+  k.ml = l.ml;
+  k.rec = l.rec;
+  const long long rts = ((long long)a.max_rows * a.group + 2 * kMT - 1) / (2 * kMT);
+  if (rts * a.batch.B > 1 << 30) return DFLASH_ERR_SHAPE;
+  k.rts = (int)rts;
+  k.part_rows = part_rows(a.group, a.max_rows);
+  k.q_tiles = k.part_rows / kMT;
+  // what the Q tiles and the control block leave: slots, for E4M3 with half
+  // the bytes of a third or more of them as the TMA ring in front
+  const int room = kSmem - kCtrlBytes - k.q_tiles * C::kTile;
+  if (E4M3) {
+    k.raw = HD == 128 ? 4 : 8;
+    k.slots = (room - k.raw * C::kRaw) / C::kTile;
+  } else {
+    k.raw = 0;
+    k.slots = room / C::kTile;
+  }
+  if (k.slots > kMaxSlots) k.slots = kMaxSlots;
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  if ((rc = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmem, s, tk, tv, k))) return rc;
+  return launch_pdl(paged_join_kernel<HD, BF16>, dim3(grid, k.q_tiles * 8), dim3(256), 0, s, k);
 }
 
 }  // namespace
 
-size_t paged_attention_workspace(int, int, int, int) { return kWsHeader; }
+size_t paged_attention_workspace(int n_q, int n_kv, int head_dim, int max_rows) {
+  return layout(nullptr, n_q / n_kv, head_dim, max_rows).bytes;
+}
 
-int launch_paged_attention(const PagedAttnArgs& a, int head_dim, int format, int type, void*, cudaStream_t s) {
+int launch_paged_attention(const PagedAttnArgs& a, int head_dim, int format, int type, void* ws, cudaStream_t s) {
   const bool bf = type == DFLASH_TYPE_BF16, e = format == DFLASH_CACHE_E4M3;
   if (head_dim == 128) {
-    if (e) return bf ? launch<128, true, true>(a, s) : launch<128, true, false>(a, s);
-    return bf ? launch<128, false, true>(a, s) : launch<128, false, false>(a, s);
+    if (e) return bf ? launch<128, true, true>(a, ws, s) : launch<128, true, false>(a, ws, s);
+    return bf ? launch<128, false, true>(a, ws, s) : launch<128, false, false>(a, ws, s);
   }
-  if (e) return bf ? launch<64, true, true>(a, s) : launch<64, true, false>(a, s);
-  return bf ? launch<64, false, true>(a, s) : launch<64, false, false>(a, s);
+  if (e) return bf ? launch<64, true, true>(a, ws, s) : launch<64, true, false>(a, ws, s);
+  return bf ? launch<64, false, true>(a, ws, s) : launch<64, false, false>(a, ws, s);
 }
 
 }  // namespace dfl
