@@ -20,13 +20,12 @@
 //   an item of more than 128 rows: its two Q tiles, both over every key tile
 //     (each K/V byte feeds 256 rows);
 //   a smaller one: even and odd key tiles of its one Q tile, joined at the end.
-// Roles (384 threads, 168 registers each):
+// Roles (384 threads):
 //   warp 0      page table and TMA: K and V tiles into a ring of slots
-//   warp 1      lane 0 issues S = Q K^T (both from shared memory) and
-//               O += P V (P from tensor memory, V MN-major as TMA left it)
+//   warp 1      issues S = Q K^T (both from shared memory) and O += P V (P from
+//               tensor memory, V MN-major as TMA left it)
 //   warps 2-3   zero the V rows that no row of the item sees (a weight of 0
-//               times whatever lies there must not become NaN); E4M3: widen
-//               each tile to fp16 (exact) between the TMA ring and the slots
+//               times whatever lies there must not become NaN)
 //   warps 4-7   softmax of stream 0, one query row per thread; warps 8-11
 //               stream 1.  P overwrites S in place.  O is rescaled only when a
 //               row's reference grows by more than a headroom, a few times a
@@ -34,12 +33,18 @@
 // Tensor memory: S0 | S1 | O0 | O1, 128 columns each, all 512 of it; the
 // shared memory of a CTA keeps any other off its SM.
 //
-// E4M3 caches: the codes are fp16 values exactly, so both products run in
-// fp16; bf16 queries become fp16 by a power of two per row (exact but for
-// parts 2^-28 below the row's largest).  The key scale multiplies the score
-// and the value scale the weight, both in float32; the weight is taken
-// relative to the largest value scale so far and times 2^8, which keeps it a
-// normal fp16 down to 2^-22 of the largest.
+// E4M3 caches: the codes go to the tensor cores as they lie in the cache
+// (kind::f8f6f4, twice the rate of 16 bits).  The other operand is a sum of
+// 8-bit terms that holds what 16 bits would:
+//   Q, times a power of two per row that brings its largest value to
+//     [128, 256), as E4M3 terms of 4 bits each: 2 for bf16, 3 for fp16, exact
+//     but for parts below 2^-18 of the row's largest;
+//   P as E5M2 terms of 3 bits each, cut from its fp16 value (an E5M2 is the
+//     upper byte of an fp16): 3 for bf16 outputs (9 bits, one more than a bf16
+//     weight), 4 for fp16 (all 11); exact down to 2^-16 absolute.
+// The key scale multiplies the score and the value scale the weight, both in
+// float32; a weight is taken relative to the largest value scale so far and
+// times 2^8, so its terms reach 2^-24 of the largest weight.
 //
 // All waits are bounded (mbar_wait_bounded).  When one gives up, the softmax
 // and widening warps run on without waiting (their barriers stay matched,
@@ -48,6 +53,7 @@
 #include <cstddef>
 #include <mutex>
 
+#include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
 #include "attention_util.cuh"
@@ -62,25 +68,14 @@ constexpr int kKT = 128;           // keys per tile
 constexpr int kMT = 128;           // rows of a Q tile
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;      // the workspace has room for so many
-constexpr int kMaxSlots = 12, kMaxRaw = 8;
+constexpr int kMaxSlots = 12;
+// Registers a thread: softmax warpgroups, the other one; of 168 at launch.
+constexpr int kRegsSoftmax = 208, kRegsOther = 80;
 constexpr int kCtrlBytes = 3072;
 constexpr int kSmem = 227 * 1024;  // all that a CTA may have
 constexpr uint32_t kColO = 256;    // O of stream 0; S of stream s at 128 s
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kVShift = 256.0f;  // E4M3: factor on the weights
-
-struct Ctrl {
-  uint64_t full[kMaxSlots], empty[kMaxSlots], raw_full[kMaxRaw], raw_empty[kMaxRaw];
-  uint64_t s_full[2], p_full[2], q_full[2], o_full, fix, fixed, fin;
-  unsigned long long scan[34];
-  long long start_off;
-  int start_pair, abort_flag;
-  uint32_t tmem;
-  float vmax[2][4];
-  float vfac[2];
-  alignas(16) float x[2][256];  // per warpgroup: key and value scales; (m, l) of the join; row scales of Q
-};
-static_assert(sizeof(Ctrl) <= kCtrlBytes && offsetof(Ctrl, x) % 16 == 0, "control block");
 
 // Where an item that this CTA starts but does not finish continues.
 struct Rec {
@@ -94,7 +89,7 @@ struct KernelArgs {
   Rec* rec;       // [CTA]
   int rts;        // items per request at most
   int part_rows;  // 128 or 256
-  int slots, raw; // slots of the 16-bit ring and of the E4M3 ring
+  int slots;      // of the K/V ring
   int q_tiles;    // Q tiles in shared memory
 };
 
@@ -157,25 +152,28 @@ struct Seg {
   long long before;  // units of this CTA before it
 };
 
+struct Start {
+  long long off;  // units of its pair before this CTA's part
+  int pair;
+};
+
 struct Walk {
-  const KernelArgs& k;
   long long left, total;
-  int pair, head, off, end;
-  Item it;
+  int pair, head, off;
   bool loaded;
-  __device__ Walk(const KernelArgs& kk, const Ctrl* c, long long n)
-      : k(kk), left(n), total(n), pair(c->start_pair), end(kk.a.batch.B * kk.rts), loaded(false) {
-    Item i;
-    (void)find_item(k, &pair, end, &i);
-    it = i;
+  Item it;
+  __device__ void begin(const KernelArgs& k, const Start& st, long long n) {
+    left = total = n;
+    pair = st.pair;
+    (void)find_item(k, &pair, k.a.batch.B * k.rts, &it);
     loaded = true;
-    head = (int)(c->start_off / it.units);
-    off = (int)(c->start_off - (long long)head * it.units);
+    head = (int)(st.off / it.units);
+    off = (int)(st.off - (long long)head * it.units);
   }
-  __device__ bool next(Seg* s) {
+  __device__ bool next(const KernelArgs& k, Seg* s) {
     if (left <= 0) return false;
     if (!loaded) {
-      if (!find_item(k, &pair, end, &it)) return false;
+      if (!find_item(k, &pair, k.a.batch.B * k.rts, &it)) return false;
       loaded = true;
     }
     const int take = (int)min(left, (long long)(it.units - off));
@@ -200,7 +198,49 @@ struct Walk {
   }
 };
 
+struct Ctrl {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t s_full[2], p_full[2], q_full[2], o_full, fix, fixed, fin;
+  Start start;
+  Walk walk[2];  // of the softmax warpgroups: kept here, not in every thread's registers
+  Seg seg[2];
+  int more[2];
+  int fix_slot, fix_lo, fix_hi;  // V rows outside [lo, hi) of a slot to be zeroed; slot < 0: no more
+  int abort_flag;
+  uint32_t tmem;
+  float vmax[2][4];
+  float vfac[2];
+  // per warpgroup: key and value scales; (m, l) of the join; row scales of Q.
+  // Before the roles start: scratch of the scan
+  alignas(16) float x[2][256];
+};
+static_assert(sizeof(Ctrl) <= kCtrlBytes && offsetof(Ctrl, x) % 16 == 0, "control block");
+
 // -------------------------------------------------------------- PTX helpers
+
+// Bounded wait on an mbarrier phase, like mbar_wait_bounded; the clock and the
+// abort flag are looked at after every 64 polls only (a poll already suspends
+// the thread for a while).
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  unsigned long long t0 = 0;
+  for (int i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) != 63) continue;
+    if (*abort_flag) return false;
+    const unsigned long long t = globaltimer_ns();
+    if (!t0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      report_status(status, DFLASH_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  const bool ok = wait_on(bar, parity, abort_flag, status);
+  return __all_sync(0xffffffffu, ok);
+}
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
@@ -226,32 +266,113 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Matrix descriptor of V as TMA writes it with the 128-byte swizzle: rows
-// along K of 128 bytes (64 values along N), 8-row atoms 1024 bytes apart,
-// further blocks of 64 values along N kKT x 128 bytes apart.
-__device__ __forceinline__ uint64_t v_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((kKT * 128) >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Instruction descriptor of kind::f8f6f4: float32 accumulator, A E4M3 (0) or
+// E5M2 (1), B E4M3.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t a_format) {
+  return (1u << 4) | (a_format << 7) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The warp's MMA instructions are executed by one elected lane while the whole
+// warp runs the same control flow, so that descriptors stay in uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
+template <bool E4M3>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (!E4M3) {
+    tc_mma_f16(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+template <bool E4M3>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (!E4M3) {
+    tc_mma_f16_ta(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// The fp16 pairs h0 (values 0, 1) and h1 (2, 3): their E5M2 parts, one byte
+// each in order; h0 and h1 keep the rest, which is exact.
+__device__ __forceinline__ uint32_t take_e5m2(uint32_t& h0, uint32_t& h1) {
+  const uint32_t bytes = __byte_perm(h0, h1, 0x7531);
+  auto rest = [](uint32_t h) {
+    const uint32_t top = h & 0xFF00FF00u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&top));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  h0 = rest(h0);
+  h1 = rest(h1);
+  return bytes;
+}
+
+template <int N>
+__device__ __forceinline__ void set_max_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int HD, bool E4M3, bool BF16>
 struct Cfg {
-  static constexpr int kTile = kKT * HD * 2;              // 16-bit tile of K, V or Q
-  static constexpr int kRaw = kKT * HD;                   // E4M3 tile
-  static constexpr bool kMmaBF = BF16 && !E4M3;
-  static constexpr float kHeadroom = E4M3 ? 4.0f : 8.0f;  // growth of a reference (log2) before O is rescaled
+  static constexpr int kRow = E4M3 ? HD : HD * 2;          // bytes of a cached row
+  static constexpr int kTile = kKT * kRow;                 // of a K or V tile
+  static constexpr int kQTerms = E4M3 ? (BF16 ? 2 : 3) : 1;
+  static constexpr int kPTerms = E4M3 ? (BF16 ? 3 : 4) : 1;
+  static constexpr int kQTile = kMT * kRow * kQTerms;
+  static constexpr float kHeadroom = E4M3 ? 4.0f : 8.0f;   // growth of a reference (log2) before O is rescaled
+  // Operand layouts.  A row of K or Q is kRow bytes cut into spans of at most
+  // 128; a span of all rows is one swizzled tile (128-byte swizzle, or 64 for
+  // 64-byte rows), spans kKT x span bytes apart.
+  static constexpr int kSpan = kRow < 128 ? kRow : 128;
+  static constexpr int kStepsPerSpan = kSpan / 32;         // an MMA takes 32 bytes of K and Q
+  static constexpr int kQkSteps = kRow / 32;
+  static constexpr int kPvSteps = E4M3 ? kKT / 32 : kKT / 16;  // keys per MMA: 32 codes, 16 halves
+  static constexpr int kVStep = (E4M3 ? 32 : 16) * kSpan;      // bytes of V to the next MMA's keys
+  static constexpr uint32_t kDescHi = (uint32_t)((8 * kSpan) >> 4) | (1u << 14) | ((kSpan == 64 ? 4u : 2u) << 29);
+  static constexpr uint32_t kVDescLo = (uint32_t)((kKT * kSpan) >> 4) << 16;  // next span of V along N
+  static constexpr uint32_t kIdQk = E4M3 ? idesc_f8(kMT, kKT, 0) : idesc_f32acc(kMT, kKT, BF16);
+  static constexpr uint32_t kIdPv = (E4M3 ? idesc_f8(kMT, HD, 1) : idesc_f32acc(kMT, HD, BF16)) | (1u << 16);  // V MN-major
 };
 
 // ------------------------------------------------------------------ Q tile
 
-// Rows [row0, row0 + 128) of the item's packed rows into a swizzled tile, by
-// the 128 threads of a warpgroup; rows past the item's are zero.  E4M3 with
-// bf16: fp16 by a power of two per row, its inverse in row_scale.
+// Rows [row0, row0 + 128) of the item's packed rows, those of them in
+// [r_begin, r_end), into a swizzled tile by the 128 threads of a warpgroup;
+// rows past the item's are zero.  E4M3: as terms, the inverse of the row's
+// factor in row_scale.
 template <int HD, bool E4M3, bool BF16>
 __device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, int head, int row0, uint8_t* q_s,
                                        float* row_scale, int t, int r_begin, int r_end) {
@@ -262,28 +383,44 @@ __device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, i
     const int packed = it.row0 + (ok ? pr : 0);
     const int tok = packed / a.group, g = packed - tok * a.group;
     const uint8_t* src = a.q + ((size_t)(it.s0 + tok) * a.q_row + (size_t)(head * a.group + g) * a.q_head + ch * 8) * 2;
-    uint8_t* dst = q_s + (ch >> 3) * (kMT * 128) + swz(r, (ch & 7) * 8);
-    if (!(E4M3 && BF16)) {
-      cp_async16(dst, src, ok);
+    if (!E4M3) {
+      cp_async16(q_s + (ch >> 3) * (kMT * 128) + swz(r, (ch & 7) * 8), src, ok);
     } else {
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (ok) w = __ldg(reinterpret_cast<const uint4*>(src));
-      uint32_t v[4] = {w.x, w.y, w.z, w.w}, m = 0;
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
 #pragma unroll
       for (int o = kCh / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
       m = max(m & 0xFFFFu, m >> 16);
-      int e = max((int)(m >> 7), 15);   // largest exponent field of the row
-      const bool fin = e < 255;
-      const float f = fin ? __uint_as_float((uint32_t)(268 - e) << 23) : 1.0f;   // largest into [2^14, 2^15)
+      // exponent field of the row's largest magnitude; a row that is not
+      // finite becomes NaN
+      const int e = max((int)(__float_as_uint(unpack16<BF16>(m).x) >> 23), 8);
+      const float f = e < 255 ? __uint_as_float((uint32_t)(261 - e) << 23) : __uint_as_float(0x7FC00000u);
+      float x[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 y = unpack16<true>(v[i]);
-        v[i] = pack_f16(y.x * f, y.y * f);
+        const float2 y = unpack16<BF16>(v[i]);
+        x[2 * i] = y.x * f;
+        x[2 * i + 1] = y.y * f;
       }
-      *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
-      if (ch == 0) row_scale[r] = fin ? __uint_as_float((uint32_t)(e - 14) << 23) : 1.0f;
+      const int chunk = HD == 128 ? (ch >> 1) ^ (r & 7) : (ch >> 1) ^ ((r >> 1) & 3);
+      uint8_t* dst = q_s + r * HD + chunk * 16 + (ch & 1) * 8;
+#pragma unroll
+      for (int term = 0; term < Cfg<HD, E4M3, BF16>::kQTerms; ++term) {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+          const float2 y = unpack16<false>(e4m3x2_to_f16x2((uint16_t)c[i]));
+          x[2 * i] -= y.x;
+          x[2 * i + 1] -= y.y;
+        }
+        *reinterpret_cast<uint2*>(dst + term * (kMT * HD)) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+      }
+      if (ch == 0) row_scale[r] = e < 255 ? __uint_as_float((uint32_t)(e - 7) << 23) : 1.0f;
     }
   }
 }
@@ -300,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PagedAttnArgs& a = k.a;
   uint8_t* ring_s = smem;
   uint8_t* q_s = ring_s + k.slots * C::kTile;
-  uint8_t* raw_s = q_s + k.q_tiles * C::kTile;
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + kSmem - kCtrlBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023) {  // the swizzled tiles want 1024-byte atoms
@@ -330,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rt >= items) p = (b + 1) * k.rts;
   }
   unsigned long long total;
-  const unsigned long long excl = block_exclusive_scan(mine, c->scan, &total);
+  const unsigned long long excl = block_exclusive_scan(mine, reinterpret_cast<unsigned long long*>(c->x), &total);
   const long long W = (long long)total * a.n_kv;
   const int ctas = (int)min((long long)gridDim.x, W);
   const int cta = blockIdx.x;
@@ -349,18 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += n;
       ++p;
     }
-    c->start_pair = p;
-    c->start_off = w0 - at;
+    c->start.pair = p;
+    c->start.off = w0 - at;
   }
 
   if (tid == 0) {
     for (int s = 0; s < k.slots; ++s) {
-      mbar_init(&c->full[s], E4M3 ? 2 : 1);
+      mbar_init(&c->full[s], 1);
       mbar_init(&c->empty[s], 1);
-    }
-    for (int s = 0; s < k.raw; ++s) {
-      mbar_init(&c->raw_full[s], 1);
-      mbar_init(&c->raw_empty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->s_full[i], 1);
@@ -383,226 +515,232 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = c->tmem;
   volatile int* stop = &c->abort_flag;
-  Walk walk(k, c, w1 - w0);
-  Seg s;
-
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
-    const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
-    uint8_t* dst0 = E4M3 ? raw_s : ring_s;
-    uint64_t* full = E4M3 ? c->raw_full : c->full;
-    uint64_t* empty = E4M3 ? c->raw_empty : c->empty;
-    const int ring = E4M3 ? k.raw : k.slots;
-    constexpr int kBytes = E4M3 ? C::kRaw : C::kTile;
-    int slot = 0, issued = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    while (ok && walk.next(&s)) {
-      const int32_t* table = a.batch.table + s.it.b * a.batch.table_stride;
-      int ids = 0, ids_at = -1;  // page ids of 32 pages from ids_at on, one per lane
-      for (int t = s.t0; ok && t < s.t0 + s.nt; ++t) {
-        const int first = t * per_tile;
-        // pages of the tile that hold a visible position
-        const int g0 = max(first, s.it.lo >> shift), g1 = min(first + per_tile, ((s.it.hi - 1) >> shift) + 1);
-        if (ids_at < 0 || first + per_tile > ids_at + 32) {
-          ids_at = first;
-          const int g = first + lane;
-          int id = -1;
-          if (g >= (s.it.lo >> shift) && g <= (s.it.hi - 1) >> shift) {
-            id = __ldg(table + g);
-            if (id < 0 || id >= a.batch.n_pages) {
-              report_status(a.status, DFLASH_ERR_ARG);
-              id = a.batch.n_pages;  // outside the tensor: TMA fills zeros
-            }
-          }
-          ids = id;
-        }
-        for (int side = 0; side < 2; ++side) {
-          bool got = true;
-          if (lane == 0) got = mbar_wait_bounded(&empty[slot], phase ^ 1u, stop, a.status);
-          ok = __shfl_sync(0xffffffffu, got, 0);
-          if (!ok) break;
-          uint8_t* dst = dst0 + slot * kBytes;
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)((g1 - g0) << shift) * (E4M3 ? HD : HD * 2));
-          for (int g = g0; g < g1; ++g) {
-            const int id = __shfl_sync(0xffffffffu, ids, g - ids_at);
-            if (lane == 0) {
-              const int row = (g - first) << shift;
-              const void* map = side ? &tmV : &tmK;
-              if (E4M3) {
-                tma_load_3d(dst + row * HD, map, &full[slot], 0, s.head * page_rows, id);
-              } else {
-#pragma unroll
-                for (int h = 0; h < HD / 64; ++h)
-                  tma_load_3d(dst + h * (kKT * 128) + row * 128, map, &full[slot], h * 64, s.head * page_rows, id);
+  // one setmaxnreg for a whole warpgroup
+  if (warp < 4) {
+    set_max_regs_dec<kRegsOther>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      Walk walk;
+      Seg s;
+      walk.begin(k, c->start, w1 - w0);
+      if (lane == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
+      const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
+      const int ring = k.slots;
+      int slot = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && walk.next(k, &s)) {
+        const int32_t* table = a.batch.table + s.it.b * a.batch.table_stride;
+        int ids = 0, ids_at = -1;  // page ids of 32 pages from ids_at on, one per lane
+        for (int t = s.t0; ok && t < s.t0 + s.nt; ++t) {
+          const int first = t * per_tile;
+          // pages of the tile that hold a visible position
+          const int g0 = max(first, s.it.lo >> shift), g1 = min(first + per_tile, ((s.it.hi - 1) >> shift) + 1);
+          if (ids_at < 0 || first + per_tile > ids_at + 32) {
+            ids_at = first;
+            const int g = first + lane;
+            int id = -1;
+            if (g >= (s.it.lo >> shift) && g <= (s.it.hi - 1) >> shift) {
+              id = __ldg(table + g);
+              if (id < 0 || id >= a.batch.n_pages) {
+                report_status(a.status, DFLASH_ERR_ARG);
+                id = a.batch.n_pages;  // outside the tensor: TMA fills zeros
               }
             }
+            ids = id;
           }
-          ++issued;
-          if (++slot == ring) {
-            slot = 0;
+          for (int side = 0; side < 2; ++side) {
+            bool got = true;
+            if (lane == 0) got = wait_on(&c->empty[slot], phase ^ 1u, stop, a.status);
+            ok = __shfl_sync(0xffffffffu, got, 0);
+            if (!ok) break;
+            uint8_t* dst = ring_s + slot * C::kTile;
+            if (lane == 0) mbar_arrive_expect_tx(&c->full[slot], (uint32_t)((g1 - g0) << shift) * C::kRow);
+            for (int g = g0; g < g1; ++g) {
+              const int id = __shfl_sync(0xffffffffu, ids, g - ids_at);
+              if (lane == 0) {
+                const int row = (g - first) << shift;
+                const void* map = side ? &tmV : &tmK;
+#pragma unroll
+                for (int h = 0; h < C::kRow / C::kSpan; ++h)
+                  tma_load_3d(dst + (h * kKT + row) * C::kSpan, map, &c->full[slot], h * 64, s.head * page_rows, id);
+              }
+            }
+            ++issued;
+            if (++slot == ring) {
+              slot = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+      }
+      if (!ok && lane == 0) {
+        // a wait gave up: let the copies in flight land before the CTA leaves
+        int dummy = 0;
+        for (int j = issued > ring ? issued - ring : 0; j < issued; ++j)
+          (void)mbar_wait_bounded(&c->full[j % ring], (uint32_t)(j / ring) & 1u, &dummy, nullptr, 100000000ull);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      const bool lead = elect_one();
+      const uint32_t ring_d = smem_u32(ring_s) >> 4, q_d = smem_u32(q_s) >> 4;
+      constexpr uint32_t kTileD = C::kTile >> 4;
+      uint32_t seg = 0, fixes = 0, p_phase[2] = {0, 0};
+      int kslot = 0;              // slot of the next K tile; its V tile is in the next one
+      uint32_t kphase = 0;
+      bool ok = true;
+      while (true) {
+        ok = warp_wait_on(&c->q_full[0], seg & 1u, stop, a.status) && warp_wait_on(&c->q_full[1], seg & 1u, stop, a.status);
+        ++seg;
+        if (!ok || !c->more[0]) break;
+        // the segment as warpgroup 0 described it (it stays until o_full)
+        const bool split = c->seg[0].split;
+        const int nt = c->seg[0].nt, t0 = c->seg[0].t0, lo = c->seg[0].it.lo, hi = c->seg[0].it.hi;
+        const int jobs = split ? nt : 2 * nt;
+        // K of job j + 2 comes two tiles (a split item) or one after job j's:
+        // kslot walks over the K tiles, vslot over the V tiles
+        int vslot = kslot + 1 == k.slots ? 0 : kslot + 1;
+        uint32_t vphase = kslot + 1 == k.slots ? kphase ^ 1u : kphase;
+        auto step2 = [&](int& slot, uint32_t& phase) {
+          slot += 2;
+          if (slot >= k.slots) {
+            slot -= k.slots;
             phase ^= 1u;
           }
-        }
-      }
-    }
-    if (!ok && lane == 0) {
-      // a wait gave up: let the copies in flight land before the CTA leaves
-      int dummy = 0;
-      for (int j = issued > ring ? issued - ring : 0; j < issued; ++j)
-        (void)mbar_wait_bounded(&full[j % ring], (uint32_t)(j / ring) & 1u, &dummy, nullptr, 100000000ull);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f32acc(kMT, kKT, C::kMmaBF);
-      constexpr uint32_t id_pv = idesc_f32acc(kMT, HD, C::kMmaBF) | (1u << 16);  // V is MN-major
-      const uint32_t ring_a = smem_u32(ring_s), q_a = smem_u32(q_s);
-      uint32_t base = 0, seg = 0, fixes = 0;  // ring index of the segment's first K tile
-      uint32_t jobs_p[2] = {0, 0};
-      bool ok = true;
-      while (ok && walk.next(&s)) {
-        const int jobs = s.split ? s.nt : 2 * s.nt;
-        ok = mbar_wait_bounded(&c->q_full[0], seg & 1u, stop, a.status) &&
-             mbar_wait_bounded(&c->q_full[1], seg & 1u, stop, a.status);
-        ++seg;
+        };
         tc_fence_after();
-        auto qk = [&](int j) -> bool {
-          const int st = j & 1, t = s.split ? j : j >> 1;
-          const uint32_t r = base + 2 * t, slot = r % k.slots;
-          if (s.split || st == 0) {
-            if (!mbar_wait_bounded(&c->full[slot], (r / k.slots) & 1u, stop, a.status)) return false;
+        auto qk = [&](int st) {
+          if (split || st == 0) {
+            ok = ok && warp_wait_on(&c->full[kslot], kphase, stop, a.status);
             tc_fence_after();
           }
-          const uint32_t ka = ring_a + slot * C::kTile, qa = q_a + (s.split ? 0 : st) * C::kTile;
+          const uint32_t kd = ring_d + kslot * kTileD, qd = q_d + (split ? 0u : (uint32_t)st * (C::kQTile >> 4));
+          if (lead) {
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kKT * 128) + (kk & 3) * 32;
-            tc_mma_f16(tmem + st * kKT, smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id_qk, kk > 0);
-          }
-          tc_commit(&c->s_full[st]);
-          if (s.split || st == 1) tc_commit(&c->empty[slot]);
-          return true;
-        };
-        auto pv = [&](int j) -> bool {
-          const int st = j & 1, t = s.split ? j : j >> 1;
-          const uint32_t r = base + 2 * t + 1, slot = r % k.slots;
-          bool edge = false;  // V rows of the tile are out of sight: have them zeroed
-          if (s.split || st == 0) {
-            if (!mbar_wait_bounded(&c->full[slot], (r / k.slots) & 1u, stop, a.status)) return false;
-            const int k0 = (s.t0 + t) * kKT;
-            edge = !E4M3 && (k0 < s.it.lo || k0 + kKT > s.it.hi);
-            if (edge) mbar_arrive(&c->fix);
-          }
-          if (!mbar_wait_bounded(&c->p_full[st], jobs_p[st]++ & 1u, stop, a.status)) return false;
-          if (edge && !mbar_wait_bounded(&c->fixed, fixes++ & 1u, stop, a.status)) return false;
-          tc_fence_after();
-          const uint32_t va = ring_a + slot * C::kTile;
-          const bool fresh = s.split ? j < 2 : t == 0;
+            for (int term = 0; term < C::kQTerms; ++term)
 #pragma unroll
-          for (int kk = 0; kk < kKT / 16; ++kk)
-            tc_mma_f16_ta(tmem + kColO + st * 128, tmem + st * kKT + kk * 8, v_desc(va + kk * 2048), id_pv,
-                          !fresh || kk > 0);
-          if (s.split || st == 1) tc_commit(&c->empty[slot]);
-          return true;
+              for (int kk = 0; kk < C::kQkSteps; ++kk) {
+                const uint32_t off = (kk / C::kStepsPerSpan) * ((kKT * C::kSpan) >> 4) + (kk % C::kStepsPerSpan) * 2;
+                mma_ss<E4M3>(tmem + st * kKT, desc64(qd + term * ((kMT * C::kRow) >> 4) + off + (1u << 16), C::kDescHi),
+                             desc64(kd + off + (1u << 16), C::kDescHi), C::kIdQk, term > 0 || kk > 0);
+              }
+            tc_commit(&c->s_full[st]);
+            if (split || st == 1) tc_commit(&c->empty[kslot]);
+          }
+          __syncwarp();
+          if (split || st == 1) step2(kslot, kphase);
         };
-        if (ok && jobs > 0) ok = qk(0);
-        if (ok && jobs > 1) ok = qk(1);
+        if (ok && jobs > 0) qk(0);
+        if (ok && jobs > 1) qk(1);
         for (int j = 0; ok && j < jobs; ++j) {
-          ok = pv(j);
+          const int st = j & 1;
+          bool edge = false;  // V rows of the tile are out of sight: have them zeroed
+          if (split || st == 0) {
+            ok = warp_wait_on(&c->full[vslot], vphase, stop, a.status);
+            const int k0 = (t0 + (split ? j : j >> 1)) * kKT;
+            edge = k0 < lo || k0 + kKT > hi;
+            if (edge && lead) {
+              c->fix_slot = vslot;
+              c->fix_lo = lo - k0;
+              c->fix_hi = hi - k0;
+              mbar_arrive(&c->fix);
+            }
+            __syncwarp();
+          }
+          ok = ok && warp_wait_on(&c->p_full[st], p_phase[st], stop, a.status);
+          p_phase[st] ^= 1u;
+          if (edge) {
+            ok = ok && warp_wait_on(&c->fixed, fixes & 1u, stop, a.status);
+            ++fixes;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t vd = ring_d + vslot * kTileD + C::kVDescLo;
+          const uint32_t fresh = j < 2;  // the stream's first job
+          if (lead) {
+#pragma unroll
+            for (int term = 0; term < C::kPTerms; ++term)
+#pragma unroll
+              for (int kk = 0; kk < C::kPvSteps; ++kk)
+                mma_ts<E4M3>(tmem + kColO + st * 128, tmem + st * kKT + term * 32 + kk * 8,
+                             desc64(vd + kk * (C::kVStep >> 4), C::kDescHi), C::kIdPv,
+                             (term > 0 || kk > 0) ? 1u : fresh ^ 1u);
+            if (split || st == 1) tc_commit(&c->empty[vslot]);
+          }
+          __syncwarp();
+          if (split || st == 1) step2(vslot, vphase);
           // P of a job overwrites its S: the next scores of the stream follow
           // its P V in the tensor pipe's order
-          if (ok && j + 2 < jobs) ok = qk(j + 2);
+          if (j + 2 < jobs) qk(st);
         }
-        tc_commit(&c->o_full);
-        base += 2 * s.nt;
+        if (!ok) break;
+        if (lead) tc_commit(&c->o_full);
+        __syncwarp();
       }
-      tc_commit(&c->fin);  // every MMA this thread issued
-    }
-    __syncwarp();
-  } else if (warp < 4) {
-    // ------------------------------- V rows out of sight; E4M3: widening
-    const int ct = tid - 64;  // 0..63
-    uint32_t r = 0, fixes = 0;
-    while (walk.next(&s)) {
-      for (int t = s.t0; t < s.t0 + s.nt; ++t) {
-        const int k0 = t * kKT;
-        const int v0 = max(0, s.it.lo - k0), v1 = min(kKT, s.it.hi - k0);  // rows in sight
-        if (!E4M3) {
-          if (v0 > 0 || v1 < kKT) {
-            const uint32_t rv = r + 1, slot = rv % k.slots;
-            (void)warp_wait(&c->fix, fixes++ & 1u, stop, a.status);  // the tile is there
-            uint8_t* v = ring_s + slot * C::kTile;
-            for (int idx = ct; idx < kKT * (HD / 8); idx += 64) {
-              const int row = idx / (HD / 8), ch = idx % (HD / 8);
-              if (row < v0 || row >= v1)
-                *reinterpret_cast<uint4*>(v + (ch >> 3) * (kKT * 128) + row * 128 + (ch & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->fixed);
-          }
-        } else {
-          for (int side = 0; side < 2; ++side) {
-            const uint32_t rs = r + side, raw = rs % k.raw, slot = rs % k.slots;
-            (void)warp_wait(&c->raw_full[raw], (rs / k.raw) & 1u, stop, a.status);
-            (void)warp_wait(&c->empty[slot], ((rs / k.slots) & 1u) ^ 1u, stop, a.status);
-            const uint4* src = reinterpret_cast<const uint4*>(raw_s + raw * C::kRaw);
-            uint8_t* dst = ring_s + slot * C::kTile;
-            constexpr int kCh = HD / 16;  // 16-code chunks of a row
-#pragma unroll 4
-            for (int i = 0; i < kKT * kCh / 64; ++i) {
-              const int idx = ct + i * 64, row = idx / kCh, ch = idx % kCh;
-              uint4 w = src[idx];
-              if (side && (row < v0 || row >= v1)) w = make_uint4(0u, 0u, 0u, 0u);
-              const uint4 lo = make_uint4(e4m3x2_to_f16x2((uint16_t)w.x), e4m3x2_to_f16x2((uint16_t)(w.x >> 16)),
-                                          e4m3x2_to_f16x2((uint16_t)w.y), e4m3x2_to_f16x2((uint16_t)(w.y >> 16)));
-              const uint4 hi = make_uint4(e4m3x2_to_f16x2((uint16_t)w.z), e4m3x2_to_f16x2((uint16_t)(w.z >> 16)),
-                                          e4m3x2_to_f16x2((uint16_t)w.w), e4m3x2_to_f16x2((uint16_t)(w.w >> 16)));
-              uint8_t* base = dst + (ch >> 2) * (kKT * 128) + row * 128;
-              const int c0 = (ch & 3) * 2;
-              // the upper half's chunks go in the other order: the eight
-              // threads of a row then hit eight different 16-byte banks
-              const bool swap = (ch >> 2) & 1;
-              *reinterpret_cast<uint4*>(base + (((c0 + swap) ^ row) & 7) * 16) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(base + (((c0 + !swap) ^ row) & 7) * 16) = swap ? lo : hi;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&c->raw_empty[raw]);
-              mbar_arrive(&c->full[slot]);
-            }
-          }
+      if (lead) {
+        c->fix_slot = -1;
+        mbar_arrive(&c->fix);
+        tc_commit(&c->fin);  // every MMA this thread issued
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------ V rows out of sight
+      const int ct = tid - 64;  // 0..63
+      uint32_t fixes = 0;
+      while (warp_wait_on(&c->fix, fixes++ & 1u, stop, a.status)) {
+        const int slot = c->fix_slot, v0 = c->fix_lo, v1 = c->fix_hi;
+        if (slot < 0) break;
+        uint8_t* v = ring_s + slot * C::kTile;
+        for (int idx = ct; idx < kKT * (C::kRow / 16); idx += 64) {
+          const int row = (idx / (C::kSpan / 16)) % kKT;  // a row of a span: all its chunks, whatever the swizzle
+          if (row < v0 || row >= v1) reinterpret_cast<uint4*>(v)[idx] = make_uint4(0u, 0u, 0u, 0u);
         }
-        r += 2;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->fixed);
       }
     }
   } else {
     // ------------------------------------------------------------ softmax
+    set_max_regs_inc<kRegsSoftmax>();
     const int wg = (warp >> 2) - 1, t = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + wg * kKT, tO = tmem + lane_off + kColO;
     float* x = c->x[wg];
     uint32_t jobs = 0, seg = 0;
-    Rec rec = {-1, 0, 0, 0};
-    while (walk.next(&s)) {
+    if (t == 0) {
+      c->walk[wg].begin(k, c->start, w1 - w0);
+      if (wg == 0) k.rec[cta].pair = -1;
+    }
+    while (true) {
+      named_sync(1 + wg, 128);  // the last segment's description has been read
+      if (t == 0) {
+        c->more[wg] = c->walk[wg].next(k, &c->seg[wg]);
+        const Seg& n = c->seg[wg];
+        if (wg == 0 && c->more[0] && n.first && !n.last) {
+          const long long u = w0 + n.before + n.it.units - 1;  // the item's last unit
+          k.rec[cta] = Rec{n.pair, n.head, n.slot, (int)(((u + 1) * ctas - 1) / W)};
+        }
+      }
+      named_sync(1 + wg, 128);
+      if (!c->more[wg]) {
+        if (t == 0) mbar_arrive(&c->q_full[wg]);  // wakes the MMA warp, which sees the end too
+        break;
+      }
+      const Seg& s = c->seg[wg];
       const Item& it = s.it;
       // ---- queries of this stream (a split item's one tile: half by each
       // warpgroup, or all by both where the row scales are needed by both)
       if (s.split) {
-        constexpr bool kAll = E4M3 && BF16;
-        load_q<HD, E4M3, BF16>(a, it, s.head, 0, q_s, x, t, kAll ? 0 : 64 * wg, kAll ? kMT : 64 * wg + 64);
+        load_q<HD, E4M3, BF16>(a, it, s.head, 0, q_s, x, t, E4M3 ? 0 : 64 * wg, E4M3 ? kMT : 64 * wg + 64);
       } else {
-        load_q<HD, E4M3, BF16>(a, it, s.head, kMT * wg, q_s + wg * C::kTile, x, t, 0, kMT);
+        load_q<HD, E4M3, BF16>(a, it, s.head, kMT * wg, q_s + wg * C::kQTile, x, t, 0, kMT);
       }
-      if (!(E4M3 && BF16)) cp_async_wait_all();
+      if (!E4M3) cp_async_wait_all();
       fence_proxy_async_smem();
       named_sync(1 + wg, 128);
       if (t == 0) mbar_arrive(&c->q_full[wg]);
@@ -615,10 +753,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows past the item's see everything: their scores are zero
       const int hi = !real ? 1 << 30 : a.causal ? min(it.len, pos + 1) : it.len;
       const int lo = real && a.window ? pos - a.window + 1 : -(1 << 30);
-      const float cs = a.scale_log2 * (E4M3 && BF16 ? x[t] : 1.0f);
+      const float cs = a.scale_log2 * (E4M3 ? x[t] : 1.0f);
 
       float m_ref = -INFINITY, l = 0.0f, vref = 0.0f;
-      const int step = s.split ? 2 : 1, j0 = s.split ? wg : 0;
+      const int step = s.split ? 2 : 1, j0 = s.split ? wg : 0, nt = s.nt, t0 = s.t0;
       float nks = 0.0f, nvs = 0.0f;  // scales of key t of the next tile
       auto fetch = [&](int tile) {
         const int key = tile * kKT + t;
@@ -632,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      if (E4M3 && j0 < s.nt) fetch(s.t0 + j0);
-      for (int j = j0; j < s.nt; j += step) {
+      if (E4M3 && j0 < nt) fetch(t0 + j0);
+      for (int j = j0; j < nt; j += step) {
         float fv = 1.0f;  // E4M3: change of the value reference
         float cv = 0.0f;
         if (E4M3) {
@@ -650,9 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             vref = nv;
           }
           cv = kVShift / vref;
-          if (j + step < s.nt) fetch(s.t0 + j + step);
+          if (j + step < nt) fetch(t0 + j + step);
         }
-        (void)warp_wait(&c->s_full[wg], jobs++ & 1u, stop, a.status);
+        (void)warp_wait_on(&c->s_full[wg], jobs++ & 1u, stop, a.status);
         tc_fence_after();
         if (!live) {
           // no query row in this warp's lanes: whatever their P holds only
@@ -675,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sv[e + 3] *= f.w;
           }
         }
-        const int k0 = (s.t0 + j) * kKT;
+        const int k0 = (t0 + j) * kKT;
         if (!__all_sync(0xffffffffu, k0 >= lo && k0 + kKT <= hi)) {
           const int e0 = lo - k0, e1 = hi - k0;  // visible: e0 <= e < e1
 #pragma unroll
@@ -717,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t pw[16];
+          uint32_t pw[16];  // 16-bit weights of 32 keys
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             float p[4];
@@ -733,10 +871,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[2] *= f.z * cv;
               p[3] *= f.w * cv;
             }
-            pw[e / 2] = pack16<C::kMmaBF>(p[0], p[1]);
-            pw[e / 2 + 1] = pack16<C::kMmaBF>(p[2], p[3]);
+            pw[e / 2] = pack16<!E4M3 && BF16>(p[0], p[1]);
+            pw[e / 2 + 1] = pack16<!E4M3 && BF16>(p[2], p[3]);
           }
-          tmem_st_x16(tS + q * 16, pw);
+          if (!E4M3) {
+            tmem_st_x16(tS + q * 16, pw);
+          } else {
+            // three terms keep 9 bits: round there first (positive values)
+            if (C::kPTerms == 3) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pw[e] += 0x00020002u;
+            }
+#pragma unroll
+            for (int term = 0; term < C::kPTerms; ++term) {
+              uint32_t b[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) b[e] = take_e5m2(pw[2 * e], pw[2 * e + 1]);
+              tmem_st_x8(tS + term * 32 + q * 8, b);
+            }
+          }
         }
         l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         tc_wait_st();
@@ -746,13 +899,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- end of the segment: O is final
-      (void)warp_wait(&c->o_full, seg++ & 1u, stop, a.status);
+      (void)warp_wait_on(&c->o_full, seg++ & 1u, stop, a.status);
       tc_fence_after();
       const bool whole = s.first && s.last;
-      if (s.first && !s.last) {
-        const long long u = w0 + s.before + it.units - 1;  // the item's last unit
-        rec = {s.pair, s.head, s.slot, (int)(((u + 1) * ctas - 1) / W)};
-      }
       float f0, f1 = 0.0f, M = m_ref, L = l;  // factors of O0 and O1 (a row-split item: of its own O)
       f0 = E4M3 ? vref * (1.0f / kVShift) : 1.0f;
       if (s.split) {
@@ -814,7 +963,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
-    if (warp == 4 && lane == 0) k.rec[cta] = rec;
   }
 
   // tensor memory is no longer read: free it once every MMA has completed
@@ -909,7 +1057,7 @@ int encode_pages(CUtensorMap* map, const void* ptr, const PagedAttnArgs& a, int 
                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUresult r = g_encode(map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                              e4m3 && hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
@@ -949,6 +1097,10 @@ int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   } else {
     DFL_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     DFL_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    // the register split has to fit what a CTA is launched with
+    cudaFuncAttributes fa;
+    DFL_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+    if (fa.numRegs * kThreads < kRegsSoftmax * 256 + kRegsOther * 128) return DFLASH_ERR_UNSUPPORTED;
     if (dev < 64) known[dev].store(sms);
   }
   KernelArgs k;
@@ -962,16 +1114,7 @@ int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   k.rts = (int)rts;
   k.part_rows = part_rows(a.group, a.max_rows);
   k.q_tiles = k.part_rows / kMT;
-  // what the Q tiles and the control block leave: slots, for E4M3 with half
-  // the bytes of a third or more of them as the TMA ring in front
-  const int room = kSmem - kCtrlBytes - k.q_tiles * C::kTile;
-  if (E4M3) {
-    k.raw = HD == 128 ? 4 : 8;
-    k.slots = (room - k.raw * C::kRaw) / C::kTile;
-  } else {
-    k.raw = 0;
-    k.slots = room / C::kTile;
-  }
+  k.slots = (kSmem - kCtrlBytes - k.q_tiles * C::kQTile) / C::kTile;
   if (k.slots > kMaxSlots) k.slots = kMaxSlots;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   if ((rc = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmem, s, tk, tv, k))) return rc;
