@@ -69,13 +69,11 @@ constexpr int kMT = 128;           // rows of a Q tile
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;      // the workspace has room for so many
 constexpr int kMaxSlots = 12;
-// Registers a thread: softmax warpgroups, the other one; of 168 at launch.
-constexpr int kRegsSoftmax = 208, kRegsOther = 80;
 constexpr int kCtrlBytes = 3072;
 constexpr int kSmem = 227 * 1024;  // all that a CTA may have
 constexpr uint32_t kColO = 256;    // O of stream 0; S of stream s at 128 s
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kVShift = 256.0f;  // E4M3: factor on the weights
+constexpr float kVShiftLog2 = 8.0f;  // E4M3: factor on the weights
 
 // Where an item that this CTA starts but does not finish continues.
 struct Rec {
@@ -209,7 +207,6 @@ struct Ctrl {
   int abort_flag;
   uint32_t tmem;
   float vmax[2][4];
-  float vfac[2];
   // per warpgroup: key and value scales; (m, l) of the join; row scales of Q.
   // Before the roles start: scratch of the scan
   alignas(16) float x[2][256];
@@ -250,7 +247,7 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float* v) {
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -322,6 +319,32 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8
       : "memory");
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // The fp16 pairs h0 (values 0, 1) and h1 (2, 3): their E5M2 parts, one byte
 // each in order; h0 and h1 keep the rest, which is exact.
 __device__ __forceinline__ uint32_t take_e5m2(uint32_t& h0, uint32_t& h1) {
@@ -334,15 +357,6 @@ __device__ __forceinline__ uint32_t take_e5m2(uint32_t& h0, uint32_t& h1) {
   h0 = rest(h0);
   h1 = rest(h1);
   return bytes;
-}
-
-template <int N>
-__device__ __forceinline__ void set_max_regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_max_regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int HD, bool E4M3, bool BF16>
@@ -361,6 +375,11 @@ struct Cfg {
   static constexpr int kQkSteps = kRow / 32;
   static constexpr int kPvSteps = E4M3 ? kKT / 32 : kKT / 16;  // keys per MMA: 32 codes, 16 halves
   static constexpr int kVStep = (E4M3 ? 32 : 16) * kSpan;      // bytes of V to the next MMA's keys
+  // Column of the weights of MMA kk (and term) in S: the weights of 32 keys lie
+  // in the 32 columns that held those keys' scores.
+  static __host__ __device__ constexpr uint32_t p_col(int term, int kk) {
+    return E4M3 ? kk * 32 + term * 8 : (kk >> 1) * 32 + (kk & 1) * 8;
+  }
   static constexpr uint32_t kDescHi = (uint32_t)((8 * kSpan) >> 4) | (1u << 14) | ((kSpan == 64 ? 4u : 2u) << 29);
   static constexpr uint32_t kVDescLo = (uint32_t)((kKT * kSpan) >> 4) << 16;  // next span of V along N
   static constexpr uint32_t kIdQk = E4M3 ? idesc_f8(kMT, kKT, 0) : idesc_f32acc(kMT, kKT, BF16);
@@ -377,18 +396,35 @@ template <int HD, bool E4M3, bool BF16>
 __device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, int head, int row0, uint8_t* q_s,
                                        float* row_scale, int t, int r_begin, int r_end) {
   constexpr int kCh = HD / 8;  // 16-byte chunks of a row
-  for (int idx = r_begin * kCh + t; idx < r_end * kCh; idx += 128) {
-    const int r = idx / kCh, ch = idx % kCh, pr = row0 + r;
-    const bool ok = pr < it.rows;
-    const int packed = it.row0 + (ok ? pr : 0);
+  auto source = [&](int idx, bool* ok) {
+    const int pr = row0 + idx / kCh;
+    *ok = pr < it.rows;
+    const int packed = it.row0 + (*ok ? pr : 0);
     const int tok = packed / a.group, g = packed - tok * a.group;
-    const uint8_t* src = a.q + ((size_t)(it.s0 + tok) * a.q_row + (size_t)(head * a.group + g) * a.q_head + ch * 8) * 2;
-    if (!E4M3) {
+    return a.q + ((size_t)(it.s0 + tok) * a.q_row + (size_t)(head * a.group + g) * a.q_head + (idx % kCh) * 8) * 2;
+  };
+  if (!E4M3) {
+    for (int idx = r_begin * kCh + t; idx < r_end * kCh; idx += 128) {
+      bool ok;
+      const uint8_t* src = source(idx, &ok);
+      const int r = idx / kCh, ch = idx % kCh;
       cp_async16(q_s + (ch >> 3) * (kMT * 128) + swz(r, (ch & 7) * 8), src, ok);
-    } else {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (ok) w = __ldg(reinterpret_cast<const uint4*>(src));
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    }
+    return;
+  }
+  constexpr int kBatch = 4;  // loads in flight per thread
+  for (int i0 = r_begin * kCh; i0 < r_end * kCh; i0 += 128 * kBatch) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      bool ok;
+      const uint8_t* src = source(i0 + u * 128 + t, &ok);
+      w[u] = ok ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int idx = i0 + u * 128 + t, r = idx / kCh, ch = idx % kCh;
+      const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
@@ -515,9 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = c->tmem;
   volatile int* stop = &c->abort_flag;
-  // one setmaxnreg for a whole warpgroup
   if (warp < 4) {
-    set_max_regs_dec<kRegsOther>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       Walk walk;
@@ -666,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int term = 0; term < C::kPTerms; ++term)
 #pragma unroll
               for (int kk = 0; kk < C::kPvSteps; ++kk)
-                mma_ts<E4M3>(tmem + kColO + st * 128, tmem + st * kKT + term * 32 + kk * 8,
+                mma_ts<E4M3>(tmem + kColO + st * 128, tmem + st * kKT + C::p_col(term, kk),
                              desc64(vd + kk * (C::kVStep >> 4), C::kDescHi), C::kIdPv,
                              (term > 0 || kk > 0) ? 1u : fresh ^ 1u);
             if (split || st == 1) tc_commit(&c->empty[vslot]);
@@ -706,7 +740,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    set_max_regs_inc<kRegsSoftmax>();
     const int wg = (warp >> 2) - 1, t = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + wg * kKT, tO = tmem + lane_off + kColO;
@@ -755,7 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo = real && a.window ? pos - a.window + 1 : -(1 << 30);
       const float cs = a.scale_log2 * (E4M3 ? x[t] : 1.0f);
 
-      float m_ref = -INFINITY, l = 0.0f, vref = 0.0f;
+      float m_ref = -INFINITY, l = 0.0f;
+      float vref = 0.0f, cv = 0.0f;  // E4M3: reference of the value scales, log2 of the weights' factor
       const int step = s.split ? 2 : 1, j0 = s.split ? wg : 0, nt = s.nt, t0 = s.t0;
       float nks = 0.0f, nvs = 0.0f;  // scales of key t of the next tile
       auto fetch = [&](int tile) {
@@ -773,7 +807,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (E4M3 && j0 < nt) fetch(t0 + j0);
       for (int j = j0; j < nt; j += step) {
         float fv = 1.0f;  // E4M3: change of the value reference
-        float cv = 0.0f;
         if (E4M3) {
           named_sync(1 + wg, 128);  // the last job's scales have been read
           x[t] = nks;
@@ -783,11 +816,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_sync(1 + wg, 128);
           const float vm = fmaxf(fmaxf(c->vmax[wg][0], c->vmax[wg][1]), fmaxf(c->vmax[wg][2], c->vmax[wg][3]));
           if (vm > 8.0f * vref || vref == 0.0f) {
-            const float nv = fmaxf(vm, 1e-30f);
+            const float nv = fmaxf(vm, 0x1p-60f);
             fv = vref / nv;
             vref = nv;
+            cv = kVShiftLog2 - log2f(vref);
           }
-          cv = kVShift / vref;
           if (j + step < nt) fetch(t0 + j + step);
         }
         (void)warp_wait_on(&c->s_full[wg], jobs++ & 1u, stop, a.status);
@@ -799,46 +832,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&c->p_full[wg]);
           continue;
         }
-        float sv[kKT];
+        const int k0 = (t0 + j) * kKT;
+        const bool edge = !__all_sync(0xffffffffu, k0 >= lo && k0 + kKT <= hi);
+        const int e0 = lo - k0, e1 = hi - k0;  // visible: e0 <= e < e1
+        // the scores of 32 keys from column 32 q on, scaled and masked
+        auto ready = [&](int q, float (&v)[32]) {
+          if (E4M3) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_x32(tS + i * 32, sv + i * 32);
-        tc_wait_ld();
-        if (E4M3) {
+            for (int e = 0; e < 32; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(x + q * 32 + e);
+              const float2 a0 = mul2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y));
+              const float2 a1 = mul2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w));
+              v[e] = a0.x;
+              v[e + 1] = a0.y;
+              v[e + 2] = a1.x;
+              v[e + 3] = a1.y;
+            }
+          }
+          if (edge) {
 #pragma unroll
-          for (int e = 0; e < kKT; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(x + e);
-            sv[e] *= f.x;
-            sv[e + 1] *= f.y;
-            sv[e + 2] *= f.z;
-            sv[e + 3] *= f.w;
+            for (int e = 0; e < 32; ++e)
+              if (q * 32 + e < e0 || q * 32 + e >= e1) v[e] = -INFINITY;
+          }
+        };
+        // ---- the row's largest score; the scores stay in tensor memory, so
+        // that the code of a pass is short and the registers few
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+          float v0[32], v1[32];
+          tmem_ld_x32(tS + q * 32, v0);
+          tmem_ld_x32(tS + q * 32 + 32, v1);
+          tc_wait_ld();
+          ready(q, v0);
+          ready(q + 1, v1);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(v0[e + i], v1[e + i]));
           }
         }
-        const int k0 = (t0 + j) * kKT;
-        if (!__all_sync(0xffffffffu, k0 >= lo && k0 + kKT <= hi)) {
-          const int e0 = lo - k0, e1 = hi - k0;  // visible: e0 <= e < e1
-#pragma unroll
-          for (int e = 0; e < kKT; ++e)
-            if (e < e0 || e >= e1) sv[e] = -INFINITY;
-        }
-        float mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          mx[i] = sv[i];
-#pragma unroll
-          for (int e = i + 8; e < kKT; e += 8) mx[i] = fmaxf(mx[i], sv[e]);
-        }
-        const float m_tile =
-            fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * cs;
+        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
         const bool grow = m_tile > m_ref + C::kHeadroom || (m_ref == -INFINITY && m_tile > -INFINITY);
         if (__any_sync(0xffffffffu, grow || fv != 1.0f)) {
           const float m_new = grow ? m_tile : m_ref;
-          const float f = grow ? ex2_approx(m_ref - m_new) : 1.0f;  // 0 while nothing was seen
+          const float fo = (grow ? ex2_approx(m_ref - m_new) : 1.0f) * fv;  // 0 while nothing was seen
           if (j > j0) {
             // O holds the stream's earlier jobs: their P V precede these
             // scores in the tensor pipe, the next one waits for this P
-            const float fo = f * fv;
             uint32_t r[16];
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < HD / 16; ++i) {
               const uint32_t oa = tO + wg * 128 + i * 16;
               tmem_ld_x16(oa, r);
@@ -848,34 +891,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_x16(oa, r);
             }
           }
-          l *= f;
+          l *= fo;
           m_ref = m_new;
         }
-        const float nb = m_ref == -INFINITY ? 0.0f : -m_ref;
-        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        // ---- weights 2^(z - m_ref + cv); l and O carry the factor, too
+        const float nb = m_ref == -INFINITY ? 0.0f : cv - m_ref;
+        const float2 cs2 = make_float2(cs, cs), nb2 = make_float2(nb, nb);
+        float2 ls0 = make_float2(0.0f, 0.0f), ls1 = ls0;
+        auto weigh = [&](int q, float (&v)[32]) {
+          ready(q, v);
           uint32_t pw[16];  // 16-bit weights of 32 keys
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              p[i] = ex2_approx(fmaf(sv[q * 32 + e + i], cs, nb));
-              ls[i] += p[i];
-            }
+            float2 p0 = fma2(make_float2(v[e], v[e + 1]), cs2, nb2), p1 = fma2(make_float2(v[e + 2], v[e + 3]), cs2, nb2);
+            p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
+            p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
+            ls0 = add2(ls0, p0);
+            ls1 = add2(ls1, p1);
             if (E4M3) {
               const float4 f = *reinterpret_cast<const float4*>(x + 128 + q * 32 + e);
-              p[0] *= f.x * cv;
-              p[1] *= f.y * cv;
-              p[2] *= f.z * cv;
-              p[3] *= f.w * cv;
+              p0 = mul2(p0, make_float2(f.x, f.y));
+              p1 = mul2(p1, make_float2(f.z, f.w));
             }
-            pw[e / 2] = pack16<!E4M3 && BF16>(p[0], p[1]);
-            pw[e / 2 + 1] = pack16<!E4M3 && BF16>(p[2], p[3]);
+            pw[e / 2] = pack16<!E4M3 && BF16>(p0.x, p0.y);
+            pw[e / 2 + 1] = pack16<!E4M3 && BF16>(p1.x, p1.y);
           }
           if (!E4M3) {
-            tmem_st_x16(tS + q * 16, pw);
+            tmem_st_x16(tS + q * 32, pw);
           } else {
             // three terms keep 9 bits: round there first (positive values)
             if (C::kPTerms == 3) {
@@ -887,11 +929,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t b[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) b[e] = take_e5m2(pw[2 * e], pw[2 * e + 1]);
-              tmem_st_x8(tS + term * 32 + q * 8, b);
+              tmem_st_x8(tS + q * 32 + term * 8, b);
             }
           }
+        };
+        {
+          float v0[32], v1[32];
+          tmem_ld_x32(tS, v0);
+#pragma unroll 1
+          for (int q = 0; q < 4; q += 2) {
+            tc_wait_ld();
+            tmem_ld_x32(tS + q * 32 + 32, v1);
+            weigh(q, v0);
+            tc_wait_ld();
+            if (q == 0) tmem_ld_x32(tS + 64, v0);
+            weigh(q + 1, v1);
+          }
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -902,20 +957,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       (void)warp_wait_on(&c->o_full, seg++ & 1u, stop, a.status);
       tc_fence_after();
       const bool whole = s.first && s.last;
-      float f0, f1 = 0.0f, M = m_ref, L = l;  // factors of O0 and O1 (a row-split item: of its own O)
-      f0 = E4M3 ? vref * (1.0f / kVShift) : 1.0f;
+      // factors of O0 and O1 (a row-split item: of its own O)
+      float f0 = 1.0f, f1 = 0.0f, M = m_ref - cv, L = l;
       if (s.split) {
         named_sync(1 + wg, 128);  // scales are no longer read
-        x[t] = m_ref;
+        x[t] = M;
         x[128 + t] = l;
-        if (t == 0) c->vfac[wg] = f0;
         named_sync(3, 256);
         const float m0 = c->x[0][t], m1 = c->x[1][t];
         M = fmaxf(m0, m1);
-        const float e0 = m0 == -INFINITY ? 0.0f : ex2_approx(m0 - M), e1 = m1 == -INFINITY ? 0.0f : ex2_approx(m1 - M);
-        L = c->x[0][128 + t] * e0 + c->x[1][128 + t] * e1;
-        f0 = e0 * c->vfac[0];
-        f1 = e1 * c->vfac[1];
+        f0 = m0 == -INFINITY ? 0.0f : ex2_approx(m0 - M);
+        f1 = m1 == -INFINITY ? 0.0f : ex2_approx(m1 - M);
+        L = c->x[0][128 + t] * f0 + c->x[1][128 + t] * f1;
         named_sync(3, 256);  // read by all before the next segment's scales
       }
       const float inv = whole ? (L > 0.0f || L != L ? 1.0f / L : 0.0f) : 1.0f;
@@ -1097,10 +1150,6 @@ int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   } else {
     DFL_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     DFL_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-    // the register split has to fit what a CTA is launched with
-    cudaFuncAttributes fa;
-    DFL_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
-    if (fa.numRegs * kThreads < kRegsSoftmax * 256 + kRegsOther * 128) return DFLASH_ERR_UNSUPPORTED;
     if (dev < 64) known[dev].store(sms);
   }
   KernelArgs k;
