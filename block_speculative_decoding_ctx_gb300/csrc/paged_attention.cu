@@ -22,9 +22,9 @@
 //   a smaller one: even and odd key tiles of its one Q tile, joined at the end.
 // Roles (384 threads):
 //   warp 0      page table and TMA: K and V tiles into a ring of slots
-//   warp 1      issues S = Q K^T (both from shared memory) and O += P V (P from
-//               tensor memory, V MN-major as TMA left it)
-//   warps 2-3   zero the V rows that no row of the item sees (a weight of 0
+//   warps 1, 2  issue their stream's S = Q K^T (both from shared memory) and
+//               O += P V (P from tensor memory, V MN-major as TMA left it), and
+//               zero the V rows that no row of the item sees (a weight of 0
 //               times whatever lies there must not become NaN)
 //   warps 4-7   softmax of stream 0, one query row per thread; warps 8-11
 //               stream 1.  P overwrites S in place.  O is rescaled only when a
@@ -64,7 +64,8 @@ namespace {
 
 using namespace attn;
 
-constexpr int kKT = 128;           // keys per tile
+constexpr int kKT = 128;           // keys per tile: what TMA loads
+constexpr int kHK = 64;            // keys per job: half a tile
 constexpr int kMT = 128;           // rows of a Q tile
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;      // the workspace has room for so many
@@ -198,12 +199,12 @@ struct Walk {
 
 struct Ctrl {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], q_full[2], o_full, fix, fixed, fin;
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half of the key tile]
+  uint64_t q_full[2], o_full, fin;
   Start start;
   Walk walk[2];  // of the softmax warpgroups: kept here, not in every thread's registers
   Seg seg[2];
   int more[2];
-  int fix_slot, fix_lo, fix_hi;  // V rows outside [lo, hi) of a slot to be zeroed; slot < 0: no more
   int abort_flag;
   uint32_t tmem;
   float vmax[2][4];
@@ -247,20 +248,40 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
+// Tensor-memory accesses of the softmax.  They touch no C++ memory, so none
+// clobbers it (shared-memory loads may move across them); being volatile they
+// keep their order, and the wait passes the loaded values through, so that no
+// use of them moves above it.
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void wait_ld(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+        "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+        "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+        "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16, "columns");
+  if (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[N - 8]),
+        "r"(r[N - 7]), "r"(r[N - 6]), "r"(r[N - 5]), "r"(r[N - 4]), "r"(r[N - 3]), "r"(r[N - 2]), "r"(r[N - 1]));
 }
 
 // Instruction descriptor of kind::f8f6f4: float32 accumulator, A E4M3 (0) or
@@ -311,14 +332,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
   }
 }
 
-// 32 lanes x 8 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
-
 // Two float32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
@@ -366,14 +379,17 @@ struct Cfg {
   static constexpr int kQTerms = E4M3 ? (BF16 ? 2 : 3) : 1;
   static constexpr int kPTerms = E4M3 ? (BF16 ? 3 : 4) : 1;
   static constexpr int kQTile = kMT * kRow * kQTerms;
-  static constexpr float kHeadroom = E4M3 ? 4.0f : 8.0f;   // growth of a reference (log2) before O is rescaled
+  // Growth of a row's reference (log2) before O is rescaled: as much as the
+  // weights' type holds beside the factors on them (fp16 to 2^15; a bf16 has
+  // float32's exponents, so there only sums must stay finite).
+  static constexpr float kHeadroom = E4M3 ? 6.0f : BF16 ? 60.0f : 15.0f;
   // Operand layouts.  A row of K or Q is kRow bytes cut into spans of at most
   // 128; a span of all rows is one swizzled tile (128-byte swizzle, or 64 for
   // 64-byte rows), spans kKT x span bytes apart.
   static constexpr int kSpan = kRow < 128 ? kRow : 128;
   static constexpr int kStepsPerSpan = kSpan / 32;         // an MMA takes 32 bytes of K and Q
   static constexpr int kQkSteps = kRow / 32;
-  static constexpr int kPvSteps = E4M3 ? kKT / 32 : kKT / 16;  // keys per MMA: 32 codes, 16 halves
+  static constexpr int kPvSteps = E4M3 ? kHK / 32 : kHK / 16;  // keys per MMA: 32 codes, 16 halves
   static constexpr int kVStep = (E4M3 ? 32 : 16) * kSpan;      // bytes of V to the next MMA's keys
   // Column of the weights of MMA kk (and term) in S: the weights of 32 keys lie
   // in the 32 columns that held those keys' scores.
@@ -382,7 +398,7 @@ struct Cfg {
   }
   static constexpr uint32_t kDescHi = (uint32_t)((8 * kSpan) >> 4) | (1u << 14) | ((kSpan == 64 ? 4u : 2u) << 29);
   static constexpr uint32_t kVDescLo = (uint32_t)((kKT * kSpan) >> 4) << 16;  // next span of V along N
-  static constexpr uint32_t kIdQk = E4M3 ? idesc_f8(kMT, kKT, 0) : idesc_f32acc(kMT, kKT, BF16);
+  static constexpr uint32_t kIdQk = E4M3 ? idesc_f8(kMT, kHK, 0) : idesc_f32acc(kMT, kHK, BF16);
   static constexpr uint32_t kIdPv = (E4M3 ? idesc_f8(kMT, HD, 1) : idesc_f32acc(kMT, HD, BF16)) | (1u << 16);  // V MN-major
 };
 
@@ -528,17 +544,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < k.slots; ++s) {
       mbar_init(&c->full[s], 1);
-      mbar_init(&c->empty[s], 1);
+      mbar_init(&c->empty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c->s_full[i], 1);
-      mbar_init(&c->p_full[i], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&c->s_full[i][h], 1);
+        mbar_init(&c->p_full[i][h], 4);
+        mbar_init(&c->pv_done[i][h], 1);
+      }
       mbar_init(&c->q_full[i], 1);
     }
-    mbar_init(&c->o_full, 1);
-    mbar_init(&c->fix, 1);
-    mbar_init(&c->fixed, 2);
-    mbar_init(&c->fin, 1);
+    mbar_init(&c->o_full, 2);
+    mbar_init(&c->fin, 2);
     c->abort_flag = 0;
     fence_barrier_init();
   }
@@ -618,125 +635,133 @@ __global__ void __launch_bounds__(kThreads, 1)
           (void)mbar_wait_bounded(&c->full[j % ring], (uint32_t)(j / ring) & 1u, &dummy, nullptr, 100000000ull);
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // -------------------------------------------------------- MMA issuer
+    } else if (warp < 3) {
+      // ------------------------------------------ MMA issuer of one stream
+      // A wait costs hundreds of clocks even when its phase is long complete
+      // (the operand reads of the tensor cores keep shared memory busy), so
+      // each stream has a warp of its own, and K and V are waited for before
+      // P: after it the products follow one another without a wait.
+      const int st = warp - 1;
       const bool lead = elect_one();
       const uint32_t ring_d = smem_u32(ring_s) >> 4, q_d = smem_u32(q_s) >> 4;
       constexpr uint32_t kTileD = C::kTile >> 4;
-      uint32_t seg = 0, fixes = 0, p_phase[2] = {0, 0};
-      int kslot = 0;              // slot of the next K tile; its V tile is in the next one
-      uint32_t kphase = 0;
+      const uint32_t tS = tmem + st * kKT, tO = tmem + kColO + st * 128;
+      constexpr uint32_t kHalfD = (kHK * C::kSpan) >> 4;  // a tile's second half of K or V rows
+      uint32_t seg = 0, p_phase = 0;
+      int base = 0;  // slot of the segment's first K tile; its V tile is in the next slot
+      uint32_t base_phase = 0;
       bool ok = true;
       while (true) {
-        ok = warp_wait_on(&c->q_full[0], seg & 1u, stop, a.status) && warp_wait_on(&c->q_full[1], seg & 1u, stop, a.status);
+        ok = warp_wait_on(&c->q_full[0], seg & 1u, stop, a.status) &&
+             warp_wait_on(&c->q_full[1], seg & 1u, stop, a.status);
         ++seg;
-        if (!ok || !c->more[0]) break;
-        // the segment as warpgroup 0 described it (it stays until o_full)
-        const bool split = c->seg[0].split;
-        const int nt = c->seg[0].nt, t0 = c->seg[0].t0, lo = c->seg[0].it.lo, hi = c->seg[0].it.hi;
-        const int jobs = split ? nt : 2 * nt;
-        // K of job j + 2 comes two tiles (a split item) or one after job j's:
-        // kslot walks over the K tiles, vslot over the V tiles
-        int vslot = kslot + 1 == k.slots ? 0 : kslot + 1;
-        uint32_t vphase = kslot + 1 == k.slots ? kphase ^ 1u : kphase;
-        auto step2 = [&](int& slot, uint32_t& phase) {
-          slot += 2;
-          if (slot >= k.slots) {
+        if (!ok || !c->more[st]) break;
+        // the segment as this stream's warpgroup described it (it stays until o_full)
+        const bool split = c->seg[st].split;
+        const int nt = c->seg[st].nt, lo = c->seg[st].it.lo, hi = c->seg[st].it.hi;
+        const int stride = split ? 2 : 1, first = split ? st : 0;
+        int k0 = (c->seg[st].t0 + first) * kKT;  // first key of the job
+        auto advance = [&](int& slot, uint32_t& phase, int n) {
+          slot += n;
+          while (slot >= k.slots) {
             slot -= k.slots;
             phase ^= 1u;
           }
         };
-        tc_fence_after();
-        auto qk = [&](int st) {
-          if (split || st == 0) {
-            ok = ok && warp_wait_on(&c->full[kslot], kphase, stop, a.status);
-            tc_fence_after();
-          }
-          const uint32_t kd = ring_d + kslot * kTileD, qd = q_d + (split ? 0u : (uint32_t)st * (C::kQTile >> 4));
+        int ks = base, vs;
+        uint32_t kp = base_phase, vp;
+        advance(ks, kp, 2 * first);
+        vs = ks;
+        vp = kp;
+        advance(vs, vp, 1);
+        const uint32_t qd = q_d + (split ? 0u : (uint32_t)st * (C::kQTile >> 4)) + (1u << 16);
+        // every slot is given back twice: by both streams, or twice by one
+        auto give_back = [&](int slot) {
+          tc_commit(&c->empty[slot]);
+          if (split) mbar_arrive(&c->empty[slot]);
+        };
+        auto qk = [&](int h) {
+          const uint32_t kd = ring_d + ks * kTileD + h * kHalfD + (1u << 16);
           if (lead) {
 #pragma unroll
             for (int term = 0; term < C::kQTerms; ++term)
 #pragma unroll
               for (int kk = 0; kk < C::kQkSteps; ++kk) {
                 const uint32_t off = (kk / C::kStepsPerSpan) * ((kKT * C::kSpan) >> 4) + (kk % C::kStepsPerSpan) * 2;
-                mma_ss<E4M3>(tmem + st * kKT, desc64(qd + term * ((kMT * C::kRow) >> 4) + off + (1u << 16), C::kDescHi),
-                             desc64(kd + off + (1u << 16), C::kDescHi), C::kIdQk, term > 0 || kk > 0);
+                mma_ss<E4M3>(tS + h * kHK, desc64(qd + term * ((kMT * C::kRow) >> 4) + off, C::kDescHi),
+                             desc64(kd + off, C::kDescHi), C::kIdQk, term > 0 || kk > 0);
               }
-            tc_commit(&c->s_full[st]);
-            if (split || st == 1) tc_commit(&c->empty[kslot]);
+            tc_commit(&c->s_full[st][h]);
+            if (h) give_back(ks);
           }
           __syncwarp();
-          if (split || st == 1) step2(kslot, kphase);
+          if (h) advance(ks, kp, 2 * stride);
         };
-        if (ok && jobs > 0) qk(0);
-        if (ok && jobs > 1) qk(1);
-        for (int j = 0; ok && j < jobs; ++j) {
-          const int st = j & 1;
-          bool edge = false;  // V rows of the tile are out of sight: have them zeroed
-          if (split || st == 0) {
-            ok = warp_wait_on(&c->full[vslot], vphase, stop, a.status);
-            const int k0 = (t0 + (split ? j : j >> 1)) * kKT;
-            edge = k0 < lo || k0 + kKT > hi;
-            if (edge && lead) {
-              c->fix_slot = vslot;
-              c->fix_lo = lo - k0;
-              c->fix_hi = hi - k0;
-              mbar_arrive(&c->fix);
+        tc_fence_after();
+        if (first < nt) {
+          ok = warp_wait_on(&c->full[ks], kp, stop, a.status);
+          tc_fence_after();
+          if (ok) {
+            qk(0);
+            qk(1);
+          }
+        }
+        for (int t = first; ok && t < nt; t += stride, k0 += stride * kKT) {
+          ok = warp_wait_on(&c->full[vs], vp, stop, a.status);
+          if (k0 < lo || k0 + kKT > hi) {
+            // V rows that no row of the item sees
+            uint4* v = reinterpret_cast<uint4*>(ring_s + vs * C::kTile);
+            for (int idx = lane; idx < kKT * (C::kRow / 16); idx += 32) {
+              const int key = k0 + (idx / (C::kSpan / 16)) % kKT;  // a row of a span: all its chunks, whatever the swizzle
+              if (key < lo || key >= hi) v[idx] = make_uint4(0u, 0u, 0u, 0u);
             }
+            fence_proxy_async_smem();
             __syncwarp();
           }
-          ok = ok && warp_wait_on(&c->p_full[st], p_phase[st], stop, a.status);
-          p_phase[st] ^= 1u;
-          if (edge) {
-            ok = ok && warp_wait_on(&c->fixed, fixes & 1u, stop, a.status);
-            ++fixes;
-          }
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t vd = ring_d + vslot * kTileD + C::kVDescLo;
-          const uint32_t fresh = j < 2;  // the stream's first job
-          if (lead) {
+          const bool more = t + stride < nt;
+          const uint32_t vd = ring_d + vs * kTileD + C::kVDescLo;
 #pragma unroll
-            for (int term = 0; term < C::kPTerms; ++term)
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && warp_wait_on(&c->p_full[st][h], p_phase, stop, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+              const uint32_t keep = t > first || h > 0;  // O holds earlier jobs
 #pragma unroll
               for (int kk = 0; kk < C::kPvSteps; ++kk)
-                mma_ts<E4M3>(tmem + kColO + st * 128, tmem + st * kKT + C::p_col(term, kk),
-                             desc64(vd + kk * (C::kVStep >> 4), C::kDescHi), C::kIdPv,
-                             (term > 0 || kk > 0) ? 1u : fresh ^ 1u);
-            if (split || st == 1) tc_commit(&c->empty[vslot]);
+#pragma unroll
+                for (int term = 0; term < C::kPTerms; ++term)
+                  mma_ts<E4M3>(tO, tS + h * kHK + C::p_col(term, kk),
+                               desc64(vd + h * kHalfD + kk * (C::kVStep >> 4), C::kDescHi), C::kIdPv,
+                               (term > 0 || kk > 0) ? 1u : keep);
+              tc_commit(&c->pv_done[st][h]);
+              if (h) give_back(vs);
+            }
+            __syncwarp();
+            // P of a job overwrites its S: the half's next scores follow its
+            // P V in the tensor pipe's order
+            if (more) {
+              if (h == 0) {
+                ok = warp_wait_on(&c->full[ks], kp, stop, a.status);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              qk(h);
+            }
           }
-          __syncwarp();
-          if (split || st == 1) step2(vslot, vphase);
-          // P of a job overwrites its S: the next scores of the stream follow
-          // its P V in the tensor pipe's order
-          if (j + 2 < jobs) qk(st);
+          if (!ok) break;
+          p_phase ^= 1u;
+          advance(vs, vp, 2 * stride);
         }
         if (!ok) break;
         if (lead) tc_commit(&c->o_full);
         __syncwarp();
+        const int n = base + 2 * nt;
+        base = n % k.slots;
+        base_phase ^= (uint32_t)(n / k.slots) & 1u;
       }
-      if (lead) {
-        c->fix_slot = -1;
-        mbar_arrive(&c->fix);
-        tc_commit(&c->fin);  // every MMA this thread issued
-      }
+      if (lead) tc_commit(&c->fin);  // every MMA this thread issued
       __syncwarp();
-    } else {
-      // ------------------------------------------------ V rows out of sight
-      const int ct = tid - 64;  // 0..63
-      uint32_t fixes = 0;
-      while (warp_wait_on(&c->fix, fixes++ & 1u, stop, a.status)) {
-        const int slot = c->fix_slot, v0 = c->fix_lo, v1 = c->fix_hi;
-        if (slot < 0) break;
-        uint8_t* v = ring_s + slot * C::kTile;
-        for (int idx = ct; idx < kKT * (C::kRow / 16); idx += 64) {
-          const int row = (idx / (C::kSpan / 16)) % kKT;  // a row of a span: all its chunks, whatever the swizzle
-          if (row < v0 || row >= v1) reinterpret_cast<uint4*>(v)[idx] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->fixed);
-      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -744,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + wg * kKT, tO = tmem + lane_off + kColO;
     float* x = c->x[wg];
-    uint32_t jobs = 0, seg = 0;
+    uint32_t tiles = 0, seg = 0;
     if (t == 0) {
       c->walk[wg].begin(k, c->start, w1 - w0);
       if (wg == 0) k.rec[cta].pair = -1;
@@ -815,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) c->vmax[wg][warp & 3] = wm;
           named_sync(1 + wg, 128);
           const float vm = fmaxf(fmaxf(c->vmax[wg][0], c->vmax[wg][1]), fmaxf(c->vmax[wg][2], c->vmax[wg][3]));
-          if (vm > 8.0f * vref || vref == 0.0f) {
+          if (vm > 2.0f * vref || vref == 0.0f) {
             const float nv = fmaxf(vm, 0x1p-60f);
             fv = vref / nv;
             vref = nv;
@@ -823,134 +848,127 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j + step < nt) fetch(t0 + j + step);
         }
-        (void)warp_wait_on(&c->s_full[wg], jobs++ & 1u, stop, a.status);
-        tc_fence_after();
-        if (!live) {
-          // no query row in this warp's lanes: whatever their P holds only
-          // reaches lanes of O that nobody reads
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c->p_full[wg]);
-          continue;
-        }
-        const int k0 = (t0 + j) * kKT;
-        const bool edge = !__all_sync(0xffffffffu, k0 >= lo && k0 + kKT <= hi);
-        const int e0 = lo - k0, e1 = hi - k0;  // visible: e0 <= e < e1
-        // the scores of 32 keys from column 32 q on, scaled and masked
-        auto ready = [&](int q, float (&v)[32]) {
-          if (E4M3) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(x + q * 32 + e);
-              const float2 a0 = mul2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y));
-              const float2 a1 = mul2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w));
-              v[e] = a0.x;
-              v[e + 1] = a0.y;
-              v[e + 2] = a1.x;
-              v[e + 3] = a1.y;
-            }
-          }
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (q * 32 + e < e0 || q * 32 + e >= e1) v[e] = -INFINITY;
-          }
-        };
-        // ---- the row's largest score; the scores stay in tensor memory, so
-        // that the code of a pass is short and the registers few
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const uint32_t phase = tiles++ & 1u;
 #pragma unroll 1
-        for (int q = 0; q < 4; q += 2) {
+        for (int h = 0; h < 2; ++h) {
+          (void)warp_wait_on(&c->s_full[wg][h], phase, stop, a.status);
+          tc_fence_after();
+          if (!live) {
+            // no query row in this warp's lanes: whatever their P holds only
+            // reaches lanes of O that nobody reads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->p_full[wg][h]);
+            continue;
+          }
+          const uint32_t ta = tS + h * kHK;
           float v0[32], v1[32];
-          tmem_ld_x32(tS + q * 32, v0);
-          tmem_ld_x32(tS + q * 32 + 32, v1);
-          tc_wait_ld();
-          ready(q, v0);
-          ready(q + 1, v1);
+          tmem_ld_x32(ta, v0);
+          tmem_ld_x32(ta + 32, v1);
+          const int k0 = (t0 + j) * kKT + h * kHK;
+          const bool edge = !__all_sync(0xffffffffu, k0 >= lo && k0 + kHK <= hi);
+          const int e0 = lo - k0, e1 = hi - k0;  // visible: e0 <= e < e1
+          // the scores of 32 keys, scaled and masked
+          auto ready = [&](int q, float (&v)[32]) {
+            if (E4M3) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(x + h * kHK + q * 32 + e);
+                const float2 a0 = mul2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y));
+                const float2 a1 = mul2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w));
+                v[e] = a0.x;
+                v[e + 1] = a0.y;
+                v[e + 2] = a1.x;
+                v[e + 3] = a1.y;
+              }
+            }
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (q * 32 + e < e0 || q * 32 + e >= e1) v[e] = -INFINITY;
+            }
+          };
+          wait_ld(v0);
+          wait_ld(v1);
+          ready(0, v0);
+          ready(1, v1);
+          // ---- the row's largest score
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(v0[e + i], v1[e + i]));
           }
-        }
-        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
-        const bool grow = m_tile > m_ref + C::kHeadroom || (m_ref == -INFINITY && m_tile > -INFINITY);
-        if (__any_sync(0xffffffffu, grow || fv != 1.0f)) {
-          const float m_new = grow ? m_tile : m_ref;
-          const float fo = (grow ? ex2_approx(m_ref - m_new) : 1.0f) * fv;  // 0 while nothing was seen
-          if (j > j0) {
-            // O holds the stream's earlier jobs: their P V precede these
-            // scores in the tensor pipe, the next one waits for this P
-            uint32_t r[16];
+          const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
+          const bool grow = m_tile > m_ref + C::kHeadroom || (m_ref == -INFINITY && m_tile > -INFINITY);
+          if (__any_sync(0xffffffffu, grow || fv != 1.0f)) {
+            const float m_new = grow ? m_tile : m_ref;
+            const float fo = (grow ? ex2_approx(m_ref - m_new) : 1.0f) * fv;  // 0 while nothing was seen
+            if (j > j0 || h) {
+              // O holds the stream's earlier jobs: wait for the last one's
+              // P V; the next one waits for this P
+              (void)warp_wait_on(&c->pv_done[wg][h ^ 1], h ? phase : phase ^ 1u, stop, a.status);
+              tc_fence_after();
+              uint32_t r[16];
 #pragma unroll 1
-            for (int i = 0; i < HD / 16; ++i) {
-              const uint32_t oa = tO + wg * 128 + i * 16;
-              tmem_ld_x16(oa, r);
-              tc_wait_ld();
+              for (int i = 0; i < HD / 16; ++i) {
+                const uint32_t oa = tO + wg * 128 + i * 16;
+                tmem_ld_x16(oa, r);
+                tc_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fo);
-              tmem_st_x16(oa, r);
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fo);
+                tmem_st_x16(oa, r);
+              }
             }
+            l *= fo;
+            m_ref = m_new;
+            fv = 1.0f;
           }
-          l *= fo;
-          m_ref = m_new;
+          // ---- weights 2^(z - m_ref + cv); l and O carry the factor, too
+          const float nb = m_ref == -INFINITY ? 0.0f : cv - m_ref;
+          const float2 cs2 = make_float2(cs, cs), nb2 = make_float2(nb, nb);
+          float2 ls0 = make_float2(0.0f, 0.0f), ls1 = ls0;
+          auto weigh = [&](int q, const float (&v)[32]) {
+            uint32_t pw[16];  // 16-bit weights of 32 keys
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float2 p0 = fma2(make_float2(v[e], v[e + 1]), cs2, nb2), p1 = fma2(make_float2(v[e + 2], v[e + 3]), cs2, nb2);
+              p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
+              p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
+              ls0 = add2(ls0, p0);
+              ls1 = add2(ls1, p1);
+              if (E4M3) {
+                const float4 f = *reinterpret_cast<const float4*>(x + 128 + h * kHK + q * 32 + e);
+                p0 = mul2(p0, make_float2(f.x, f.y));
+                p1 = mul2(p1, make_float2(f.z, f.w));
+              }
+              pw[e / 2] = pack16<!E4M3 && BF16>(p0.x, p0.y);
+              pw[e / 2 + 1] = pack16<!E4M3 && BF16>(p1.x, p1.y);
+            }
+            if (!E4M3) {
+              tmem_st(ta + q * 32, pw);
+            } else {
+              // three terms keep 9 bits: round there first (positive values)
+              if (C::kPTerms == 3) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pw[e] += 0x00020002u;
+              }
+#pragma unroll
+              for (int term = 0; term < C::kPTerms; ++term) {
+                uint32_t b[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[e] = take_e5m2(pw[2 * e], pw[2 * e + 1]);
+                tmem_st(ta + q * 32 + term * 8, b);
+              }
+            }
+          };
+          weigh(0, v0);
+          weigh(1, v1);
+          l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->p_full[wg][h]);
         }
-        // ---- weights 2^(z - m_ref + cv); l and O carry the factor, too
-        const float nb = m_ref == -INFINITY ? 0.0f : cv - m_ref;
-        const float2 cs2 = make_float2(cs, cs), nb2 = make_float2(nb, nb);
-        float2 ls0 = make_float2(0.0f, 0.0f), ls1 = ls0;
-        auto weigh = [&](int q, float (&v)[32]) {
-          ready(q, v);
-          uint32_t pw[16];  // 16-bit weights of 32 keys
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float2 p0 = fma2(make_float2(v[e], v[e + 1]), cs2, nb2), p1 = fma2(make_float2(v[e + 2], v[e + 3]), cs2, nb2);
-            p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
-            p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
-            ls0 = add2(ls0, p0);
-            ls1 = add2(ls1, p1);
-            if (E4M3) {
-              const float4 f = *reinterpret_cast<const float4*>(x + 128 + q * 32 + e);
-              p0 = mul2(p0, make_float2(f.x, f.y));
-              p1 = mul2(p1, make_float2(f.z, f.w));
-            }
-            pw[e / 2] = pack16<!E4M3 && BF16>(p0.x, p0.y);
-            pw[e / 2 + 1] = pack16<!E4M3 && BF16>(p1.x, p1.y);
-          }
-          if (!E4M3) {
-            tmem_st_x16(tS + q * 32, pw);
-          } else {
-            // three terms keep 9 bits: round there first (positive values)
-            if (C::kPTerms == 3) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) pw[e] += 0x00020002u;
-            }
-#pragma unroll
-            for (int term = 0; term < C::kPTerms; ++term) {
-              uint32_t b[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) b[e] = take_e5m2(pw[2 * e], pw[2 * e + 1]);
-              tmem_st_x8(tS + q * 32 + term * 8, b);
-            }
-          }
-        };
-        {
-          float v0[32], v1[32];
-          tmem_ld_x32(tS, v0);
-#pragma unroll 1
-          for (int q = 0; q < 4; q += 2) {
-            tc_wait_ld();
-            tmem_ld_x32(tS + q * 32 + 32, v1);
-            weigh(q, v0);
-            tc_wait_ld();
-            if (q == 0) tmem_ld_x32(tS + 64, v0);
-            weigh(q + 1, v1);
-          }
-        }
-        l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->p_full[wg]);
       }
 
       // ---- end of the segment: O is final
