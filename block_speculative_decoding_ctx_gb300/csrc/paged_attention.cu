@@ -21,7 +21,12 @@
 //     (each K/V byte feeds 256 rows);
 //   a smaller one: even and odd key tiles of its one Q tile, joined at the end.
 // Roles (384 threads):
-//   warp 0      page table and TMA: K and V tiles into a ring of slots
+//   warp 0      page table and TMA: K and V tiles into two rings of slots, for an
+//               item of two Q tiles one of K and one of V tiles, for a smaller
+//               one a ring per stream: whoever reads a ring waits for every
+//               phase of its barriers in turn.  (One ring for both streams of a
+//               smaller item would not do: loads may land out of order, and a
+//               wait whose previous phase is still open returns at once.)
 //   warps 1, 2  issue their stream's S = Q K^T (both from shared memory) and
 //               O += P V (P from tensor memory, V MN-major as TMA left it), and
 //               zero the V rows that no row of the item sees (a weight of 0
@@ -88,7 +93,7 @@ struct KernelArgs {
   Rec* rec;       // [CTA]
   int rts;        // items per request at most
   int part_rows;  // 128 or 256
-  int slots;      // of the K/V ring
+  int half;       // slots of each of the two rings
   int q_tiles;    // Q tiles in shared memory
 };
 
@@ -234,6 +239,18 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
       return false;
     }
   }
+}
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   const bool ok = wait_on(bar, parity, abort_flag, status);
@@ -488,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const PagedAttnArgs& a = k.a;
   uint8_t* ring_s = smem;
-  uint8_t* q_s = ring_s + k.slots * C::kTile;
+  uint8_t* q_s = ring_s + 2 * k.half * C::kTile;
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + kSmem - kCtrlBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023) {  // the swizzled tiles want 1024-byte atoms
@@ -542,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (tid == 0) {
-    for (int s = 0; s < k.slots; ++s) {
+    for (int s = 0; s < 2 * k.half; ++s) {
       mbar_init(&c->full[s], 1);
       mbar_init(&c->empty[s], 2);
     }
@@ -579,9 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmV);
       }
       const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
-      const int ring = k.slots;
-      int slot = 0, issued = 0;
-      uint32_t phase = 0;
+      int at0 = 0, at1 = 0;  // next slot of either ring
+      uint32_t ph0 = 0, ph1 = 0, used = 0, parity = 0;  // per slot: in use, phase of its last load
       bool ok = true;
       while (ok && walk.next(k, &s)) {
         const int32_t* table = a.batch.table + s.it.b * a.batch.table_stride;
@@ -605,7 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           for (int side = 0; side < 2; ++side) {
             bool got = true;
-            if (lane == 0) got = wait_on(&c->empty[slot], phase ^ 1u, stop, a.status);
+            const int r = s.split ? (t - s.t0) & 1 : side;
+            const int slot = r ? k.half + at1 : at0;
+            const uint32_t ph = r ? ph1 : ph0;
+            if (lane == 0) got = wait_on(&c->empty[slot], ph ^ 1u, stop, a.status);
             ok = __shfl_sync(0xffffffffu, got, 0);
             if (!ok) break;
             uint8_t* dst = ring_s + slot * C::kTile;
@@ -620,10 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tma_load_3d(dst + (h * kKT + row) * C::kSpan, map, &c->full[slot], h * 64, s.head * page_rows, id);
               }
             }
-            ++issued;
-            if (++slot == ring) {
-              slot = 0;
-              phase ^= 1u;
+            used |= 1u << slot;
+            parity = (parity & ~(1u << slot)) | (ph << slot);
+            const int next = (r ? at1 : at0) + 1;
+            const uint32_t wrap = next == k.half;
+            if (r) {
+              at1 = wrap ? 0 : next;
+              ph1 ^= wrap;
+            } else {
+              at0 = wrap ? 0 : next;
+              ph0 ^= wrap;
             }
           }
         }
@@ -631,8 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) {
         // a wait gave up: let the copies in flight land before the CTA leaves
         int dummy = 0;
-        for (int j = issued > ring ? issued - ring : 0; j < issued; ++j)
-          (void)mbar_wait_bounded(&c->full[j % ring], (uint32_t)(j / ring) & 1u, &dummy, nullptr, 100000000ull);
+        for (int j = 0; j < 2 * k.half; ++j)
+          if ((used >> j) & 1u) (void)mbar_wait_bounded(&c->full[j], (parity >> j) & 1u, &dummy, nullptr, 100000000ull);
       }
       __syncwarp();
     } else if (warp < 3) {
@@ -643,13 +668,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P: after it the products follow one another without a wait.
       const int st = warp - 1;
       const bool lead = elect_one();
-      const uint32_t ring_d = smem_u32(ring_s) >> 4, q_d = smem_u32(q_s) >> 4;
+      const uint32_t q_d = smem_u32(q_s) >> 4;
       constexpr uint32_t kTileD = C::kTile >> 4;
       const uint32_t tS = tmem + st * kKT, tO = tmem + kColO + st * 128;
       constexpr uint32_t kHalfD = (kHK * C::kSpan) >> 4;  // a tile's second half of K or V rows
       uint32_t seg = 0, p_phase = 0;
-      int base = 0;  // slot of the segment's first K tile; its V tile is in the next slot
-      uint32_t base_phase = 0;
+      int at0 = 0, at1 = 0;  // first slot of the segment in either ring
+      uint32_t ph0 = 0, ph1 = 0;
       bool ok = true;
       while (true) {
         ok = warp_wait_on(&c->q_full[0], seg & 1u, stop, a.status) &&
@@ -661,27 +686,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = c->seg[st].nt, lo = c->seg[st].it.lo, hi = c->seg[st].it.hi;
         const int stride = split ? 2 : 1, first = split ? st : 0;
         int k0 = (c->seg[st].t0 + first) * kKT;  // first key of the job
-        auto advance = [&](int& slot, uint32_t& phase, int n) {
-          slot += n;
-          while (slot >= k.slots) {
-            slot -= k.slots;
+        auto advance = [&](int& at, uint32_t& phase, int n) {
+          at += n;
+          if (at >= k.half) {
+            at -= k.half;
             phase ^= 1u;
           }
         };
-        int ks = base, vs;
-        uint32_t kp = base_phase, vp;
-        advance(ks, kp, 2 * first);
-        vs = ks;
-        vp = kp;
-        advance(vs, vp, 1);
+        // K and V slots: of the stream's own ring in turn, or of the K and the V ring
+        const bool kr = split && st, vr = !split || st;
+        uint8_t* const k_s = ring_s + (kr ? k.half * C::kTile : 0);
+        uint8_t* const v_s = ring_s + (vr ? k.half * C::kTile : 0);
+        uint64_t *const k_full = c->full + (kr ? k.half : 0), *const k_empty = c->empty + (kr ? k.half : 0);
+        uint64_t *const v_full = c->full + (vr ? k.half : 0), *const v_empty = c->empty + (vr ? k.half : 0);
+        const uint32_t k_d = smem_u32(k_s) >> 4, v_d = smem_u32(v_s) >> 4;
+        int ks = kr ? at1 : at0, vs = vr ? at1 : at0;
+        uint32_t kp = kr ? ph1 : ph0, vp = vr ? ph1 : ph0;
+        if (split) advance(vs, vp, 1);
         const uint32_t qd = q_d + (split ? 0u : (uint32_t)st * (C::kQTile >> 4)) + (1u << 16);
         // every slot is given back twice: by both streams, or twice by one
-        auto give_back = [&](int slot) {
-          tc_commit(&c->empty[slot]);
-          if (split) mbar_arrive(&c->empty[slot]);
+        auto give_back = [&](uint64_t* bar) {
+          tc_commit(bar);
+          if (split) mbar_arrive(bar);
         };
         auto qk = [&](int h) {
-          const uint32_t kd = ring_d + ks * kTileD + h * kHalfD + (1u << 16);
+          const uint32_t kd = k_d + ks * kTileD + h * kHalfD + (1u << 16);
           if (lead) {
 #pragma unroll
             for (int term = 0; term < C::kQTerms; ++term)
@@ -692,14 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                              desc64(kd + off, C::kDescHi), C::kIdQk, term > 0 || kk > 0);
               }
             tc_commit(&c->s_full[st][h]);
-            if (h) give_back(ks);
+            if (h) give_back(&k_empty[ks]);
           }
           __syncwarp();
-          if (h) advance(ks, kp, 2 * stride);
+          if (h) advance(ks, kp, stride);
         };
         tc_fence_after();
         if (first < nt) {
-          ok = warp_wait_on(&c->full[ks], kp, stop, a.status);
+          ok = warp_wait_on(&k_full[ks], kp, stop, a.status);
           tc_fence_after();
           if (ok) {
             qk(0);
@@ -707,10 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         for (int t = first; ok && t < nt; t += stride, k0 += stride * kKT) {
-          ok = warp_wait_on(&c->full[vs], vp, stop, a.status);
+          ok = warp_wait_on(&v_full[vs], vp, stop, a.status);
           if (k0 < lo || k0 + kKT > hi) {
             // V rows that no row of the item sees
-            uint4* v = reinterpret_cast<uint4*>(ring_s + vs * C::kTile);
+            uint4* v = reinterpret_cast<uint4*>(v_s + vs * C::kTile);
             for (int idx = lane; idx < kKT * (C::kRow / 16); idx += 32) {
               const int key = k0 + (idx / (C::kSpan / 16)) % kKT;  // a row of a span: all its chunks, whatever the swizzle
               if (key < lo || key >= hi) v[idx] = make_uint4(0u, 0u, 0u, 0u);
@@ -719,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           const bool more = t + stride < nt;
-          const uint32_t vd = ring_d + vs * kTileD + C::kVDescLo;
+          bool early = false;  // the next tile's first scores are on their way
+          const uint32_t vd = v_d + vs * kTileD + C::kVDescLo;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             ok = ok && warp_wait_on(&c->p_full[st][h], p_phase, stop, a.status);
@@ -735,30 +765,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                                desc64(vd + h * kHalfD + kk * (C::kVStep >> 4), C::kDescHi), C::kIdPv,
                                (term > 0 || kk > 0) ? 1u : keep);
               tc_commit(&c->pv_done[st][h]);
-              if (h) give_back(vs);
+              if (h) give_back(&v_empty[vs]);
             }
             __syncwarp();
             // P of a job overwrites its S: the half's next scores follow its
-            // P V in the tensor pipe's order
-            if (more) {
-              if (h == 0) {
-                ok = warp_wait_on(&c->full[ks], kp, stop, a.status);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              qk(h);
+            // P V in the tensor pipe's order.  If the next K tile is not there
+            // yet, this tile's second half goes first, so that V is given back
+            // (decoding, where the loads set the pace).
+            if (more && h == 0) early = __all_sync(0xffffffffu, mbar_test(&k_full[ks], kp));
+            if (more && h == 1 && !early) {
+              ok = warp_wait_on(&k_full[ks], kp, stop, a.status);
+              if (!ok) break;
             }
+            if (more && (h == 1 || early)) tc_fence_after();
+            if (more && ((h == 0) == early)) qk(0);
+            if (more && h == 1) qk(1);
           }
           if (!ok) break;
           p_phase ^= 1u;
-          advance(vs, vp, 2 * stride);
+          advance(vs, vp, stride);
         }
         if (!ok) break;
         if (lead) tc_commit(&c->o_full);
         __syncwarp();
-        const int n = base + 2 * nt;
-        base = n % k.slots;
-        base_phase ^= (uint32_t)(n / k.slots) & 1u;
+        const int n0 = at0 + (split ? 2 * ((nt + 1) / 2) : nt), n1 = at1 + (split ? 2 * (nt / 2) : nt);
+        at0 = n0 % k.half;
+        ph0 ^= (uint32_t)(n0 / k.half) & 1u;
+        at1 = n1 % k.half;
+        ph1 ^= (uint32_t)(n1 / k.half) & 1u;
       }
       if (lead) tc_commit(&c->fin);  // every MMA this thread issued
       __syncwarp();
@@ -1181,8 +1215,7 @@ int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   k.rts = (int)rts;
   k.part_rows = part_rows(a.group, a.max_rows);
   k.q_tiles = k.part_rows / kMT;
-  k.slots = (kSmem - kCtrlBytes - k.q_tiles * C::kQTile) / C::kTile;
-  if (k.slots > kMaxSlots) k.slots = kMaxSlots;
+  k.half = min(kMaxSlots, (kSmem - kCtrlBytes - k.q_tiles * C::kQTile) / C::kTile) / 2;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   if ((rc = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmem, s, tk, tv, k))) return rc;
   return launch_pdl(paged_join_kernel<HD, BF16>, dim3(grid, k.q_tiles * 8), dim3(256), 0, s, k);
