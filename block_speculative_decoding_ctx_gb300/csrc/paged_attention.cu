@@ -21,7 +21,7 @@
 //     (each K/V byte feeds 256 rows);
 //   a smaller one: even and odd key tiles of its one Q tile, joined at the end.
 // Roles (384 threads):
-//   warp 0      page table and TMA: K and V tiles into two rings of slots, for an
+//   warps 0, 3  page table and TMA: K and V tiles into two rings of slots, for an
 //               item of two Q tiles one of K and one of V tiles, for a smaller
 //               one a ring per stream: whoever reads a ring waits for every
 //               phase of its barriers in turn.  (One ring for both streams of a
@@ -586,81 +586,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = c->tmem;
   volatile int* stop = &c->abort_flag;
   if (warp < 4) {
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
+    if (warp == 0 || warp == 3) {
+      // -------------------------------------- producers: K (0) and V (3)
+      const int side = warp ? 1 : 0;
+      const bool lead = elect_one();
+      const void* map = side ? &tmV : &tmK;
       Walk walk;
       Seg s;
       walk.begin(k, c->start, w1 - w0);
-      if (lane == 0) {
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-      }
+      if (lead) tma_prefetch_desc(map);
       const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
-      int at0 = 0, at1 = 0;  // next slot of either ring
+      auto advance = [&](int& at, uint32_t& phase, int n) {
+        at += n;
+        if (at >= k.half) {
+          at -= k.half;
+          phase ^= 1u;
+        }
+      };
+      int at0 = 0, at1 = 0;  // first slot of the segment in either ring
       uint32_t ph0 = 0, ph1 = 0, used = 0, parity = 0;  // per slot: in use, phase of its last load
       bool ok = true;
       while (ok && walk.next(k, &s)) {
         const int32_t* table = a.batch.table + s.it.b * a.batch.table_stride;
-        int ids = 0, ids_at = -1;  // page ids of 32 pages from ids_at on, one per lane
+        const int g_lo = s.it.lo >> shift, g_hi = (s.it.hi - 1) >> shift;  // pages in sight
+        // ids of 32 pages, one per lane, and of the next 32
+        auto look_up = [&](int from) {
+          const int g = from + lane;
+          return g >= g_lo && g <= g_hi ? __ldg(table + g) : 0;
+        };
+        int ids_at = s.t0 * per_tile, ids = 0, ids_next = 0;
+        if (s.nt > 0) {
+          ids = look_up(ids_at);
+          ids_next = look_up(ids_at + 32);
+        }
+        int s0 = at0, s1 = at1;
+        uint32_t q0 = ph0, q1 = ph1;
+        if (s.split) {
+          advance(s0, q0, side);
+          advance(s1, q1, side);
+        }
         for (int t = s.t0; ok && t < s.t0 + s.nt; ++t) {
           const int first = t * per_tile;
           // pages of the tile that hold a visible position
-          const int g0 = max(first, s.it.lo >> shift), g1 = min(first + per_tile, ((s.it.hi - 1) >> shift) + 1);
-          if (ids_at < 0 || first + per_tile > ids_at + 32) {
-            ids_at = first;
-            const int g = first + lane;
-            int id = -1;
-            if (g >= (s.it.lo >> shift) && g <= (s.it.hi - 1) >> shift) {
-              id = __ldg(table + g);
-              if (id < 0 || id >= a.batch.n_pages) {
-                report_status(a.status, DFLASH_ERR_ARG);
-                id = a.batch.n_pages;  // outside the tensor: TMA fills zeros
-              }
-            }
-            ids = id;
+          const int g0 = max(first, g_lo), g1 = min(first + per_tile, g_hi + 1);
+          if (first + per_tile > ids_at + 32) {
+            ids_at += 32;
+            ids = ids_next;
+            ids_next = look_up(ids_at + 32);
           }
-          for (int side = 0; side < 2; ++side) {
-            bool got = true;
-            const int r = s.split ? (t - s.t0) & 1 : side;
-            const int slot = r ? k.half + at1 : at0;
-            const uint32_t ph = r ? ph1 : ph0;
-            if (lane == 0) got = wait_on(&c->empty[slot], ph ^ 1u, stop, a.status);
-            ok = __shfl_sync(0xffffffffu, got, 0);
-            if (!ok) break;
-            uint8_t* dst = ring_s + slot * C::kTile;
-            if (lane == 0) mbar_arrive_expect_tx(&c->full[slot], (uint32_t)((g1 - g0) << shift) * C::kRow);
-            for (int g = g0; g < g1; ++g) {
-              const int id = __shfl_sync(0xffffffffu, ids, g - ids_at);
-              if (lane == 0) {
-                const int row = (g - first) << shift;
-                const void* map = side ? &tmV : &tmK;
+          const int r = s.split ? (t - s.t0) & 1 : side;
+          const int slot = r ? k.half + s1 : s0;
+          const uint32_t ph = r ? q1 : q0;
+          ok = warp_wait_on(&c->empty[slot], ph ^ 1u, stop, a.status);
+          if (!ok) break;
+          uint8_t* dst = ring_s + slot * C::kTile;
+          if (lead) mbar_arrive_expect_tx(&c->full[slot], (uint32_t)((g1 - g0) << shift) * C::kRow);
+          for (int g = g0; g < g1; ++g) {
+            int id = __shfl_sync(0xffffffffu, ids, g - ids_at);
+            if (id < 0 || id >= a.batch.n_pages) {
+              if (lead) report_status(a.status, DFLASH_ERR_ARG);
+              id = a.batch.n_pages;  // outside the tensor: TMA fills zeros
+            }
+            if (lead) {
+              const int row = (g - first) << shift;
 #pragma unroll
-                for (int h = 0; h < C::kRow / C::kSpan; ++h)
-                  tma_load_3d(dst + (h * kKT + row) * C::kSpan, map, &c->full[slot], h * 64, s.head * page_rows, id);
-              }
-            }
-            used |= 1u << slot;
-            parity = (parity & ~(1u << slot)) | (ph << slot);
-            const int next = (r ? at1 : at0) + 1;
-            const uint32_t wrap = next == k.half;
-            if (r) {
-              at1 = wrap ? 0 : next;
-              ph1 ^= wrap;
-            } else {
-              at0 = wrap ? 0 : next;
-              ph0 ^= wrap;
+              for (int h = 0; h < C::kRow / C::kSpan; ++h)
+                tma_load_3d(dst + (h * kKT + row) * C::kSpan, map, &c->full[slot], h * 64, s.head * page_rows, id);
             }
           }
+          __syncwarp();
+          used |= 1u << slot;
+          parity = (parity & ~(1u << slot)) | (ph << slot);
+          if (r)
+            advance(s1, q1, s.split ? 2 : 1);
+          else
+            advance(s0, q0, s.split ? 2 : 1);
         }
+        const int n0 = at0 + (s.split ? 2 * ((s.nt + 1) / 2) : s.nt), n1 = at1 + (s.split ? 2 * (s.nt / 2) : s.nt);
+        at0 = n0 % k.half;
+        ph0 ^= (uint32_t)(n0 / k.half) & 1u;
+        at1 = n1 % k.half;
+        ph1 ^= (uint32_t)(n1 / k.half) & 1u;
       }
-      if (!ok && lane == 0) {
+      if (!ok && lead) {
         // a wait gave up: let the copies in flight land before the CTA leaves
         int dummy = 0;
         for (int j = 0; j < 2 * k.half; ++j)
           if ((used >> j) & 1u) (void)mbar_wait_bounded(&c->full[j], (parity >> j) & 1u, &dummy, nullptr, 100000000ull);
       }
       __syncwarp();
-    } else if (warp < 3) {
+    } else {
       // ------------------------------------------ MMA issuer of one stream
       // A wait costs hundreds of clocks even when its phase is long complete
       // (the operand reads of the tensor cores keep shared memory busy), so
@@ -850,20 +865,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.0f;
       float vref = 0.0f, cv = 0.0f;  // E4M3: reference of the value scales, log2 of the weights' factor
       const int step = s.split ? 2 : 1, j0 = s.split ? wg : 0, nt = s.nt, t0 = s.t0;
-      float nks = 0.0f, nvs = 0.0f;  // scales of key t of the next tile
-      auto fetch = [&](int tile) {
+      // E4M3: scales of key t of the next tile, and the page of the one after
+      // it, so that neither load is waited for in its own tile
+      float nks = 0.0f, nvs = 0.0f;
+      int page = -1;
+      auto look_up = [&](int tile) {
         const int key = tile * kKT + t;
+        page = -1;
+        if (key >= it.lo && key < it.hi)
+          page = __ldg(a.batch.table + it.b * a.batch.table_stride + (key >> a.batch.page_shift));
+      };
+      auto fetch = [&](int tile) {
+        const int at = (tile * kKT + t) & ((1 << a.batch.page_shift) - 1);
         nks = nvs = 0.0f;
-        if (key >= it.lo && key < it.hi) {
-          const int id = __ldg(a.batch.table + it.b * a.batch.table_stride + (key >> a.batch.page_shift));
-          if (id >= 0 && id < a.batch.n_pages) {
-            const size_t o = (((size_t)id * a.n_kv + s.head) << a.batch.page_shift) + (key & ((1 << a.batch.page_shift) - 1));
-            nks = __ldg(a.k_scale + o);
-            nvs = __ldg(a.v_scale + o);
-          }
+        if (page >= 0 && page < a.batch.n_pages) {
+          const size_t o = (((size_t)page * a.n_kv + s.head) << a.batch.page_shift) + at;
+          nks = __ldg(a.k_scale + o);
+          nvs = __ldg(a.v_scale + o);
         }
       };
-      if (E4M3 && j0 < nt) fetch(t0 + j0);
+      if (E4M3 && j0 < nt) {
+        look_up(t0 + j0);
+        fetch(t0 + j0);
+        look_up(t0 + j0 + step);
+      }
       for (int j = j0; j < nt; j += step) {
         float fv = 1.0f;  // E4M3: change of the value reference
         if (E4M3) {
@@ -880,7 +905,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             vref = nv;
             cv = kVShiftLog2 - log2f(vref);
           }
-          if (j + step < nt) fetch(t0 + j + step);
+          fetch(t0 + j + step);
+          look_up(t0 + j + 2 * step);
         }
         const uint32_t phase = tiles++ & 1u;
 #pragma unroll 1
