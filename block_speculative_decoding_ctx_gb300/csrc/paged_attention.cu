@@ -75,7 +75,6 @@ constexpr int kMT = 128;           // rows of a Q tile
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;      // the workspace has room for so many
 constexpr int kMaxSlots = 12;
-constexpr int kCtrlBytes = 3072;
 constexpr int kSmem = 227 * 1024;  // all that a CTA may have
 constexpr uint32_t kColO = 256;    // O of stream 0; S of stream s at 128 s
 constexpr float kLn2 = 0.693147180559945309f;
@@ -94,6 +93,7 @@ struct KernelArgs {
   int rts;        // items per request at most
   int part_rows;  // 128 or 256
   int half;       // slots of each of the two rings
+  int seg_cost;   // what beginning an item costs, in key tiles
   int q_tiles;    // Q tiles in shared memory
 };
 
@@ -104,14 +104,15 @@ struct Item {
   int row0, rows;        // packed rows
   int lo, hi;            // positions that some row sees
   int t_lo, tiles;       // key tiles
-  int units;             // length on the line: a CTA's turn for an empty item, too
+  int units;             // length on the line: the tiles and seg_cost for the rest, 1 for an empty item
 };
 
 __device__ __forceinline__ bool item_rows(const PagedAttnArgs& a, int b, RequestSpan* r) {
   return request_span(a.batch, b, r) && r->n <= a.max_rows;
 }
 
-__device__ __forceinline__ Item make_item(const PagedAttnArgs& a, const RequestSpan& r, int b, int rt) {
+__device__ __forceinline__ Item make_item(const KernelArgs& k, const RequestSpan& r, int b, int rt) {
+  const PagedAttnArgs& a = k.a;
   Item it;
   it.b = b;
   it.s0 = r.s0;
@@ -125,7 +126,7 @@ __device__ __forceinline__ Item make_item(const PagedAttnArgs& a, const RequestS
   it.lo = a.window ? max(0, p0 - a.window + 1) : 0;
   it.t_lo = it.lo / kKT;
   it.tiles = it.hi > it.lo ? (it.hi + kKT - 1) / kKT - it.t_lo : 0;
-  it.units = max(it.tiles, 1);
+  it.units = it.tiles ? it.tiles + k.seg_cost : 1;
   return it;
 }
 
@@ -136,7 +137,7 @@ __device__ __forceinline__ bool find_item(const KernelArgs& k, int* pair, int en
     const int b = *pair / k.rts, rt = *pair - b * k.rts;
     RequestSpan r;
     if (item_rows(k.a, b, &r) && rt * (2 * kMT) < r.n * k.a.group) {
-      *it = make_item(k.a, r, b, rt);
+      *it = make_item(k, r, b, rt);
       return true;
     }
     *pair = (b + 1) * k.rts;
@@ -153,7 +154,7 @@ struct Seg {
   bool first, last;
   int slot;        // partial slot
   int pair;
-  long long before;  // units of this CTA before it
+  long long end;   // where the item ends on the line, from the CTA's first unit on
 };
 
 struct Start {
@@ -175,49 +176,64 @@ struct Walk {
     off = (int)(st.off - (long long)head * it.units);
   }
   __device__ bool next(const KernelArgs& k, Seg* s) {
-    if (left <= 0) return false;
-    if (!loaded) {
-      if (!find_item(k, &pair, k.a.batch.B * k.rts, &it)) return false;
-      loaded = true;
+    while (left > 0) {
+      if (!loaded) {
+        if (!find_item(k, &pair, k.a.batch.B * k.rts, &it)) return false;
+        loaded = true;
+      }
+      // the item's first seg_cost units stand for its beginning and end; the
+      // CTA that holds its first tile does that work
+      const int skip = it.tiles ? k.seg_cost : 0;
+      const int take = (int)min(left, (long long)(it.units - off));
+      const int a0 = max(off - skip, 0), a1 = max(off + take - skip, 0);
+      const bool any = a1 > 0;
+      s->it = it;
+      s->head = head;
+      s->t0 = it.t_lo + a0;
+      s->nt = it.tiles ? a1 - a0 : 0;
+      s->split = it.rows <= kMT;
+      s->first = a0 == 0;
+      s->last = off + take == it.units;
+      s->slot = left == total ? 0 : 1;
+      s->pair = pair;
+      s->end = total - left - off + it.units;
+      left -= take;
+      off = 0;
+      if (++head == k.a.n_kv) {
+        head = 0;
+        ++pair;
+        loaded = false;
+      }
+      if (any) return true;
     }
-    const int take = (int)min(left, (long long)(it.units - off));
-    s->it = it;
-    s->head = head;
-    s->t0 = it.t_lo + off;
-    s->nt = max(0, min(take, it.tiles - off));
-    s->split = it.rows <= kMT;
-    s->first = off == 0;
-    s->last = off + take == it.units;
-    s->slot = left == total ? 0 : 1;
-    s->pair = pair;
-    s->before = total - left;
-    left -= take;
-    off = 0;
-    if (++head == k.a.n_kv) {
-      head = 0;
-      ++pair;
-      loaded = false;
-    }
-    return true;
+    return false;
   }
 };
 
+// E4M3 scales of a tile: this one's, the next one's, and the last one's that a
+// slower warp may still be reading.
+template <bool E4M3>
+constexpr int kScaleTurns = E4M3 ? 3 : 1;
+
+template <bool E4M3>
 struct Ctrl {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half of the key tile]
   uint64_t q_full[2], o_full, fin;
   Start start;
   Walk walk[2];  // of the softmax warpgroups: kept here, not in every thread's registers
-  Seg seg[2];
-  int more[2];
+  Seg seg[2][2];  // [warpgroup][turn]
+  int more[2][2];
   int abort_flag;
   uint32_t tmem;
-  float vmax[2][4];
+  alignas(16) float vmax[2][3][4];
   // per warpgroup: key and value scales; (m, l) of the join; row scales of Q.
   // Before the roles start: scratch of the scan
-  alignas(16) float x[2][256];
+  alignas(16) float x[2][kScaleTurns<E4M3> * 256];
 };
-static_assert(sizeof(Ctrl) <= kCtrlBytes && offsetof(Ctrl, x) % 16 == 0, "control block");
+template <bool E4M3>
+constexpr int kCtrlBytes = (int)((sizeof(Ctrl<E4M3>) + 1023) / 1024 * 1024);
+static_assert(kCtrlBytes<false> <= 3072, "control block: six 32 KiB slots beside one Q tile");
 
 // -------------------------------------------------------------- PTX helpers
 
@@ -423,12 +439,13 @@ struct Cfg {
 
 // Rows [row0, row0 + 128) of the item's packed rows, those of them in
 // [r_begin, r_end), into a swizzled tile by the 128 threads of a warpgroup;
-// rows past the item's are zero.  E4M3: as terms, the inverse of the row's
-// factor in row_scale.
+// rows past the item's keep what was there: it only reaches lanes that nobody
+// reads.  E4M3: as terms, the inverse of the row's factor in row_scale.
 template <int HD, bool E4M3, bool BF16>
 __device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, int head, int row0, uint8_t* q_s,
                                        float* row_scale, int t, int r_begin, int r_end) {
   constexpr int kCh = HD / 8;  // 16-byte chunks of a row
+  r_end = min(r_end, it.rows - row0);
   auto source = [&](int idx, bool* ok) {
     const int pr = row0 + idx / kCh;
     *ok = pr < it.rows;
@@ -441,7 +458,7 @@ __device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, i
       bool ok;
       const uint8_t* src = source(idx, &ok);
       const int r = idx / kCh, ch = idx % kCh;
-      cp_async16(q_s + (ch >> 3) * (kMT * 128) + swz(r, (ch & 7) * 8), src, ok);
+      cp_async16(q_s + (ch >> 3) * (kMT * 128) + swz(r, (ch & 7) * 8), src, true);
     }
     return;
   }
@@ -506,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PagedAttnArgs& a = k.a;
   uint8_t* ring_s = smem;
   uint8_t* q_s = ring_s + 2 * k.half * C::kTile;
-  Ctrl* c = reinterpret_cast<Ctrl*>(smem + kSmem - kCtrlBytes);
+  auto* c = reinterpret_cast<Ctrl<E4M3>*>(smem + kSmem - kCtrlBytes<E4M3>);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023) {  // the swizzled tiles want 1024-byte atoms
     if (tid == 0) {
@@ -531,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       continue;
     }
     const int items = (r.n * a.group + 2 * kMT - 1) / (2 * kMT);
-    for (; rt < items && p < p1; ++rt, ++p) mine += make_item(a, r, b, rt).units;
+    for (; rt < items && p < p1; ++rt, ++p) mine += make_item(k, r, b, rt).units;
     if (rt >= items) p = (b + 1) * k.rts;
   }
   unsigned long long total;
@@ -694,13 +711,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (true) {
         ok = warp_wait_on(&c->q_full[0], seg & 1u, stop, a.status) &&
              warp_wait_on(&c->q_full[1], seg & 1u, stop, a.status);
-        ++seg;
-        if (!ok || !c->more[st]) break;
         // the segment as this stream's warpgroup described it (it stays until o_full)
-        const bool split = c->seg[st].split;
-        const int nt = c->seg[st].nt, lo = c->seg[st].it.lo, hi = c->seg[st].it.hi;
+        const Seg& s = c->seg[st][seg & 1u];
+        if (!ok || !c->more[st][seg & 1u]) break;
+        ++seg;
+        const bool split = s.split;
+        const int nt = s.nt, lo = s.it.lo, hi = s.it.hi;
         const int stride = split ? 2 : 1, first = split ? st : 0;
-        int k0 = (c->seg[st].t0 + first) * kKT;  // first key of the job
+        int k0 = (s.t0 + first) * kKT;  // first key of the job
         auto advance = [&](int& at, uint32_t& phase, int n) {
           at += n;
           if (at >= k.half) {
@@ -817,50 +835,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = (warp >> 2) - 1, t = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + wg * kKT, tO = tmem + lane_off + kColO;
-    float* x = c->x[wg];
+    float* const x0 = c->x[wg];
     uint32_t tiles = 0, seg = 0;
+    // the next segment's description, a segment ahead
+    auto describe = [&](uint32_t turn) {
+      Seg* n = &c->seg[wg][turn & 1u];
+      const bool more = c->walk[wg].next(k, n);
+      c->more[wg][turn & 1u] = more;
+      if (wg == 0 && more && n->first && !n->last) {
+        const long long u = w0 + n->end - 1;  // the item's last unit
+        k.rec[cta] = Rec{n->pair, n->head, n->slot, (int)(((u + 1) * ctas - 1) / W)};
+      }
+    };
     if (t == 0) {
       c->walk[wg].begin(k, c->start, w1 - w0);
       if (wg == 0) k.rec[cta].pair = -1;
+      describe(0);
     }
-    while (true) {
-      named_sync(1 + wg, 128);  // the last segment's description has been read
-      if (t == 0) {
-        c->more[wg] = c->walk[wg].next(k, &c->seg[wg]);
-        const Seg& n = c->seg[wg];
-        if (wg == 0 && c->more[0] && n.first && !n.last) {
-          const long long u = w0 + n.before + n.it.units - 1;  // the item's last unit
-          k.rec[cta] = Rec{n.pair, n.head, n.slot, (int)(((u + 1) * ctas - 1) / W)};
-        }
-      }
+    for (;; ++seg) {
       named_sync(1 + wg, 128);
-      if (!c->more[wg]) {
+      if (!c->more[wg][seg & 1u]) {
         if (t == 0) mbar_arrive(&c->q_full[wg]);  // wakes the MMA warp, which sees the end too
         break;
       }
-      const Seg& s = c->seg[wg];
+      const Seg& s = c->seg[wg][seg & 1u];
       const Item& it = s.it;
       // ---- queries of this stream (a split item's one tile: half by each
       // warpgroup, or all by both where the row scales are needed by both)
       if (s.split) {
-        load_q<HD, E4M3, BF16>(a, it, s.head, 0, q_s, x, t, E4M3 ? 0 : 64 * wg, E4M3 ? kMT : 64 * wg + 64);
+        load_q<HD, E4M3, BF16>(a, it, s.head, 0, q_s, x0, t, E4M3 ? 0 : 64 * wg, E4M3 ? kMT : 64 * wg + 64);
       } else {
-        load_q<HD, E4M3, BF16>(a, it, s.head, kMT * wg, q_s + wg * C::kQTile, x, t, 0, kMT);
+        load_q<HD, E4M3, BF16>(a, it, s.head, kMT * wg, q_s + wg * C::kQTile, x0, t, 0, kMT);
       }
       if (!E4M3) cp_async_wait_all();
       fence_proxy_async_smem();
       named_sync(1 + wg, 128);
-      if (t == 0) mbar_arrive(&c->q_full[wg]);
+      if (t == 0) {
+        mbar_arrive(&c->q_full[wg]);
+        describe(seg + 1);
+      }
       const int pr = (s.split ? 0 : kMT * wg) + t;   // row of the item
       const bool real = pr < it.rows;
       const bool live = __any_sync(0xffffffffu, real);
       const int packed = it.row0 + (real ? pr : 0);
       const int tok = packed / a.group, g = packed - tok * a.group;
       const int pos = it.len - it.n + tok;
-      // rows past the item's see everything: their scores are zero
+      // rows past the item's do not ask for masking
       const int hi = !real ? 1 << 30 : a.causal ? min(it.len, pos + 1) : it.len;
       const int lo = real && a.window ? pos - a.window + 1 : -(1 << 30);
-      const float cs = a.scale_log2 * (E4M3 ? x[t] : 1.0f);
+      const float cs = real ? a.scale_log2 * (E4M3 ? x0[t] : 1.0f) : 0.0f;
 
       float m_ref = -INFINITY, l = 0.0f;
       float vref = 0.0f, cv = 0.0f;  // E4M3: reference of the value scales, log2 of the weights' factor
@@ -884,29 +907,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           nvs = __ldg(a.v_scale + o);
         }
       };
-      if (E4M3 && j0 < nt) {
+      // what was fetched into one of the buffers, and the largest value scale
+      // of each warp's keys
+      auto put = [&](int turn) {
+        x0[turn * 256 + t] = nks;
+        x0[turn * 256 + 128 + t] = nvs;
+        const float wm = warp_max_f(nvs);
+        if (lane == 0) c->vmax[wg][turn][warp & 3] = wm;
+      };
+      int turn = 0;
+      if (E4M3) {
         look_up(t0 + j0);
         fetch(t0 + j0);
         look_up(t0 + j0 + step);
+        named_sync(1 + wg, 128);  // the row scales of Q have been read from there
+        put(0);
+        fetch(t0 + j0 + step);
+        look_up(t0 + j0 + 2 * step);
       }
       for (int j = j0; j < nt; j += step) {
         float fv = 1.0f;  // E4M3: change of the value reference
+        const float* x = x0 + turn * 256;
         if (E4M3) {
-          named_sync(1 + wg, 128);  // the last job's scales have been read
-          x[t] = nks;
-          x[128 + t] = nvs;
-          const float wm = warp_max_f(nvs);
-          if (lane == 0) c->vmax[wg][warp & 3] = wm;
+          // the next tile's scales go where the last but one's were; after the
+          // barrier this tile's are there and nobody reads the last one's
+          const int next = turn == 2 ? 0 : turn + 1;
+          put(next);
+          fetch(t0 + j + 2 * step);
+          look_up(t0 + j + 3 * step);
           named_sync(1 + wg, 128);
-          const float vm = fmaxf(fmaxf(c->vmax[wg][0], c->vmax[wg][1]), fmaxf(c->vmax[wg][2], c->vmax[wg][3]));
+          const float4 vm4 = *reinterpret_cast<const float4*>(c->vmax[wg][turn]);
+          const float vm = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
           if (vm > 2.0f * vref || vref == 0.0f) {
             const float nv = fmaxf(vm, 0x1p-60f);
             fv = vref / nv;
             vref = nv;
             cv = kVShiftLog2 - log2f(vref);
           }
-          fetch(t0 + j + step);
-          look_up(t0 + j + 2 * step);
+          turn = next;
         }
         const uint32_t phase = tiles++ & 1u;
 #pragma unroll 1
@@ -968,15 +1006,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               // P V; the next one waits for this P
               (void)warp_wait_on(&c->pv_done[wg][h ^ 1], h ? phase : phase ^ 1u, stop, a.status);
               tc_fence_after();
-              uint32_t r[16];
 #pragma unroll 1
-              for (int i = 0; i < HD / 16; ++i) {
-                const uint32_t oa = tO + wg * 128 + i * 16;
-                tmem_ld_x16(oa, r);
-                tc_wait_ld();
+              for (int i = 0; i < HD / 32; ++i) {
+                const uint32_t oa = tO + wg * 128 + i * 32;
+                float o[32];
+                uint32_t r[16];
+                tmem_ld_x32(oa, o);
+                wait_ld(o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fo);
-                tmem_st_x16(oa, r);
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[q * 16 + e] * fo);
+                  tmem_st(oa + q * 16, r);
+                }
               }
             }
             l *= fo;
@@ -1032,15 +1074,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- end of the segment: O is final
-      (void)warp_wait_on(&c->o_full, seg++ & 1u, stop, a.status);
+      (void)warp_wait_on(&c->o_full, seg & 1u, stop, a.status);
       tc_fence_after();
       const bool whole = s.first && s.last;
       // factors of O0 and O1 (a row-split item: of its own O)
       float f0 = 1.0f, f1 = 0.0f, M = m_ref - cv, L = l;
       if (s.split) {
         named_sync(1 + wg, 128);  // scales are no longer read
-        x[t] = M;
-        x[128 + t] = l;
+        x0[t] = M;
+        x0[128 + t] = l;
         named_sync(3, 256);
         const float m0 = c->x[0][t], m1 = c->x[1][t];
         M = fmaxf(m0, m1);
@@ -1121,7 +1163,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const KernelArgs k) {
   const int b = rec.pair / k.rts;
   RequestSpan r;
   if (!item_rows(a, b, &r)) return;
-  const Item it = make_item(a, r, b, rec.pair - b * k.rts);
+  const Item it = make_item(k, r, b, rec.pair - b * k.rts);
   const int n = rec.last_cta - cta + 1;
   constexpr int kE = HD / 32;
   for (int row = w; row < it.rows; row += 8 * gridDim.y) {
@@ -1241,7 +1283,8 @@ int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   k.rts = (int)rts;
   k.part_rows = part_rows(a.group, a.max_rows);
   k.q_tiles = k.part_rows / kMT;
-  k.half = min(kMaxSlots, (kSmem - kCtrlBytes - k.q_tiles * C::kQTile) / C::kTile) / 2;
+  k.half = min(kMaxSlots, (kSmem - kCtrlBytes<E4M3> - k.q_tiles * C::kQTile) / C::kTile) / 2;
+  k.seg_cost = E4M3 ? 8 : 4;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   if ((rc = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmem, s, tk, tv, k))) return rc;
   return launch_pdl(paged_join_kernel<HD, BF16>, dim3(grid, k.q_tiles * 8), dim3(256), 0, s, k);
