@@ -11,6 +11,7 @@ There is no fallback: if the library is missing, every call raises.
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -373,32 +374,55 @@ def dflash_quantize_e4m3(w, codes, scales, stream=None):
 
 
 # ------------------------------------------------- the target's side of a cycle
+#
+# A decoding step makes these calls once a layer, so their argument marshalling
+# is kept short: host structs are packed bytes (laid out as the ctypes
+# structures above), addresses are plain integers.
+
+_PACK_ROWS = struct.Struct("@Pqq").pack
+_PACK_BATCH = struct.Struct("@PPPqiii4x").pack
+_PACK_RULES = struct.Struct("@PPPiPPPPPPPiP").pack
+
 
 class PagedCache:
     """One layer's paged cache (see paged_cache); keeps its tensors alive."""
 
-    def __init__(self, struct, keep):
-        self.struct = struct
-        self.device = keep[0].device
+    def __init__(self, fields, keep, index):
+        self.struct = fields
+        self.index = index
+        self._bytes = bytes(fields)
         self._keep = keep
+        self._rows = (fields.n_kv_heads, fields.head_dim)
 
 
-def _fit(name, t, dtype, shape, device):
-    """The tensor's address after checking its type, shape and device; it must
-    be contiguous.  None stays None."""
+def _misfit(name, t, dtype, shape, index):
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{index}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _fit(name, t, dtype, shape, index):
+    """The tensor's address if it is a contiguous one of this type, shape and
+    device; 0 for None."""
     if t is None:
-        return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+        return 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _misfit(name, t, dtype, shape, index)
 
 
-def _on_device(device):
-    if device.type != "cuda":
-        raise ValueError("expected a CUDA tensor")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+def _current(index, stream):
+    """The stream to launch on; the tensors' device must be the current one."""
+    if index < 0:
+        raise ValueError("expected CUDA tensors")
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _workspace(ws, index):
+    if ws.get_device() != index or not ws.is_contiguous() or ws.element_size() != 1:
+        raise ValueError(f"workspace: expected one of dfl.workspace on cuda:{index}")
+    return ws.data_ptr()
 
 
 def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None):
@@ -406,72 +430,77 @@ def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None):
     page_size, head_dim] of bfloat16, float16, or E4M3 codes (float8_e4m3fn or
     uint8) with float32 scales [n_pages, n_kv_heads, page_size].  A page is
     contiguous; pages may lie further apart (a slice of a larger tensor)."""
-    n, heads, size, hd = k_pages.shape
-    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
-        raise ValueError("k_pages and v_pages differ in shape, type or device")
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or \
+            v_pages.device != k_pages.device:
+        raise ValueError("k_pages and v_pages: expected [n_pages, n_kv_heads, page_size, head_dim], alike in "
+                         "shape, type and device")
     if k_pages.dtype not in _CACHES:
         raise ValueError(f"no cache of {k_pages.dtype}")
+    n, heads, size, hd = k_pages.shape
     for t in (k_pages, v_pages):
         if n and not t[0].is_contiguous():
             raise ValueError("a page is not contiguous")
     fmt = _CACHES[k_pages.dtype]
     if (fmt == DFLASH_CACHE_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
         raise ValueError("E4M3 pages come with k_scale and v_scale, 16-bit pages without")
+    index = k_pages.get_device()
     shape = (n, heads, size)
     page = heads * size * hd
     c = dflash_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(),
-                           _fit("k_scale", k_scale, torch.float32, shape, k_pages.device),
-                           _fit("v_scale", v_scale, torch.float32, shape, k_pages.device),
+                           _fit("k_scale", k_scale, torch.float32, shape, index),
+                           _fit("v_scale", v_scale, torch.float32, shape, index),
                            k_pages.stride(0) if n > 1 else page, v_pages.stride(0) if n > 1 else page,
                            n, heads, size, hd, fmt)
-    return PagedCache(c, (k_pages, v_pages, k_scale, v_scale))
+    return PagedCache(c, (k_pages, v_pages, k_scale, v_scale), index)
 
 
-def _rows(name, t, device):
-    if t.dim() != 3 or t.device != device or (t.numel() and t.stride(2) != 1):
-        raise ValueError(f"{name}: expected [rows, heads, head_dim] on {device} with head_dim contiguous")
-    return dflash_rows(t.data_ptr(), t.stride(0), t.stride(1))
+def _rows(name, t, index):
+    if t.dim() != 3 or t.get_device() != index or (t.stride(2) != 1 and t.numel()):
+        raise ValueError(f"{name}: expected [rows, heads, head_dim] on cuda:{index} with head_dim contiguous")
+    return _PACK_ROWS(t.data_ptr(), t.stride(0), t.stride(1))
 
 
-def _paged_batch(row_start, kv_len, page_table, rows, device):
+def _batch(row_start, kv_len, page_table, rows, index):
     B = kv_len.shape[0]
-    _on_device(device)
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32 or \
-            page_table.device != device or (page_table.numel() and page_table.stride(1) != 1):
-        raise ValueError(f"page_table: expected int32 [{B}, max_pages] on {device}")
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not torch.int32 or \
+            page_table.get_device() != index or (page_table.stride(1) != 1 and page_table.numel()):
+        raise ValueError(f"page_table: expected int32 [{B}, max_pages] on cuda:{index}")
     pages = page_table.shape[1]
-    return dflash_paged_batch(_fit("row_start", row_start, torch.int32, (B + 1,), device),
-                              _fit("kv_len", kv_len, torch.int64, (B,), device), page_table.data_ptr(),
-                              page_table.stride(0) if B > 1 else pages, B, pages, rows)
+    return _PACK_BATCH(_fit("row_start", row_start, torch.int32, (B + 1,), index),
+                       _fit("kv_len", kv_len, torch.int64, (B,), index), page_table.data_ptr(),
+                       page_table.stride(0) if B > 1 else pages, B, pages, rows)
 
 
 def dflash_paged_workspace_bytes():
     return int(lib().dflash_paged_workspace_bytes())
 
 
-def _paged_move(name, cache, k, v, row_start, kv_len, page_table, ws, stream):
-    c = cache.struct
-    if k.shape != v.shape or k.dtype != v.dtype or tuple(k.shape[1:]) != (c.n_kv_heads, c.head_dim):
-        raise ValueError(f"k and v: expected [rows, {c.n_kv_heads}, {c.head_dim}] of one type")
-    if k.dtype not in (torch.bfloat16, torch.float16):
+def _paged_move(call, name, cache, k, v, row_start, kv_len, page_table, ws, stream):
+    index = cache.index
+    if k.shape != v.shape or k.dtype is not v.dtype or k.shape[1:] != cache._rows:
+        raise ValueError("k and v: expected [rows, %d, %d] of one type" % cache._rows)
+    if k.dtype is not torch.bfloat16 and k.dtype is not torch.float16:
         raise ValueError(f"no rows of {k.dtype}")
-    b = _paged_batch(row_start, kv_len, page_table, k.shape[0], cache.device)
-    rk, rv = _rows("k", k, cache.device), _rows("v", v, cache.device)
-    _check(getattr(lib(), name)(ctypes.byref(c), ctypes.byref(b), _TYPES[k.dtype], ctypes.byref(rk),
-                                ctypes.byref(rv), _ptr(ws), ws.numel(), _stream(stream)), name)
+    stream = _current(index, stream)
+    code = call(cache._bytes, _batch(row_start, kv_len, page_table, k.shape[0], index), _TYPES[k.dtype],
+                _rows("k", k, index), _rows("v", v, index), _workspace(ws, index), ws.numel(), stream)
+    if code:
+        raise DflashError(code, name)
 
 
 def dflash_paged_append(cache, k, v, row_start, kv_len, page_table, ws, stream=None):
     """Write rows k, v [rows, n_kv_heads, head_dim] into the cache; row_start
     int32 [B + 1], kv_len int64 [B] (new rows counted), page_table int32
     [B, max_pages]."""
-    _paged_move("dflash_paged_append", cache, k, v, row_start, kv_len, page_table, ws, stream)
+    _paged_move(lib().dflash_paged_append, "dflash_paged_append", cache, k, v, row_start, kv_len, page_table, ws,
+                stream)
 
 
 def dflash_paged_gather(cache, k, v, row_start, kv_len, page_table, ws, stream=None):
     """Read the last row_start[b + 1] - row_start[b] positions of every request
     back into k, v [rows, n_kv_heads, head_dim]."""
-    _paged_move("dflash_paged_gather", cache, k, v, row_start, kv_len, page_table, ws, stream)
+    _paged_move(lib().dflash_paged_gather, "dflash_paged_gather", cache, k, v, row_start, kv_len, page_table, ws,
+                stream)
 
 
 def dflash_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_rows):
@@ -482,18 +511,20 @@ def dflash_paged_attention(cache, q, out, row_start, kv_len, page_table, max_row
                            scale=None, causal=True, window=0, stream=None):
     """q, out [rows, n_q_heads, head_dim]; lse float32 [rows, n_q_heads] or
     None; scale None: 1 / sqrt(head_dim)."""
-    c = cache.struct
-    if q.shape != out.shape or q.dtype != out.dtype or q.dim() != 3 or q.shape[2] != c.head_dim:
-        raise ValueError(f"q and out: expected [rows, n_q_heads, {c.head_dim}] of one type")
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    index, hd = cache.index, cache._rows[1]
+    shape = q.shape
+    if out.shape != shape or q.dtype is not out.dtype or len(shape) != 3 or shape[2] != hd:
+        raise ValueError(f"q and out: expected [rows, n_q_heads, {hd}] of one type")
+    if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise ValueError(f"no rows of {q.dtype}")
-    b = _paged_batch(row_start, kv_len, page_table, q.shape[0], cache.device)
-    rq, ro = _rows("q", q, cache.device), _rows("out", out, cache.device)
-    _check(lib().dflash_paged_attention(
-        ctypes.byref(c), ctypes.byref(b), _TYPES[q.dtype], q.shape[1], ctypes.byref(rq), ctypes.byref(ro),
-        _fit("lse", lse, torch.float32, q.shape[:2], cache.device), int(max_rows),
-        c.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window), _ptr(ws),
-        ws.numel(), _stream(stream)), "dflash_paged_attention")
+    stream = _current(index, stream)
+    code = lib().dflash_paged_attention(
+        cache._bytes, _batch(row_start, kv_len, page_table, shape[0], index), _TYPES[q.dtype], shape[1],
+        _rows("q", q, index), _rows("out", out, index), _fit("lse", lse, torch.float32, shape[:2], index) or None,
+        max_rows, hd ** -0.5 if scale is None else scale, 1 if causal else 0, window, _workspace(ws, index),
+        ws.numel(), stream)
+    if code:
+        raise DflashError(code, "dflash_paged_attention")
 
 
 def dflash_logits_adjust_workspace_bytes():
@@ -509,33 +540,37 @@ def dflash_logits_adjust(logits, out, ws, counts=None, prompt_mask=None, req_slo
     repetition, frequency, presence float32 [B]; bias_start int32 [B + 1] with
     bias_ids int32 and bias_vals float32 [n_bias]; allow int32
     [B, G, ceil(V / 32)] bits."""
-    if logits.dim() != 3 or logits.dtype not in _TYPES or out.shape != logits.shape or \
-            out.dtype != torch.float32 or out.device != logits.device:
+    shape = logits.shape
+    index = logits.get_device()
+    if len(shape) != 3 or logits.dtype not in _TYPES or out.shape != shape or \
+            out.dtype is not torch.float32 or out.get_device() != index:
         raise ValueError("logits and out: expected [B, G, V], out float32, on one device")
-    B, G, V = logits.shape
-    dev = logits.device
-    _on_device(dev)
-    if (V > 1 and (logits.stride(2) != 1 or out.stride(2) != 1)):
+    B, G, V = shape
+    l_b, l_i, l_v = logits.stride()
+    o_b, o_i, o_v = out.stride()
+    if V > 1 and (l_v != 1 or o_v != 1):
         raise ValueError("the vocabulary is not contiguous")
+    stream = _current(index, stream)
     words = (V + 31) // 32
-    slots = next((t.shape[0] for t in (counts, prompt_mask) if t is not None), 0)
+    slots = counts.shape[0] if counts is not None else prompt_mask.shape[0] if prompt_mask is not None else 0
     n_bias = 0 if bias_ids is None else bias_ids.shape[0]
-    r = dflash_logit_rules(
-        _fit("counts", counts, torch.int32, (slots, V), dev),
-        _fit("prompt_mask", prompt_mask, torch.int32, (slots, words), dev),
-        _fit("req_slot", req_slot, torch.int32, (B,), dev), slots,
-        _fit("draft", draft, torch.int32, (B, G - 1), dev),
-        _fit("repetition", repetition, torch.float32, (B,), dev),
-        _fit("frequency", frequency, torch.float32, (B,), dev),
-        _fit("presence", presence, torch.float32, (B,), dev),
-        _fit("bias_start", bias_start, torch.int32, (B + 1,), dev),
-        _fit("bias_ids", bias_ids, torch.int32, (n_bias,), dev),
-        _fit("bias_vals", bias_vals, torch.float32, (n_bias,), dev), n_bias,
-        _fit("allow", allow, torch.int32, (B, G, words), dev))
-    _check(lib().dflash_logits_adjust(B, G, V, _TYPES[logits.dtype], _ptr(logits), logits.stride(0),
-                                      logits.stride(1), _ptr(out), out.stride(0), out.stride(1),
-                                      ctypes.byref(r), _ptr(ws), ws.numel(), _stream(stream)),
-           "dflash_logits_adjust")
+    i32, f32, per = torch.int32, torch.float32, (B,)
+    rules = _PACK_RULES(
+        _fit("counts", counts, i32, (slots, V), index),
+        _fit("prompt_mask", prompt_mask, i32, (slots, words), index),
+        _fit("req_slot", req_slot, i32, per, index), slots,
+        _fit("draft", draft, i32, (B, G - 1), index),
+        _fit("repetition", repetition, f32, per, index),
+        _fit("frequency", frequency, f32, per, index),
+        _fit("presence", presence, f32, per, index),
+        _fit("bias_start", bias_start, i32, (B + 1,), index),
+        _fit("bias_ids", bias_ids, i32, (n_bias,), index),
+        _fit("bias_vals", bias_vals, f32, (n_bias,), index), n_bias,
+        _fit("allow", allow, i32, (B, G, words), index))
+    code = lib().dflash_logits_adjust(B, G, V, _TYPES[logits.dtype], logits.data_ptr(), l_b, l_i, out.data_ptr(),
+                                      o_b, o_i, rules, _workspace(ws, index), ws.numel(), stream)
+    if code:
+        raise DflashError(code, "dflash_logits_adjust")
 
 
 def quantize_weights_e4m3(weights, stream=None):
