@@ -4,9 +4,11 @@
 //
 // Both move every byte once and compute next to nothing, so memory (or, for a
 // step's few rows, the latency of the dependent loads row_start -> kv_len ->
-// page_table) bounds them.  A thread moves 16 values of one (row, KV head,
-// K or V): 32 bytes on the 16-bit side and 32 or 16 on the cache's, so 8 or 4
-// neighbouring threads hold a whole row of head_dim values and find its
+// page_table) bounds them.  A block has a few rows; one thread each finds
+// their places in the cache, once for all heads, K and V.  Then a thread moves
+// 16 values of one (row, KV head, K or V) at a time, two such pieces on their
+// way: 32 bytes each on the 16-bit side and 32 or 16 on the cache's, so that 8
+// or 4 neighbouring threads hold a whole row of head_dim values and find its
 // largest magnitude with shuffles.
 #include <cuda_fp8.h>
 
@@ -17,6 +19,41 @@ namespace {
 
 constexpr int kMoveThreads = 256;
 constexpr float kE4M3Max = 448.0f;
+constexpr int kPieces = 2;
+// Pieces of one block, and the number of blocks (4 for each of 152 SMs) that
+// comes first: a step's few rows are spread over as many.
+constexpr int kMostUnits = 256, kBlocks = 608;
+
+// E4M3 codes of 16 values over s: x / s rounded to float32, then to E4M3.
+// The quotient's rounding matters, since values that lie exactly half way
+// between two codes are common (0.75 of the largest value is one).  It is
+// made from the correctly rounded y = 1 / s: q = x y is a unit or two in the
+// last place off, r = x - q s is exact in a fused operation, and q + r y
+// rounded once is the quotient (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990), three operations
+// where a division takes ten or more.  A scale so small that y or r could leave
+// float32's range takes the division.
+template <bool BF16>
+__device__ __forceinline__ uint4 quantize16(const uint32_t (&v)[8], float s) {
+  const float y = __fdiv_rn(1.0f, s);
+  const float2 y2 = make_float2(y, y), ms = make_float2(-s, -s);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = unpack16<BF16>(v[i]);
+    float2 q = mul2(x, y2);
+    q = fma2(fma2(q, ms, x), y2, q);
+    c[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  }
+  if (s < 0x1p-100f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = unpack16<BF16>(v[i]);
+      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)), __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+  return make_uint4(c[0] | (c[1] << 16), c[2] | (c[3] << 16), c[4] | (c[5] << 16), c[6] | (c[7] << 16));
+}
 
 struct Place {
   bool owned;  // some request owns the row
@@ -63,99 +100,141 @@ __device__ __forceinline__ Place find_row(const PagedBatch& p, int b, int n, int
   return r;
 }
 
+// rows: of a block, at most kMoveThreads.
 template <int HD, bool E4M3, bool BF16, bool APPEND>
-__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMoveArgs a, int rows) {
   pdl_enter();
   constexpr int kLanes = HD / 16;                   // threads per (row, head, side)
-  constexpr int kUnits = kMoveThreads / kLanes;     // (row, head, side) per block
+  constexpr int kUnits = kMoveThreads / kLanes;     // (row, head, side) at once
   constexpr int kCell = E4M3 ? 1 : 2;               // bytes of a cached value
-  const long long u0 = (long long)blockIdx.x * kUnits;
-  const int per_row = 2 * a.n_kv;
-  const int b0 = first_request(a.batch, (int)(u0 / per_row), a.status);
+  __shared__ Place places[kMoveThreads];
+  const int n0 = blockIdx.x * rows, lane = threadIdx.x % kLanes;
+  const uint32_t per_row = 2u * a.n_kv;
+  const uint32_t units = min(rows, a.batch.rows - n0) * per_row;
 
-  const long long u = u0 + threadIdx.x / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  const long long n = u / per_row;
-  const int hs = (int)(u - n * per_row), side = hs >= a.n_kv, head = side ? hs - a.n_kv : hs;
-  Place pl = {false, false, 0, 0};
-  if (n < a.batch.rows) pl = find_row(a.batch, b0, (int)n, a.status);
-
-  uint8_t* x = a.x[side] + ((size_t)n * a.row_stride[side] + (size_t)head * a.head_stride[side] + lane * 16) * 2;
-  const size_t row = ((size_t)head << a.batch.page_shift) + pl.at;   // row of the page
-  uint8_t* cell = a.pages[side] + ((size_t)pl.page * a.page_stride[side] + row * HD + lane * 16) * kCell;
-  float* scale = E4M3 ? a.scale[side] + ((((size_t)pl.page * a.n_kv) << a.batch.page_shift) + row) : nullptr;
-
-  if (APPEND) {
-    uint4 w[2] = {};
-    if (pl.there) {
-      w[0] = __ldg(reinterpret_cast<const uint4*>(x));
-      w[1] = __ldg(reinterpret_cast<const uint4*>(x) + 1);
-    }
-    if (!E4M3) {
-      if (pl.there) {
-        reinterpret_cast<uint4*>(cell)[0] = w[0];
-        reinterpret_cast<uint4*>(cell)[1] = w[1];
+  struct Piece {
+    int row, head, side;  // row of the block
+    uint8_t* x;
+  };
+  auto piece = [&](uint32_t u) {
+    Piece p;
+    p.row = (int)(u / per_row);
+    const int hs = (int)(u - p.row * per_row);
+    p.side = hs >= a.n_kv;
+    p.head = p.side ? hs - a.n_kv : hs;
+    p.x = a.x[p.side] +
+          ((size_t)(n0 + p.row) * a.row_stride[p.side] + (size_t)p.head * a.head_stride[p.side] + lane * 16) * 2;
+    return p;
+  };
+  uint4 w[kPieces][2] = {};
+  auto load_rows = [&](uint32_t u0) {
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      const uint32_t u = u0 + q * kUnits;
+      if (u < units) {
+        const uint4* x = reinterpret_cast<const uint4*>(piece(u).x);
+        w[q][0] = __ldg(x);
+        w[q][1] = __ldg(x + 1);
       }
-      return;
     }
-    // magnitudes of both types order like their bits, NaN above infinity
-    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-    uint32_t m = 0;
+  };
+  // the rows exist whoever owns them: the first are on their way while the
+  // places are looked up
+  if (APPEND) load_rows(threadIdx.x / kLanes);
+  const int b0 = first_request(a.batch, min(n0, a.batch.rows), a.status);
+  if ((int)threadIdx.x < rows && n0 + (int)threadIdx.x < a.batch.rows)
+    places[threadIdx.x] = find_row(a.batch, b0, n0 + threadIdx.x, a.status);
+  __syncthreads();
+
+  // whole warps stay together: pieces past the last take part in the shuffles
+  const uint32_t turns = (units + kUnits * kPieces - 1) / (kUnits * kPieces);
+  for (uint32_t turn = 0; turn < turns; ++turn) {
+    const uint32_t u0 = turn * (kUnits * kPieces) + threadIdx.x / kLanes;
+    uint8_t *x[kPieces], *cell[kPieces];
+    float* scale[kPieces];
+    bool owned[kPieces], there[kPieces];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = max(m & 0xFFFFu, m >> 16);
-    const bool finite = m < (BF16 ? 0x7F80u : 0x7C00u);
-    const float amax = unpack16<BF16>(m).x;
-    const float s = !finite ? __uint_as_float(0x7FC00000u) : m ? __fdiv_rn(amax, kE4M3Max) : 1.0f;
-    if (!pl.there) return;
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack16<BF16>(v[2 * i]), g = unpack16<BF16>(v[2 * i + 1]);
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s)),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(g.x, s), __fdiv_rn(g.y, s)),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      c[i] = lo | (hi << 16);
+    for (int q = 0; q < kPieces; ++q) {
+      const uint32_t u = u0 + q * kUnits;
+      const Piece p = piece(min(u, units - 1));
+      const Place pl = places[p.row];
+      x[q] = p.x;
+      owned[q] = pl.owned && u < units;
+      there[q] = pl.there && u < units;
+      const size_t row = ((size_t)p.head << a.batch.page_shift) + pl.at;
+      cell[q] = a.pages[p.side] + ((size_t)pl.page * a.page_stride[p.side] + row * HD + lane * 16) * kCell;
+      scale[q] = a.scale[p.side] + (((size_t)pl.page * a.n_kv) << a.batch.page_shift) + row;
     }
-    *reinterpret_cast<uint4*>(cell) = make_uint4(c[0], c[1], c[2], c[3]);
-    if (lane == 0) *scale = s;
-  } else {
-    if (!pl.owned) return;
-    uint4 w[2] = {};
-    if (pl.there) {
-      if (E4M3) {
-        const uint4 c = __ldg(reinterpret_cast<const uint4*>(cell));
-        const float s = __ldg(scale);
-        const uint32_t v[4] = {c.x, c.y, c.z, c.w};
-        uint32_t o[8];
+    if (APPEND) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t h = e4m3x2_to_f16x2((uint16_t)(v[i / 2] >> (16 * (i & 1))));
-          const float2 f = unpack16<false>(h);
-          o[i] = pack16<BF16>(f.x * s, f.y * s);
+      for (int q = 0; q < kPieces; ++q) {
+        if (!E4M3) {
+          if (there[q]) {
+            reinterpret_cast<uint4*>(cell[q])[0] = w[q][0];
+            reinterpret_cast<uint4*>(cell[q])[1] = w[q][1];
+          }
+          continue;
         }
-        w[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        w[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      } else {
-        w[0] = __ldg(reinterpret_cast<const uint4*>(cell));
-        w[1] = __ldg(reinterpret_cast<const uint4*>(cell) + 1);
+        // magnitudes of both types order like their bits, NaN above infinity
+        const uint32_t v[8] = {w[q][0].x, w[q][0].y, w[q][0].z, w[q][0].w, w[q][1].x, w[q][1].y, w[q][1].z, w[q][1].w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = max(m & 0xFFFFu, m >> 16);
+        const bool finite = m < (BF16 ? 0x7F80u : 0x7C00u);
+        const float amax = unpack16<BF16>(m).x;
+        const float s = !finite ? __uint_as_float(0x7FC00000u) : m ? __fdiv_rn(amax, kE4M3Max) : 1.0f;
+        if (!there[q]) continue;
+        *reinterpret_cast<uint4*>(cell[q]) = quantize16<BF16>(v, s);
+        if (lane == 0) *scale[q] = s;
+      }
+      if (turn + 1 < turns) load_rows(u0 + kUnits * kPieces);
+    } else {
+      uint4 c[kPieces];
+      float s[kPieces];
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        w[q][0] = w[q][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (!there[q]) continue;
+        if (E4M3) {
+          c[q] = __ldg(reinterpret_cast<const uint4*>(cell[q]));
+          s[q] = __ldg(scale[q]);
+        } else {
+          w[q][0] = __ldg(reinterpret_cast<const uint4*>(cell[q]));
+          w[q][1] = __ldg(reinterpret_cast<const uint4*>(cell[q]) + 1);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        if (!owned[q]) continue;
+        if (E4M3 && there[q]) {
+          const uint32_t v[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = unpack16<false>(e4m3x2_to_f16x2((uint16_t)(v[i / 2] >> (16 * (i & 1)))));
+            o[i] = pack16<BF16>(f.x * s[q], f.y * s[q]);
+          }
+          w[q][0] = make_uint4(o[0], o[1], o[2], o[3]);
+          w[q][1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        reinterpret_cast<uint4*>(x[q])[0] = w[q][0];
+        reinterpret_cast<uint4*>(x[q])[1] = w[q][1];
       }
     }
-    reinterpret_cast<uint4*>(x)[0] = w[0];
-    reinterpret_cast<uint4*>(x)[1] = w[1];
   }
 }
 
 template <int HD, bool E4M3, bool BF16, bool APPEND>
 int launch_move(const PagedMoveArgs& a, cudaStream_t s) {
-  const long long units = (long long)a.batch.rows * 2 * a.n_kv;
-  const long long per = kMoveThreads / (HD / 16);
-  const long long grid = units > 0 ? (units + per - 1) / per : 1;
-  if (grid > 0x7FFFFFFFll) return DFLASH_ERR_SHAPE;
-  return launch_pdl(paged_move_kernel<HD, E4M3, BF16, APPEND>, dim3((unsigned)grid), dim3(kMoveThreads), 0, s, a);
+  const int per_row = 2 * a.n_kv, at_once = kMoveThreads / (HD / 16);
+  const long long units = (long long)a.batch.rows * per_row;
+  const long long each = min((long long)kMostUnits, max((long long)at_once, units / kBlocks));
+  const int rows = min(kMoveThreads, max(1, (int)(each / per_row)));
+  const int grid = max(1, ceil_div(a.batch.rows, rows));
+  return launch_pdl(paged_move_kernel<HD, E4M3, BF16, APPEND>, dim3(grid), dim3(kMoveThreads), 0, s, a, rows);
 }
 
 template <bool APPEND>

@@ -110,6 +110,29 @@ def test_append_then_gather_returns_16_bit_rows_exactly_and_codes_within_half_a_
             assert ((a - b).abs() <= step + b.abs() * 2.0 ** -7).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, FH])
+def test_append_codes_of_ties_and_of_very_small_and_large_rows(dtype):
+    """Bit for bit where quotients lie half way between codes (small integers
+    over each other) and where the scale leaves the ordinary range."""
+    n, hd = 512, 128
+    rng = np.random.default_rng(4)
+    x = rng.integers(-40, 41, size=(n, 1, hd)).astype(np.float64)
+    lo, hi = (-132, 120) if dtype == BF else (-24, 9)
+    x *= 2.0 ** rng.integers(lo, hi, size=(n, 1, 1))
+    x[::7] *= 1.3
+    k = torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
+    p = Paged([n], [n], 1, hd, 64, dtype, True)
+    ws = dfl.workspace(dfl.dflash_paged_workspace_bytes())
+    dfl.dflash_paged_append(p.cache, k, k, *p.batch, ws)
+    torch.cuda.synchronize()
+    codes, scale = ot.quantize(k.float().cpu().numpy())
+    kp, vp, ks, vs = p.host()
+    for r, _, _, pid, at in ot.places(p.start_np, p.lens, p.table_np, 64):
+        np.testing.assert_array_equal(ks[pid, :, at], scale[r])
+        np.testing.assert_array_equal(kp[pid, :, at], codes[r])
+        np.testing.assert_array_equal(vp[pid, :, at], codes[r])
+
+
 def test_pages_past_2_to_31_elements():
     """Page strides whose offsets need 64 bits, in 8 and in 16 bits."""
     for e4m3, stride in ((True, 3 << 29), (False, 3 << 28)):
