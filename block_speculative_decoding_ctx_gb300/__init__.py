@@ -79,7 +79,12 @@ _CACHES = {torch.bfloat16: DFLASH_CACHE_BF16, torch.float16: DFLASH_CACHE_F16,
 class dflash_paged_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale")] + [
         (n, ctypes.c_longlong) for n in ("k_page_stride", "v_page_stride")] + [
-        (n, ctypes.c_int) for n in ("n_pages", "n_kv_heads", "page_size", "head_dim", "format")]
+        (n, ctypes.c_int) for n in ("n_pages", "n_kv_heads", "page_size", "head_dim", "format")] + [
+        ("maps", ctypes.c_void_p)]
+
+
+class dflash_paged_maps(ctypes.Structure):
+    _fields_ = [("opaque", ctypes.c_ulonglong * 48)]
 
 
 class dflash_paged_batch(ctypes.Structure):
@@ -145,6 +150,7 @@ def lib():
         "dflash_quantize_e4m3": (_I, [_P, _I, _I, _P, _P, _P]),
         "dflash_verify_noalloc": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, ctypes.c_uint64, _P, _P, _P,
                                        _P, _P]),
+        "dflash_paged_cache_maps": (_I, [_P, _P]),
         "dflash_paged_workspace_bytes": (_SZ, []),
         "dflash_paged_append": (_I, [_P, _P, _I, _P, _P, _P, _SZ, _P]),
         "dflash_paged_gather": (_I, [_P, _P, _I, _P, _P, _P, _SZ, _P]),
@@ -393,6 +399,17 @@ class PagedCache:
         self._bytes = bytes(fields)
         self._keep = keep
         self._rows = (fields.n_kv_heads, fields.head_dim)
+        self._maps = None
+
+    def _with_maps(self):
+        """The struct's bytes with the descriptors that attention needs, made
+        at the first call."""
+        maps = dflash_paged_maps()
+        _check(lib().dflash_paged_cache_maps(self._bytes, ctypes.byref(maps)), "dflash_paged_cache_maps")
+        c = dflash_paged_cache.from_buffer_copy(self._bytes)
+        c.maps = ctypes.addressof(maps)
+        self._maps = (bytes(c), maps)
+        return self._maps[0]
 
 
 def _misfit(name, t, dtype, shape, index):
@@ -450,7 +467,7 @@ def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None):
                            _fit("k_scale", k_scale, torch.float32, shape, index),
                            _fit("v_scale", v_scale, torch.float32, shape, index),
                            k_pages.stride(0) if n > 1 else page, v_pages.stride(0) if n > 1 else page,
-                           n, heads, size, hd, fmt)
+                           n, heads, size, hd, fmt, None)
     return PagedCache(c, (k_pages, v_pages, k_scale, v_scale), index)
 
 
@@ -518,8 +535,9 @@ def dflash_paged_attention(cache, q, out, row_start, kv_len, page_table, max_row
     if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise ValueError(f"no rows of {q.dtype}")
     stream = _current(index, stream)
+    maps = cache._maps
     code = lib().dflash_paged_attention(
-        cache._bytes, _batch(row_start, kv_len, page_table, shape[0], index), _TYPES[q.dtype], shape[1],
+        maps[0] if maps is not None else cache._with_maps(), _batch(row_start, kv_len, page_table, shape[0], index), _TYPES[q.dtype], shape[1],
         _rows("q", q, index), _rows("out", out, index), _fit("lse", lse, torch.float32, shape[:2], index) or None,
         max_rows, hd ** -0.5 if scale is None else scale, 1 if causal else 0, window, _workspace(ws, index),
         ws.numel(), stream)

@@ -2,6 +2,7 @@
 // adjustment.  See include/dflash.h for the contract of every entry point.
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "common.cuh"
 #include "paged.h"
@@ -34,6 +35,12 @@ int check_cache(const dflash_paged_cache* c) {
     if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)) return DFLASH_ERR_ALIGN;
   }
   return DFLASH_OK;
+}
+
+bool same_cache(const dflash_paged_cache& a, const dflash_paged_cache& b) {
+  return a.k_pages == b.k_pages && a.v_pages == b.v_pages && a.k_scale == b.k_scale && a.v_scale == b.v_scale &&
+         a.k_page_stride == b.k_page_stride && a.v_page_stride == b.v_page_stride && a.n_pages == b.n_pages &&
+         a.n_kv_heads == b.n_kv_heads && a.page_size == b.page_size && a.head_dim == b.head_dim && a.format == b.format;
 }
 
 int check_batch(const dflash_paged_batch* b, const dflash_paged_cache* c) {
@@ -116,6 +123,18 @@ int move(bool append, const dflash_paged_cache* cache, const dflash_paged_batch*
 
 extern "C" {
 
+int dflash_paged_cache_maps(const dflash_paged_cache* cache, dflash_paged_maps* maps) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (!maps) return DFLASH_ERR_ARG;
+  PagedMaps m = {};
+  m.cache = *cache;
+  m.cache.maps = nullptr;
+  if ((rc = encode_paged_maps(*cache, &m.k, &m.v))) return rc;
+  std::memcpy(maps, &m, sizeof(m));
+  return DFLASH_OK;
+}
+
 size_t dflash_paged_workspace_bytes(void) { return kWsHeader; }
 
 int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_batch* batch, int type,
@@ -147,6 +166,9 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_b
   if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads || n_q_heads > 65535) return DFLASH_ERR_SHAPE;
   const int group = n_q_heads / cache->n_kv_heads;
   if (max_rows < 0 || max_rows > batch->rows || (long long)max_rows * group > (1ll << 30)) return DFLASH_ERR_SHAPE;
+  // key tiles of an item, over all KV heads, are counted in 32 bits
+  if (((long long)batch->max_pages * cache->page_size / 128 + 16) * cache->n_kv_heads > 0x7FFFFFFFll)
+    return DFLASH_ERR_SHAPE;
   if (!(scale > 0.0f) || !std::isfinite(scale * 1.44269504f) || (causal != 0 && causal != 1) || window < 0)
     return DFLASH_ERR_ARG;
   if ((rc = check_rows(q, batch->rows, n_q_heads, cache->head_dim))) return rc;
@@ -155,15 +177,17 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_b
   if ((rc = check_workspace(workspace, ws_bytes,
                             paged_attention_workspace(n_q_heads, cache->n_kv_heads, cache->head_dim, max_rows))))
     return rc;
+  PagedMaps maps;
+  if (cache->maps) {
+    std::memcpy(&maps, cache->maps, sizeof(maps));
+    if (!same_cache(maps.cache, *cache)) return DFLASH_ERR_ARG;
+  }
   if (max_rows == 0) return DFLASH_OK;
+  if (!cache->maps && (rc = encode_paged_maps(*cache, &maps.k, &maps.v))) return rc;
   PagedAttnArgs a;
   a.batch = batch_args(batch, cache);
-  a.k_pages = static_cast<const uint8_t*>(cache->k_pages);
-  a.v_pages = static_cast<const uint8_t*>(cache->v_pages);
   a.k_scale = cache->k_scale;
   a.v_scale = cache->v_scale;
-  a.k_page_stride = cache->k_page_stride;
-  a.v_page_stride = cache->v_page_stride;
   a.q = static_cast<const uint8_t*>(q->ptr);
   a.out = static_cast<uint8_t*>(out->ptr);
   a.q_row = q->row_stride;
@@ -179,7 +203,7 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_b
   a.window = window < (1 << 30) ? window : 0;  // longer than any position: none
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = static_cast<int*>(workspace);
-  return launch_paged_attention(a, cache->head_dim, cache->format, type, workspace,
+  return launch_paged_attention(maps.k, maps.v, a, cache->head_dim, cache->format, type, workspace,
                                 reinterpret_cast<cudaStream_t>(stream));
 }
 

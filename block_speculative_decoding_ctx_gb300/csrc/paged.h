@@ -2,6 +2,7 @@
 // paged_attention.cu) and of the logit adjustment (logits.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -33,13 +34,19 @@ struct PagedMoveArgs {
 int launch_paged_append(const PagedMoveArgs& a, int head_dim, int format, int type, cudaStream_t s);
 int launch_paged_gather(const PagedMoveArgs& a, int head_dim, int format, int type, cudaStream_t s);
 
+// What dflash_paged_maps holds.
+struct PagedMaps {
+  dflash_paged_cache cache;  // with maps = nullptr
+  CUtensorMap k, v;
+};
+static_assert(sizeof(PagedMaps) <= sizeof(dflash_paged_maps), "opaque size");
+
+int encode_paged_maps(const dflash_paged_cache& c, CUtensorMap* k, CUtensorMap* v);
+
 struct PagedAttnArgs {
   PagedBatch batch;
-  const uint8_t* k_pages;
-  const uint8_t* v_pages;
   const float* k_scale;
   const float* v_scale;
-  long long k_page_stride, v_page_stride;
   const uint8_t* q;
   uint8_t* out;
   long long q_row, q_head, o_row, o_head;
@@ -51,8 +58,8 @@ struct PagedAttnArgs {
 };
 
 size_t paged_attention_workspace(int n_q, int n_kv, int head_dim, int max_rows);
-int launch_paged_attention(const PagedAttnArgs& a, int head_dim, int format, int type, void* workspace,
-                           cudaStream_t s);
+int launch_paged_attention(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnArgs& a, int head_dim,
+                           int format, int type, void* workspace, cudaStream_t s);
 
 struct LogitsArgs {
   const void* logits;

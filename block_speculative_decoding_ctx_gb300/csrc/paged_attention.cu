@@ -83,6 +83,7 @@ constexpr float kVShiftLog2 = 8.0f;  // E4M3: factor on the weights
 // Where an item that this CTA starts but does not finish continues.
 struct Rec {
   int pair, head, slot, last_cta;  // pair < 0: none
+  int s0, row0, rows;              // its rows (Item)
 };
 
 struct KernelArgs {
@@ -157,9 +158,10 @@ struct Seg {
   long long end;   // where the item ends on the line, from the CTA's first unit on
 };
 
+// Where a CTA's part of the line begins.
 struct Start {
-  long long off;  // units of its pair before this CTA's part
-  int pair;
+  Item it;
+  int pair, head, off;  // off: units of (pair, head) before it
 };
 
 struct Walk {
@@ -167,13 +169,13 @@ struct Walk {
   int pair, head, off;
   bool loaded;
   Item it;
-  __device__ void begin(const KernelArgs& k, const Start& st, long long n) {
+  __device__ void begin(const Start& st, long long n) {
     left = total = n;
+    it = st.it;
     pair = st.pair;
-    (void)find_item(k, &pair, k.a.batch.B * k.rts, &it);
+    head = st.head;
+    off = st.off;
     loaded = true;
-    head = (int)(st.off / it.units);
-    off = (int)(st.off - (long long)head * it.units);
   }
   __device__ bool next(const KernelArgs& k, Seg* s) {
     while (left > 0) {
@@ -492,20 +494,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                            const KernelArgs k) {
   using C = Cfg<HD, E4M3, BF16>;
-  pdl_enter();
+  grid_dependents_launch();
   extern __shared__ __align__(1024) uint8_t smem[];
   const PagedAttnArgs& a = k.a;
   uint8_t* ring_s = smem;
   uint8_t* q_s = ring_s + 2 * k.half * C::kTile;
   auto* c = reinterpret_cast<Ctrl<E4M3>*>(smem + kSmem - kCtrlBytes<E4M3>);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
   if (smem_u32(smem) & 1023) {  // the swizzled tiles want 1024-byte atoms
+    grid_dependency_wait();
     if (tid == 0) {
       report_status(a.status, DFLASH_ERR_UNSUPPORTED);
-      k.rec[blockIdx.x].pair = -1;
+      k.rec[cta].pair = -1;
     }
     return;
   }
+
+  // ---- what waits for nobody: barriers and tensor memory
+  if (tid == 0) {
+    for (int s = 0; s < 2 * k.half; ++s) {
+      mbar_init(&c->full[s], 1);
+      mbar_init(&c->empty[s], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&c->s_full[i][h], 1);
+        mbar_init(&c->p_full[i][h], 4);
+        mbar_init(&c->pv_done[i][h], 1);
+      }
+      mbar_init(&c->q_full[i], 1);
+    }
+    mbar_init(&c->o_full, 2);
+    mbar_init(&c->fin, 2);
+    c->abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&c->tmem, 512);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
 
   // ---- the line's length and this CTA's part of it
   const int pairs = a.batch.B * k.rts;
@@ -529,12 +560,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long excl = block_exclusive_scan(mine, reinterpret_cast<unsigned long long*>(c->x), &total);
   const long long W = (long long)total * a.n_kv;
   const int ctas = (int)min((long long)gridDim.x, W);
-  const int cta = blockIdx.x;
   if (cta >= ctas) {
     if (tid == 0) k.rec[cta].pair = -1;
+    if (warp == 1) tmem_dealloc(c->tmem, 512);  // the scan's barriers came after its allocation
     return;
   }
-  const long long w0 = W * cta / ctas, w1 = W * (cta + 1) / ctas;
+  // short divisions where they do
+  const bool few = W < 1 << 23;
+  const long long w0 = few ? (int)W * cta / ctas : W * cta / ctas;
+  const long long w1 = few ? (int)W * (cta + 1) / ctas : W * (cta + 1) / ctas;
   if ((long long)excl * a.n_kv <= w0 && w0 < (long long)(excl + mine) * a.n_kv) {
     long long at = (long long)excl * a.n_kv;
     int p = p0;
@@ -545,32 +579,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += n;
       ++p;
     }
+    const int off = (int)(w0 - at);  // fewer than n_kv x units of an item
+    c->start.it = it;
     c->start.pair = p;
-    c->start.off = w0 - at;
+    c->start.head = off / it.units;
+    c->start.off = off - c->start.head * it.units;
   }
 
-  if (tid == 0) {
-    for (int s = 0; s < 2 * k.half; ++s) {
-      mbar_init(&c->full[s], 1);
-      mbar_init(&c->empty[s], 2);
-    }
-    for (int i = 0; i < 2; ++i) {
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&c->s_full[i][h], 1);
-        mbar_init(&c->p_full[i][h], 4);
-        mbar_init(&c->pv_done[i][h], 1);
-      }
-      mbar_init(&c->q_full[i], 1);
-    }
-    mbar_init(&c->o_full, 2);
-    mbar_init(&c->fin, 2);
-    c->abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(&c->tmem, 512);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -584,8 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const void* map = side ? &tmV : &tmK;
       Walk walk;
       Seg s;
-      walk.begin(k, c->start, w1 - w0);
-      if (lead) tma_prefetch_desc(map);
+      walk.begin(c->start, w1 - w0);
       const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
       auto advance = [&](int& at, uint32_t& phase, int n) {
         at += n;
@@ -818,11 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       c->more[wg][turn & 1u] = more;
       if (wg == 0 && more && n->first && !n->last) {
         const long long u = w0 + n->end - 1;  // the item's last unit
-        k.rec[cta] = Rec{n->pair, n->head, n->slot, (int)(((u + 1) * ctas - 1) / W)};
+        const int last = few ? ((int)(u + 1) * ctas - 1) / (int)W : (int)(((u + 1) * ctas - 1) / W);
+        k.rec[cta] = Rec{n->pair, n->head, n->slot, last, n->it.s0, n->it.row0, n->it.rows};
       }
     };
     if (t == 0) {
-      c->walk[wg].begin(k, c->start, w1 - w0);
+      c->walk[wg].begin(c->start, w1 - w0);
       if (wg == 0) k.rec[cta].pair = -1;
       describe(0);
     }
@@ -1074,31 +1089,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live) {
         const size_t pi = (size_t)(cta * 2 + s.slot) * k.part_rows + pr;
         uint8_t* out = a.out + ((size_t)(it.s0 + tok) * a.o_row + (size_t)(s.head * a.group + g) * a.o_head) * 2;
-        for (int i = 0; i < cols / 16; ++i) {
-          const int col = col0 + i * 16;
-          float o[16];
-          uint32_t r0[16], r1[16];
+#pragma unroll 1
+        for (int i = 0; i < cols / 32; ++i) {
+          const int col = col0 + i * 32;
+          float o[32] = {}, o1[32] = {};
+          if (have0) tmem_ld_x32(tO + (s.split ? 0 : wg * 128) + col, o);
+          if (have1) tmem_ld_x32(tO + 128 + col, o1);
+          wait_ld(o);
+          wait_ld(o1);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r0[e] = r1[e] = 0u;
-          if (have0) tmem_ld_x16(tO + (s.split ? 0 : wg * 128) + col, r0);
-          if (have1) tmem_ld_x16(tO + 128 + col, r1);
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            o[e] = __uint_as_float(r0[e]) * f0;
-            if (have1) o[e] = fmaf(__uint_as_float(r1[e]), f1, o[e]);
+          for (int e = 0; e < 32; ++e) {
+            o[e] *= f0;
+            if (have1) o[e] = fmaf(o1[e], f1, o[e]);
           }
           if (!real) continue;
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(out + col * 2);
-            dst[0] = make_uint4(pack16<BF16>(o[0], o[1]), pack16<BF16>(o[2], o[3]), pack16<BF16>(o[4], o[5]),
-                                pack16<BF16>(o[6], o[7]));
-            dst[1] = make_uint4(pack16<BF16>(o[8], o[9]), pack16<BF16>(o[10], o[11]), pack16<BF16>(o[12], o[13]),
-                                pack16<BF16>(o[14], o[15]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack16<BF16>(o[8 * e], o[8 * e + 1]), pack16<BF16>(o[8 * e + 2], o[8 * e + 3]),
+                                  pack16<BF16>(o[8 * e + 4], o[8 * e + 5]), pack16<BF16>(o[8 * e + 6], o[8 * e + 7]));
           } else {
             float4* dst = reinterpret_cast<float4*>(k.part + pi * HD + col);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
         if (real && (!s.split || wg == 0)) {
@@ -1134,13 +1148,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const KernelArgs k) {
   if (rec.pair < 0) return;
   const PagedAttnArgs& a = k.a;
   const int lane = threadIdx.x & 31, w = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int b = rec.pair / k.rts;
-  RequestSpan r;
-  if (!item_rows(a, b, &r)) return;
-  const Item it = make_item(k, r, b, rec.pair - b * k.rts);
   const int n = rec.last_cta - cta + 1;
   constexpr int kE = HD / 32;
-  for (int row = w; row < it.rows; row += 8 * gridDim.y) {
+  for (int row = w; row < rec.rows; row += 8 * gridDim.y) {
     auto place = [&](int i) { return (size_t)((cta + i) * 2 + (i ? 0 : rec.slot)) * k.part_rows + row; };
     float M = -INFINITY;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, k.ml[place(i)].x);
@@ -1168,13 +1178,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const KernelArgs k) {
     }
     L = warp_sum(L);
     const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
-    const int packed = it.row0 + row, tok = packed / a.group, g = packed - tok * a.group;
+    const int packed = rec.row0 + row, tok = packed / a.group, g = packed - tok * a.group;
     uint32_t* out = reinterpret_cast<uint32_t*>(
-        a.out + ((size_t)(it.s0 + tok) * a.o_row + (size_t)(rec.head * a.group + g) * a.o_head + lane * kE) * 2);
+        a.out + ((size_t)(rec.s0 + tok) * a.o_row + (size_t)(rec.head * a.group + g) * a.o_head + lane * kE) * 2);
 #pragma unroll
     for (int e = 0; e < kE; e += 2) out[e / 2] = pack16<BF16>(o[e] * inv, o[e + 1] * inv);
     if (a.lse && lane == 0)
-      a.lse[(size_t)(it.s0 + tok) * a.n_q + rec.head * a.group + g] = (M + log2f(L)) * kLn2;
+      a.lse[(size_t)(rec.s0 + tok) * a.n_q + rec.head * a.group + g] = (M + log2f(L)) * kLn2;
   }
 }
 
@@ -1184,8 +1194,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
 // Tensor map of one side of the cache: [pages][heads x page rows][head_dim].
-int encode_pages(CUtensorMap* map, const void* ptr, const PagedAttnArgs& a, int hd, bool e4m3, bool bf16,
-                 long long page_stride) {
+int encode_pages(CUtensorMap* map, const dflash_paged_cache& c, const void* ptr, long long page_stride) {
   std::call_once(g_encode_once, [] {
     cudaDriverEntryPointQueryResult q;
     void* fn = nullptr;
@@ -1194,17 +1203,18 @@ int encode_pages(CUtensorMap* map, const void* ptr, const PagedAttnArgs& a, int 
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!g_encode) return DFLASH_ERR_CUDA;
-  const int cell = e4m3 ? 1 : 2, page = 1 << a.batch.page_shift;
-  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)a.n_kv * page, (cuuint64_t)a.batch.n_pages};
-  cuuint64_t strides[2] = {(cuuint64_t)hd * cell, (cuuint64_t)page_stride * cell};
-  cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? hd : 64), (cuuint32_t)page, 1};
+  const bool e4m3 = c.format == DFLASH_CACHE_E4M3;
+  const int cell = e4m3 ? 1 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.n_kv_heads * c.page_size, (cuuint64_t)c.n_pages};
+  cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * cell, (cuuint64_t)page_stride * cell};
+  cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? c.head_dim : 64), (cuuint32_t)c.page_size, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  const CUtensorMapDataType dt = e4m3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapDataType dt = e4m3                               ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : c.format == DFLASH_CACHE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUresult r = g_encode(map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              e4m3 && hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                              e4m3 && c.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
@@ -1230,12 +1240,8 @@ Layout layout(void* ws, int group, int hd, int max_rows) {
 }
 
 template <int HD, bool E4M3, bool BF16>
-int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
+int launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   using C = Cfg<HD, E4M3, BF16>;
-  CUtensorMap tk, tv;
-  int rc = encode_pages(&tk, a.k_pages, a, HD, E4M3, BF16, a.k_page_stride);
-  if (rc) return rc;
-  if ((rc = encode_pages(&tv, a.v_pages, a, HD, E4M3, BF16, a.v_page_stride))) return rc;
   auto kern = paged_attention_kernel<HD, E4M3, BF16>;
   int dev = 0, sms = 0;
   DFL_CUDA_TRY(cudaGetDevice(&dev));
@@ -1260,6 +1266,7 @@ int launch(const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   k.half = min(kMaxSlots, (kSmem - kCtrlBytes<E4M3> - k.q_tiles * C::kQTile) / C::kTile) / 2;
   k.seg_cost = E4M3 ? 8 : 4;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  int rc;
   if ((rc = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmem, s, tk, tv, k))) return rc;
   return launch_pdl(paged_join_kernel<HD, BF16>, dim3(grid, k.q_tiles * 8), dim3(256), 0, s, k);
 }
@@ -1270,14 +1277,20 @@ size_t paged_attention_workspace(int n_q, int n_kv, int head_dim, int max_rows) 
   return layout(nullptr, n_q / n_kv, head_dim, max_rows).bytes;
 }
 
-int launch_paged_attention(const PagedAttnArgs& a, int head_dim, int format, int type, void* ws, cudaStream_t s) {
+int encode_paged_maps(const dflash_paged_cache& c, CUtensorMap* k, CUtensorMap* v) {
+  const int rc = encode_pages(k, c, c.k_pages, c.k_page_stride);
+  return rc ? rc : encode_pages(v, c, c.v_pages, c.v_page_stride);
+}
+
+int launch_paged_attention(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnArgs& a, int head_dim,
+                           int format, int type, void* ws, cudaStream_t s) {
   const bool bf = type == DFLASH_TYPE_BF16, e = format == DFLASH_CACHE_E4M3;
   if (head_dim == 128) {
-    if (e) return bf ? launch<128, true, true>(a, ws, s) : launch<128, true, false>(a, ws, s);
-    return bf ? launch<128, false, true>(a, ws, s) : launch<128, false, false>(a, ws, s);
+    if (e) return bf ? launch<128, true, true>(k, v, a, ws, s) : launch<128, true, false>(k, v, a, ws, s);
+    return bf ? launch<128, false, true>(k, v, a, ws, s) : launch<128, false, false>(k, v, a, ws, s);
   }
-  if (e) return bf ? launch<64, true, true>(a, ws, s) : launch<64, true, false>(a, ws, s);
-  return bf ? launch<64, false, true>(a, ws, s) : launch<64, false, false>(a, ws, s);
+  if (e) return bf ? launch<64, true, true>(k, v, a, ws, s) : launch<64, true, false>(k, v, a, ws, s);
+  return bf ? launch<64, false, true>(k, v, a, ws, s) : launch<64, false, false>(k, v, a, ws, s);
 }
 
 }  // namespace dfl

@@ -416,7 +416,17 @@ typedef struct dflash_paged_cache {
   int page_size;
   int head_dim;
   int format;              /* DFLASH_CACHE_* */
+  const struct dflash_paged_maps* maps; /* NULL, or this cache's from dflash_paged_cache_maps */
 } dflash_paged_cache;
+
+/* The TMA descriptors that attention needs of a cache (host memory owned by
+ * the caller, 384 bytes).  Making them takes a few microseconds of the host's
+ * time; a caller that keeps them beside the cache saves that in every call.
+ * Attention refuses (DFLASH_ERR_ARG) maps whose cache had any other field. */
+typedef struct dflash_paged_maps {
+  unsigned long long opaque[48];
+} dflash_paged_maps;
+int dflash_paged_cache_maps(const dflash_paged_cache* cache, dflash_paged_maps* maps);
 
 /* The requests of a call (host struct of device pointers). */
 typedef struct dflash_paged_batch {

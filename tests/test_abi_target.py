@@ -93,10 +93,21 @@ def test_attention_refusals(L):
     assert call(causal=2) == -1 and call(window=-1) == -1
     assert call(lse=P(4098)) == -3
     assert call(ws=None) == -7 and call(n=need - 1) == -7
+    wrong = dfl.dflash_paged_maps()                    # of no cache, let alone of this one
+    assert call(c=cache(maps=ctypes.addressof(wrong))) == -1
+    assert call(b=batch(max_pages=1 << 23, table_stride=1 << 23), c=cache(n_kv_heads=4096, k_page_stride=1 << 26, v_page_stride=1 << 26),
+                n_q=4096) == -2                        # more key tiles than 32 bits count
     assert call(max_rows=0) == 0                       # nothing to do, nothing launched
     assert call(b=batch(rows=0), max_rows=0, q=rows(ptr=None), o=rows(ptr=None)) == 0
     assert dfl.dflash_paged_attention_workspace_bytes(9, 2, 128, 8) == 0
     assert dfl.dflash_paged_attention_workspace_bytes(8, 2, 96, 8) == 0
+
+
+def test_maps_refusals(L):
+    out = dfl.dflash_paged_maps()
+    for bad, code in BAD_CACHE:
+        assert L.dflash_paged_cache_maps(ref(cache(**bad)), ref(out)) == code, bad
+    assert L.dflash_paged_cache_maps(None, ref(out)) == -1 and L.dflash_paged_cache_maps(ref(cache()), None) == -1
 
 
 def test_logits_refusals(L):

@@ -221,6 +221,31 @@ def test_attention_with_scores_of_hundreds_and_one_key_far_above_the_rest():
     check_attention(p, q, out, lse)
 
 
+def test_attention_makes_the_cache_maps_itself_if_the_caller_keeps_none():
+    import ctypes
+    p = Paged([300, 40], [8, 3], 2, 64, 32, e4m3=True)
+    q = rows_tensor(p.n_rows, 8, 64, BF, 3)
+    want, _, _ = run_attention(p, q)
+    out = torch.zeros_like(q)
+    ws = dfl.workspace(dfl.dflash_paged_attention_workspace_bytes(8, 2, 64, 8))
+    rows = [dfl.dflash_rows(t.data_ptr(), t.stride(0), t.stride(1)) for t in (q, out)]
+    b = dfl.dflash_paged_batch(p.row_start.data_ptr(), p.kv_len.data_ptr(), p.table.data_ptr(), p.width, 2, p.width, p.n_rows)
+    c = p.cache.struct
+    assert not c.maps
+    call = dfl.lib().dflash_paged_attention
+    args = [ctypes.byref(b), 0, 8, ctypes.byref(rows[0]), ctypes.byref(rows[1]), None, 8, 0.125, 1, 0, ws.data_ptr(),
+            ws.numel(), torch.cuda.current_stream().cuda_stream]
+    assert call(ctypes.byref(c), *args) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out), bits(want))
+    # the maps of this cache do for no other
+    other = Paged([300, 40], [8, 3], 2, 64, 32, e4m3=True, seed=1)
+    run_attention(other, q)
+    c.maps = ctypes.addressof(other.cache._maps[1])
+    assert call(ctypes.byref(c), *args) == -1
+    c.maps = None
+
+
 def test_attention_shares_pages_between_requests():
     p = Paged([200, 200, 130], [8, 8, 8], 2, 64, 16)
     p.table_np[1, :8] = p.table_np[0, :8]
