@@ -75,6 +75,7 @@ constexpr int kMT = 128;           // rows of a Q tile
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;      // the workspace has room for so many
 constexpr int kMaxSlots = 12;
+constexpr int kJoinBlocks = 32;    // see paged_join_kernel
 constexpr int kSmem = 227 * 1024;  // all that a CTA may have
 constexpr uint32_t kColO = 256;    // O of stream 0; S of stream s at 128 s
 constexpr float kLn2 = 0.693147180559945309f;
@@ -1139,44 +1140,86 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial results of the item that CTA blockIdx.x of the kernel
-// above started and did not finish: one warp per row, CTAs in order.
+// above started and did not finish.  What bounds it is the latency of a row's
+// loads, one part after another, so a row's n parts are read by 1 to 8 warps,
+// every per-th part each, whose sums are added in order; and a row of the grid
+// has up to kJoinBlocks blocks.  One request of 60,000 keys and one KV head, cut
+// into 152 parts, 8 rows: 56.1 us with one warp to a row, 18.7 so, of which 10.8
+// are the kernel above; 64 rows: 59.7 -> 32.4 (78.9 / 50.7 / 32.4 / 29.9 us with
+// 8 / 16 / 32 / 64 blocks, but a short chunk of a prompt, whose blocks mostly find
+// nothing to do, takes 111.6 / 111.8 / 112.3 / 114.5).
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const KernelArgs k) {
+  __shared__ float red_o[8][HD];
+  __shared__ float red_l[8];
   pdl_enter();
   const int cta = blockIdx.x;
   const Rec rec = k.rec[cta];
   if (rec.pair < 0) return;
   const PagedAttnArgs& a = k.a;
-  const int lane = threadIdx.x & 31, w = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = rec.last_cta - cta + 1;
+  const int per = n > 16 ? 8 : n > 8 ? 4 : n > 4 ? 2 : 1;
+  static_assert(kMaxCtas <= 8 * 32 && kMaxCtas % 32 == 0, "a lane for each of a warp's parts");
+  const int sub = warp & (per - 1), rows = 8 / per;
+  const int mine = (n - sub + per - 1) / per;
+  constexpr int kLoads = 4;
   constexpr int kE = HD / 32;
-  for (int row = w; row < rec.rows; row += 8 * gridDim.y) {
+  for (int base = blockIdx.y * rows; base < rec.rows; base += gridDim.y * rows) {
+    const int row = base + warp / per;
+    const bool have = row < rec.rows;
     auto place = [&](int i) { return (size_t)((cta + i) * 2 + (i ? 0 : rec.slot)) * k.part_rows + row; };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, k.ml[place(i)].x);
-    M = warp_max_f(M);
-    float L = 0.0f, o[kE] = {};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float f = 0.0f;
-      if (i0 + lane < n) {
-        const float2 ml = k.ml[place(i0 + lane)];
-        f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
-        L += f * ml.y;
-      }
-      const int m = min(32, n - i0);
-#pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* p = k.part + place(i0 + i) * HD + lane * kE;
+    float M = -INFINITY, L = 0.0f, o[kE] = {};
+    if (have) {
+      // all that does not depend on M is asked for before it
+      float2 v[kLoads][kE / 2];
+      auto load = [&](int i0) {
 #pragma unroll
-        for (int e = 0; e < kE; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(p + e);
-          o[e] = fmaf(fi, v.x, o[e]);
-          o[e + 1] = fmaf(fi, v.y, o[e + 1]);
+        for (int u = 0; u < kLoads; ++u) {
+          const float* p = k.part + place(sub + min(i0 + u, mine - 1) * per) * HD + lane * kE;
+#pragma unroll
+          for (int e = 0; e < kE; e += 2) v[u][e / 2] = *reinterpret_cast<const float2*>(p + e);
         }
+      };
+      float m[kMaxCtas / 32];
+#pragma unroll
+      for (int i = 0; i < kMaxCtas / 32; ++i) m[i] = i * 32 + lane < n ? k.ml[place(i * 32 + lane)].x : -INFINITY;
+      const float2 ml = lane < mine ? k.ml[place(sub + lane * per)] : make_float2(-INFINITY, 0.0f);
+      load(0);
+#pragma unroll
+      for (int i = 0; i < kMaxCtas / 32; ++i) M = fmaxf(M, m[i]);
+      M = warp_max_f(M);
+      const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+      L = warp_sum(f * ml.y);
+      for (int i0 = 0;;) {
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const float fi = __shfl_sync(0xffffffffu, f, (i0 + u) & 31);
+          if (i0 + u >= mine) break;
+#pragma unroll
+          for (int e = 0; e < kE; e += 2) {
+            o[e] = fmaf(fi, v[u][e / 2].x, o[e]);
+            o[e + 1] = fmaf(fi, v[u][e / 2].y, o[e + 1]);
+          }
+        }
+        if ((i0 += kLoads) >= mine) break;
+        load(i0);
       }
     }
-    L = warp_sum(L);
+    if (per > 1) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) red_o[warp][lane * kE + e] = o[e];
+      if (lane == 0) red_l[warp] = L;
+      __syncthreads();
+      if (sub == 0)
+        for (int i = 1; i < per; ++i) {
+          L += red_l[warp + i];
+#pragma unroll
+          for (int e = 0; e < kE; ++e) o[e] += red_o[warp + i][lane * kE + e];
+        }
+      __syncthreads();
+    }
+    if (!have || sub) continue;
     const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
     const int packed = rec.row0 + row, tok = packed / a.group, g = packed - tok * a.group;
     uint32_t* out = reinterpret_cast<uint32_t*>(
@@ -1268,7 +1311,8 @@ int launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   int rc;
   if ((rc = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmem, s, tk, tv, k))) return rc;
-  return launch_pdl(paged_join_kernel<HD, BF16>, dim3(grid, k.q_tiles * 8), dim3(256), 0, s, k);
+  const int y = (int)min((long long)kJoinBlocks, (long long)a.max_rows * a.group);
+  return launch_pdl(paged_join_kernel<HD, BF16>, dim3(grid, y), dim3(256), 0, s, k);
 }
 
 }  // namespace
