@@ -52,14 +52,20 @@ int check_batch(const dflash_paged_batch* b, const dflash_paged_cache* c) {
   return DFLASH_OK;
 }
 
-int check_rows(const dflash_rows* r, int rows, int heads, int head_dim) {
+// written: every (row, head) has its own place, heads of a row behind one
+// another or rows of a head.
+int check_rows(const dflash_rows* r, int rows, int heads, int head_dim, bool written) {
   if (!r) return DFLASH_ERR_ARG;
   if (rows == 0) return DFLASH_OK;  // nothing is read or written
   if (!r->ptr) return DFLASH_ERR_ARG;
   if (r->row_stride < 0 || r->head_stride < 0 || (heads > 1 && r->head_stride < head_dim) ||
       (rows > 1 && r->row_stride < head_dim))
     return DFLASH_ERR_SHAPE;
+  if (r->row_stride > (1ll << 40) || r->head_stride > (1ll << 40)) return DFLASH_ERR_SHAPE;
   if (!aligned(r->ptr, 16) || r->row_stride % 8 || r->head_stride % 8) return DFLASH_ERR_ALIGN;
+  if (written && rows > 1 && heads > 1 && r->row_stride < (heads - 1) * r->head_stride + head_dim &&
+      (r->head_stride - head_dim) / r->row_stride < rows - 1)
+    return DFLASH_ERR_SHAPE;
   return DFLASH_OK;
 }
 
@@ -95,8 +101,8 @@ int move(bool append, const dflash_paged_cache* cache, const dflash_paged_batch*
   if (rc) return rc;
   if ((rc = check_batch(batch, cache))) return rc;
   if ((rc = check_type(type, cache->format))) return rc;
-  if ((rc = check_rows(k, batch->rows, cache->n_kv_heads, cache->head_dim))) return rc;
-  if ((rc = check_rows(v, batch->rows, cache->n_kv_heads, cache->head_dim))) return rc;
+  if ((rc = check_rows(k, batch->rows, cache->n_kv_heads, cache->head_dim, !append))) return rc;
+  if ((rc = check_rows(v, batch->rows, cache->n_kv_heads, cache->head_dim, !append))) return rc;
   if ((rc = check_workspace(workspace, ws_bytes, kWsHeader))) return rc;
   PagedMoveArgs a;
   a.batch = batch_args(batch, cache);
@@ -171,8 +177,8 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_b
     return DFLASH_ERR_SHAPE;
   if (!(scale > 0.0f) || !std::isfinite(scale * 1.44269504f) || (causal != 0 && causal != 1) || window < 0)
     return DFLASH_ERR_ARG;
-  if ((rc = check_rows(q, batch->rows, n_q_heads, cache->head_dim))) return rc;
-  if ((rc = check_rows(out, batch->rows, n_q_heads, cache->head_dim))) return rc;
+  if ((rc = check_rows(q, batch->rows, n_q_heads, cache->head_dim, false))) return rc;
+  if ((rc = check_rows(out, batch->rows, n_q_heads, cache->head_dim, true))) return rc;
   if (lse && !aligned(lse, 4)) return DFLASH_ERR_ALIGN;
   if ((rc = check_workspace(workspace, ws_bytes,
                             paged_attention_workspace(n_q_heads, cache->n_kv_heads, cache->head_dim, max_rows))))

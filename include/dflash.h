@@ -440,7 +440,9 @@ typedef struct dflash_paged_batch {
 } dflash_paged_batch;
 
 /* A tensor of rows (host struct): [rows, heads, head_dim], head_dim
- * contiguous; 16-byte aligned, strides (in elements) multiples of 8. */
+ * contiguous; 16-byte aligned, strides (in elements) multiples of 8, at least
+ * head_dim.  Rows that are written must not overlap one another, nor anything
+ * else that the call reads or writes. */
 typedef struct dflash_rows {
   void* ptr;
   long long row_stride;
@@ -473,7 +475,7 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  * A row that sees nothing gets out = 0 and lse = -infinity.
  *   type      DFLASH_TYPE_BF16 or _F16: q and out; a 16-bit cache has the same
  *   lse       float32 [rows, n_q_heads] or NULL
- *   max_rows  no request has more new rows than this
+ *   max_rows  no request has more new rows than this; 0: nothing is launched
  *   scale     finite and > 0;  causal 0 or 1;  window >= 0, 0 = none
  * n_q_heads is a multiple of n_kv_heads.  Cache rows that no row of a request
  * sees (behind its length, before its window, in pages it does not list) may
@@ -494,7 +496,7 @@ typedef struct dflash_logit_rules {
   const int32_t* req_slot;    /* [B] row of counts and prompt_mask, NULL: slot(b) = b */
   int slots;                  /* rows of counts and prompt_mask */
   const int32_t* draft;       /* [B, G - 1] the block's drafts; ids outside [0, V) count for nothing */
-  const float* repetition;    /* [B] r > 0 */
+  const float* repetition;    /* [B] r > 0, r and 1 / r normal numbers */
   const float* frequency;     /* [B] f */
   const float* presence;      /* [B] p */
   const int32_t* bias_start;  /* [B + 1] request b's biases: entries bias_start[b] .. bias_start[b + 1] - 1 */

@@ -103,6 +103,24 @@ def test_attention_refusals(L):
     assert dfl.dflash_paged_attention_workspace_bytes(8, 2, 96, 8) == 0
 
 
+def test_rows_that_would_be_written_twice_are_refused(L):
+    """20 rows of 2 heads of 128, and of 10 heads for attention."""
+    for n_q, f in ((2, "gather k"), (2, "gather v"), (10, "attention")):
+        span = (n_q - 1) * 128 + 128
+        tight = 19 * 128 + 128
+        for r, h, ok in ((span, 128, True), (span - 8, 128, False), (128, tight, True), (128, tight - 8, False), (128, 128, False),
+                         (256, 19 * 256 + 128, True), (256, 19 * 256 + 120, False), (1 << 41, 128, False), (128, 1 << 41, False)):
+            x, y = rows(row_stride=r, head_stride=h), rows(row_stride=2048)
+            if f == "attention":    # no workspace: a layout that passes is refused for that
+                code = L.dflash_paged_attention(ref(cache()), ref(batch()), 0, n_q, ref(y), ref(x), None, 8, 0.1, 1, 0, None, 0, None)
+            else:
+                kv = (x, y) if f == "gather k" else (y, x)
+                code = L.dflash_paged_gather(ref(cache()), ref(batch()), 0, ref(kv[0]), ref(kv[1]), None, 0, None)
+            assert code == (-7 if ok else -2), (f, r, h)
+    same = rows(row_stride=128, head_stride=128)       # rows that are only read may lie anywhere
+    assert L.dflash_paged_append(ref(cache()), ref(batch()), 0, ref(same), ref(same), None, 0, None) == -7
+
+
 def test_maps_refusals(L):
     out = dfl.dflash_paged_maps()
     for bad, code in BAD_CACHE:
