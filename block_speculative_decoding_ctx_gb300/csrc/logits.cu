@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kLT, 4) logits_adjust_kernel(const LogitsArgs 
     if (!VEC) seen |= ((__shfl_sync(0xffffffffu, prompts, k) >> lane) & 1u) << k;
 #pragma unroll
     for (int e = 0; e < kStep; ++e) {
-      off[k + e] = c[e] > 0 ? w.f * (float)c[e] + w.p : 0.0f;
+      off[k + e] = w.f * (float)c[e] + (c[e] > 0 ? w.p : 0.0f);
       if (c[e] > 0) seen |= 1u << (k + e);
     }
   }

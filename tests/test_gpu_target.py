@@ -441,6 +441,31 @@ def test_logits_adjust_masks_everything_and_keeps_infinities():
         np.testing.assert_array_equal(to64(out[b, i]), to64(z[b, i]))
 
 
+@pytest.mark.parametrize("V", [700, 701])
+def test_logits_adjust_takes_negative_counts_by_the_formula_whoever_computes_an_id(V):
+    """Every id through the chunk's pass, and again with each named by a bias
+    of 0: the same bits, and the formula's values."""
+    G = 3
+    z = torch.randn(1, G, V, device="cuda")
+    counts = torch.arange(V, dtype=torch.int32, device="cuda").reshape(1, V) % 7 - 3
+    par = dict(repetition=torch.tensor([1.25], device="cuda"), frequency=torch.tensor([0.5], device="cuda"),
+               presence=torch.tensor([0.75], device="cuda"))
+    ws = dfl.workspace(dfl.dflash_logits_adjust_workspace_bytes())
+    out, again = torch.empty_like(z), torch.empty_like(z)
+    dfl.dflash_logits_adjust(z, out, ws, counts=counts, **par)
+    dfl.dflash_logits_adjust(z, again, ws, counts=counts, bias_start=torch.tensor([0, V], dtype=torch.int32, device="cuda"),
+                             bias_ids=torch.arange(V, dtype=torch.int32, device="cuda"), bias_vals=torch.zeros(V, device="cuda"), **par)
+    torch.cuda.synchronize()
+    assert dfl.dflash_read_status(ws) == 0
+    assert torch.equal(out, again)
+    c, l = to64(counts)[0], to64(z)[0]
+    l1 = np.where(c > 0, np.where(l > 0, l / 1.25, l * 1.25), l)
+    want = l1 - (0.5 * c + 0.75 * (c > 0))
+    # at most two roundings of the quotient and one each of the two others
+    size = np.abs(l1) + 0.5 * np.abs(c) + 0.75
+    assert (np.abs(to64(out)[0] - want) <= 4 * 2.0 ** -24 * size).all()
+
+
 def test_logits_adjust_reports_bad_slots_and_ids():
     B, G, V = 3, 2, 100
     z = torch.randn(B, G, V, device="cuda")
