@@ -200,6 +200,17 @@ def test_attention_parity(lens, rows, n_q, n_kv, hd, page, dtype, e4m3, causal, 
     check_attention(p, q, out, lse, causal, window)
 
 
+@pytest.mark.parametrize("length", [300, 900, 1500, 2600, 4100, 20000])
+@pytest.mark.parametrize("rows,n_q,hd,dtype,e4m3", [(1, 3, 128, BF, False), (9, 5, 64, FH, True), (50, 4, 128, BF, True)])
+def test_attention_joins_a_request_cut_into_few_and_many_parts(length, rows, n_q, hd, dtype, e4m3):
+    """One KV head: its key tiles, 3 to 157 of them, are all there is to cut."""
+    p = Paged([length], [rows], 1, hd, 64, dtype, e4m3, seed=length)
+    q = rows_tensor(p.n_rows, n_q, hd, dtype, 3, extra=1, size=1.5)
+    out, lse, status = run_attention(p, q)
+    assert status == 0
+    check_attention(p, q, out, lse)
+
+
 def test_attention_without_lse_and_with_another_scale():
     p = Paged([400], [20], 2, 64, 32)
     q = rows_tensor(p.n_rows, 6, 64, BF, 3)
