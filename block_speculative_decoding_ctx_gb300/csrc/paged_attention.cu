@@ -873,7 +873,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows past the item's do not ask for masking
       const int hi = !real ? 1 << 30 : a.causal ? min(it.len, pos + 1) : it.len;
       const int lo = real && a.window ? pos - a.window + 1 : -(1 << 30);
-      const float cs = real ? a.scale_log2 * (E4M3 ? x0[t] : 1.0f) : 0.0f;
+      // (a row of tiny queries and a tiny scale: not 0, which a masked score,
+      // -infinity, would turn into NaN)
+      const float cs = !real ? 0.0f : E4M3 ? fmaxf(a.scale_log2 * x0[t], 0x1p-126f) : a.scale_log2;
 
       float m_ref = -INFINITY, l = 0.0f;
       float vref = 0.0f, cv = 0.0f;  // E4M3: reference of the value scales, log2 of the weights' factor

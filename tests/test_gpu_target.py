@@ -219,6 +219,18 @@ def test_attention_without_lse_and_with_another_scale():
     check_attention(p, q, out, None, scale=0.7)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_of_queries_that_are_zero_under_a_tiny_scale(e4m3):
+    """All scores vanish: the plain mean of what a row sees, masked keys out."""
+    p = Paged([200, 9], [70, 9], 2, 64, 16, e4m3=e4m3)
+    q = rows_tensor(p.n_rows, 4, 64, BF, 3)
+    q[::2] = 0
+    for scale in (1e-9, 1e-30):
+        out, lse, status = run_attention(p, q, scale=scale)
+        assert status == 0
+        check_attention(p, q, out, lse, scale=scale)
+
+
 def test_attention_with_scores_of_hundreds_and_one_key_far_above_the_rest():
     """The running maximum grows late and by a lot; scores reach far beyond
     what exp holds."""
