@@ -14,9 +14,11 @@
 // l) in the workspace, which a second kernel joins in CTA order.  The cut
 // depends on the lengths alone, so results are the same on every run.
 //
-// Inside a CTA two streams of jobs (Q tile of 128 rows x key tile) run side by
-// side, each with its own S and O in tensor memory and its own softmax
-// warpgroup, so that one's softmax runs under the other's products:
+// Inside a CTA two streams of jobs (Q tile of 128 rows x half a key tile, 64
+// keys) run side by side, each with its own S and O in tensor memory and its
+// own softmax warpgroup, so that one's softmax runs under the other's products,
+// and a stream's scores of one half are made while the other half is weighed
+// (prompt chunk: 992 us with whole tiles of 128 keys, 925 so):
 //   an item of more than 128 rows: its two Q tiles, both over every key tile
 //     (each K/V byte feeds 256 rows);
 //   a smaller one: even and odd key tiles of its one Q tile, joined at the end.
@@ -27,7 +29,9 @@
 //               phase of its barriers in turn.  (One ring for both streams of a
 //               smaller item would not do: loads may land out of order, and a
 //               wait whose previous phase is still open returns at once.)
-//   warps 1, 2  issue their stream's S = Q K^T (both from shared memory) and
+//   warps 1, 2  issue their stream's S = Q K^T (both from shared memory; a warp
+//               for both streams made each wait for the other's: blocks of 8
+//               203 us against 178) and
 //               O += P V (P from tensor memory, V MN-major as TMA left it), and
 //               zero the V rows that no row of the item sees (a weight of 0
 //               times whatever lies there must not become NaN)
@@ -35,8 +39,8 @@
 //               stream 1.  P overwrites S in place.  O is rescaled only when a
 //               row's reference grows by more than a headroom, a few times a
 //               row.
-// Tensor memory: S0 | S1 | O0 | O1, 128 columns each, all 512 of it; the
-// shared memory of a CTA keeps any other off its SM.
+// Tensor memory: S0 | S1 | O0 | O1, 128 columns each (S two halves of 64), all
+// 512 of it; the shared memory of a CTA keeps any other off its SM.
 //
 // E4M3 caches: the codes go to the tensor cores as they lie in the cache
 // (kind::f8f6f4, twice the rate of 16 bits).  The other operand is a sum of
@@ -51,9 +55,22 @@
 // float32; a weight is taken relative to the largest value scale so far and
 // times 2^8, so its terms reach 2^-24 of the largest weight.
 //
-// All waits are bounded (mbar_wait_bounded).  When one gives up, the softmax
-// and widening warps run on without waiting (their barriers stay matched,
-// results are void, the status word says so) and the CTA ends as usual.
+// All waits are bounded.  When one gives up, the softmax warps run on without
+// waiting (their barriers stay matched, results are void, the status word says
+// so) and the CTA ends as usual.
+//
+// What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16):
+//   32 requests, blocks of 8, context 8,192: HBM.  171 us for 1.08 GB, 6.3 TB/s,
+//     0.93 of the measured copy;
+//   the same over an E4M3 cache: 187 us for 0.56 GB.  Softmax: scales, two
+//     products more per weight and the terms of P; 124 us with the softmax
+//     taken out, 24 us of it the terms, 20 the barriers and scale loads;
+//   prompt chunk, 2 x 2,048 rows, context up to 16,384: the tensor cores under
+//     the power limit, 911 us, 1.32 PFLOP/s at 1.75 GHz and 1,390 W, 0.77 of
+//     what a library product sustains;
+//   one token, context 1,000: latency.  12 us, of them 6 in this kernel (setting up
+//     0.7, finding its part 1.2, queries to the last weights 2.6, the end 1.8), 2
+//     in the join.
 #include <atomic>
 #include <cstddef>
 #include <mutex>
@@ -95,7 +112,7 @@ struct KernelArgs {
   int rts;        // items per request at most
   int part_rows;  // 128 or 256
   int half;       // slots of each of the two rings
-  int seg_cost;   // what beginning an item costs, in key tiles
+  int seg_cost;   // what beginning an item costs, in key tiles (launch)
   int q_tiles;    // Q tiles in shared memory
 };
 
@@ -390,9 +407,12 @@ struct Cfg {
   static constexpr int kPTerms = E4M3 ? (BF16 ? 3 : 4) : 1;
   static constexpr int kQTile = kMT * kRow * kQTerms;
   // Growth of a row's reference (log2) before O is rescaled: as much as the
-  // weights' type holds beside the factors on them (fp16 to 2^15; a bf16 has
-  // float32's exponents, so there only sums must stay finite).
-  static constexpr float kHeadroom = E4M3 ? 6.0f : BF16 ? 60.0f : 15.0f;
+  // weights' type holds beside the factors on them (fp16 to 2^15: E4M3 has 2^8
+  // and up to 2 of a value scale there).  A bf16 has float32's exponents, so
+  // that only the sums of weights and values must stay finite: 2^30 leaves
+  // values up to 2^80 for 2^18 keys (mid-size prompt chunk: 112.7 us with
+  // 2^60, 112.9 with 2^30, 115.4 with 2^15).
+  static constexpr float kHeadroom = E4M3 ? 6.0f : BF16 ? 30.0f : 15.0f;
   // Operand layouts.  A row of K or Q is kRow bytes cut into spans of at most
   // 128; a span of all rows is one swizzled tile (128-byte swizzle, or 64 for
   // 64-byte rows), spans kKT x span bytes apart.
@@ -1309,6 +1329,11 @@ int launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
   k.part_rows = part_rows(a.group, a.max_rows);
   k.q_tiles = k.part_rows / kMT;
   k.half = min(kMaxSlots, (kSmem - kCtrlBytes<E4M3> - k.q_tiles * C::kQTile) / C::kTile) / 2;
+  // Cost of an item beside its tiles, for the cut of the line: setting out, the
+  // queries (terms of them for E4M3), the end.  Of 0 / 1 / 2 / 4 / 8 tiles: ragged
+  // E4M3 blocks 294 / 267 / 253 / 217 / 196 us; bf16 prompt chunks of 200 to 700
+  // 126 / 124 / 116 / 113 / 112; 64 single tokens over 500 keys 41.3 / 39.7 / 40.0 /
+  // 40.5 / 41.5.
   k.seg_cost = E4M3 ? 8 : 4;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   int rc;

@@ -10,6 +10,12 @@
 // way: 32 bytes each on the 16-bit side and 32 or 16 on the cache's, so that 8
 // or 4 neighbouring threads hold a whole row of head_dim values and find its
 // largest magnitude with shuffles.
+//
+// Measured on GB300 (8 KV heads of 128), bytes at the measured copy's rate in
+// brackets: E4M3 prefixes read back (776 MB) 119 us [0.96]; 16-bit prompts
+// written 57 us [0.92]; the same quantised on the way (274 MB) 59 us [0.69],
+// which the instructions of the quotients and conversions bound (65% of the
+// issue slots); a step's 256 rows 8 us, latency.
 #include <cuda_fp8.h>
 
 #include "paged_util.cuh"
@@ -19,8 +25,11 @@ namespace {
 
 constexpr int kMoveThreads = 256;
 constexpr float kE4M3Max = 448.0f;
+// Pieces of a thread on their way: 1 / 2 / 4 take 65 / 59 / 73 us to quantise
+// prompts and 123 / 119 / 124 to read prefixes back.
 constexpr int kPieces = 2;
-// Pieces of one block, and the number of blocks (4 for each of 152 SMs) that
+// Pieces of one block (128 / 256 / 512: prompts 60.4 / 58.6 / 60.5 us, prefixes
+// 120.6 / 119.3 / 123.0), and the number of blocks (4 for each of 152 SMs) that
 // comes first: a step's few rows are spread over as many.
 constexpr int kMostUnits = 256, kBlocks = 608;
 
