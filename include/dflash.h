@@ -475,7 +475,8 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  * A row that sees nothing gets out = 0 and lse = -infinity.
  *   type      DFLASH_TYPE_BF16 or _F16: q and out; a 16-bit cache has the same
  *   lse       float32 [rows, n_q_heads] or NULL
- *   max_rows  no request has more new rows than this; 0: nothing is launched
+ *   max_rows  no request has more new rows than this; at most `rows`; 0: nothing
+ *             is launched
  *   scale     finite and > 0;  causal 0 or 1;  window >= 0, 0 = none
  * n_q_heads is a multiple of n_kv_heads.  Cache rows that no row of a request
  * sees (behind its length, before its window, in pages it does not list) may

@@ -164,6 +164,21 @@ def test_pages_past_2_to_31_elements():
         assert (out.double() - want).abs().max() <= 2.0 ** -6 * v2.abs().max()
 
 
+def test_a_batch_without_new_rows():
+    p = Paged([40, 7], [0, 0], 2, 64, 16)
+    x = torch.empty(0, 2, 64, dtype=BF, device="cuda")
+    before = p.host()
+    ws = dfl.workspace(dfl.dflash_paged_attention_workspace_bytes(4, 2, 64, 0))
+    dfl.dflash_paged_append(p.cache, x, x, *p.batch, ws)
+    dfl.dflash_paged_gather(p.cache, x, x.clone(), *p.batch, ws)
+    q = torch.empty(0, 4, 64, dtype=BF, device="cuda")
+    dfl.dflash_paged_attention(p.cache, q, q.clone(), *p.batch, 0, ws)
+    torch.cuda.synchronize()
+    assert dfl.dflash_read_status(ws) == 0
+    for x0, x1 in zip(before[:2], p.host()[:2]):
+        np.testing.assert_array_equal(x0, x1)
+
+
 # --------------------------------------------------------------- attention
 
 def rid(v):
