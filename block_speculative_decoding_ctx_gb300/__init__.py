@@ -12,6 +12,7 @@ import ctypes
 import os
 import re
 import struct
+import threading
 
 import torch
 
@@ -390,6 +391,9 @@ _PACK_BATCH = struct.Struct("@PPPqiii4x").pack
 _PACK_RULES = struct.Struct("@PPPiPPPPPPPiP").pack
 
 
+_maps_lock = threading.Lock()
+
+
 class PagedCache:
     """One layer's paged cache (see paged_cache); keeps its tensors alive."""
 
@@ -403,12 +407,14 @@ class PagedCache:
 
     def _with_maps(self):
         """The struct's bytes with the descriptors that attention needs, made
-        at the first call."""
-        maps = dflash_paged_maps()
-        _check(lib().dflash_paged_cache_maps(self._bytes, ctypes.byref(maps)), "dflash_paged_cache_maps")
-        c = dflash_paged_cache.from_buffer_copy(self._bytes)
-        c.maps = ctypes.addressof(maps)
-        self._maps = (bytes(c), maps)
+        once: another thread's call may be reading them."""
+        with _maps_lock:
+            if self._maps is None:
+                maps = dflash_paged_maps()
+                _check(lib().dflash_paged_cache_maps(self._bytes, ctypes.byref(maps)), "dflash_paged_cache_maps")
+                c = dflash_paged_cache.from_buffer_copy(self._bytes)
+                c.maps = ctypes.addressof(maps)
+                self._maps = (bytes(c), maps)
         return self._maps[0]
 
 

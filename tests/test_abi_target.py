@@ -128,6 +128,28 @@ def test_maps_refusals(L):
     assert L.dflash_paged_cache_maps(None, ref(out)) == -1 and L.dflash_paged_cache_maps(ref(cache()), None) == -1
 
 
+def test_maps_of_a_cache_are_made_once_however_many_threads_ask(monkeypatch):
+    """The address of one thread's maps must not be another's to free."""
+    import threading
+    import time
+    made = []
+
+    class Slow:
+        def dflash_paged_cache_maps(self, cache, maps):
+            time.sleep(0.05)
+            made.append(maps)
+            return 0
+    monkeypatch.setattr(dfl, "lib", lambda: Slow())
+    c = dfl.PagedCache(cache(), (), 0)
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(c._with_maps())) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(made) == 1 and len(got) == 4 and all(g is got[0] for g in got)
+
+
 def test_logits_refusals(L):
     def call(B=2, G=4, V=100, t=2, z=P(1 << 20), l=(400, 100), out=P(1 << 22), o=(400, 100), ws=FAKE, n=256, none=False, **r):
         rules = dfl.dflash_logit_rules(**r)
