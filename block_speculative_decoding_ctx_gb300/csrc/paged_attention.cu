@@ -46,8 +46,12 @@
 // (kind::f8f6f4, twice the rate of 16 bits).  The other operand is a sum of
 // 8-bit terms that holds what 16 bits would:
 //   Q, times a power of two per row that brings its largest value to
-//     [128, 256), as E4M3 terms of 4 bits each: 2 for bf16, 3 for fp16, exact
-//     but for parts below 2^-18 of the row's largest;
+//     [128, 256), as an E4M3 term of 4 bits and E5M2 ones of 3 bits, 1 for
+//     bf16 and 2 for fp16, each rounded to nearest.  That is exact for values
+//     of at least 2^-6.  Of a smaller one the first term leaves up to 2^-10
+//     and each further one an eighth of what it finds, down to 2^-17: all in
+//     all 2^-13 for bf16 and 2^-16 for fp16, 2^-20 and 2^-23 of the row's
+//     largest.  (E4M3 terms throughout leave 2^-17 of it.)
 //   P as E5M2 terms of 3 bits each, cut from its fp16 value (an E5M2 is the
 //     upper byte of an fp16): 3 for bf16 outputs (9 bits, one more than a bf16
 //     weight), 4 for fp16 (all 11); exact down to 2^-16 absolute.
@@ -428,7 +432,9 @@ struct Cfg {
   }
   static constexpr uint32_t kDescHi = (uint32_t)((8 * kSpan) >> 4) | (1u << 14) | ((kSpan == 64 ? 4u : 2u) << 29);
   static constexpr uint32_t kVDescLo = (uint32_t)((kKT * kSpan) >> 4) << 16;  // next span of V along N
-  static constexpr uint32_t kIdQk = E4M3 ? idesc_f8(kMT, kHK, 0) : idesc_f32acc(kMT, kHK, BF16);
+  static __host__ __device__ constexpr uint32_t id_qk(int term) {
+    return E4M3 ? idesc_f8(kMT, kHK, term > 0) : idesc_f32acc(kMT, kHK, BF16);
+  }
   static constexpr uint32_t kIdPv = (E4M3 ? idesc_f8(kMT, HD, 1) : idesc_f32acc(kMT, HD, BF16)) | (1u << 16);  // V MN-major
 };
 
@@ -496,8 +502,10 @@ __device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, i
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-          const float2 y = unpack16<false>(e4m3x2_to_f16x2((uint16_t)c[i]));
+          c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE,
+                                          term ? __NV_E5M2 : __NV_E4M3);
+          // an E5M2 is the upper byte of an fp16
+          const float2 y = unpack16<false>(term ? __byte_perm(c[i], 0u, 0x1404) : e4m3x2_to_f16x2((uint16_t)c[i]));
           x[2 * i] -= y.x;
           x[2 * i + 1] -= y.y;
         }
@@ -760,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int kk = 0; kk < C::kQkSteps; ++kk) {
                 const uint32_t off = (kk / C::kStepsPerSpan) * ((kKT * C::kSpan) >> 4) + (kk % C::kStepsPerSpan) * 2;
                 mma_ss<E4M3>(tS + h * kHK, desc64(qd + term * ((kMT * C::kRow) >> 4) + off, C::kDescHi),
-                             desc64(kd + off, C::kDescHi), C::kIdQk, term > 0 || kk > 0);
+                             desc64(kd + off, C::kDescHi), C::id_qk(term), term > 0 || kk > 0);
               }
             tc_commit(&c->s_full[st][h]);
             if (h) give_back(&k_empty[ks]);

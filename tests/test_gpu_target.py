@@ -234,6 +234,33 @@ def test_attention_without_lse_and_with_another_scale():
     check_attention(p, q, out, None, scale=0.7)
 
 
+@pytest.mark.parametrize("dtype,left", [(BF, 2.0 ** -13), (FH, 2.0 ** -16)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_over_codes_keeps_queries_far_below_the_largest_of_their_row(dtype, left, hd):
+    """Each row sees one key, so lse is its score.  The largest query, 192,
+    meets a key of 0; all the others are below 2^-10.  As 8-bit terms a query
+    may lose `left` (largest in [128, 256)); beside that, hd products are
+    summed, 2 half steps each, and the scale and the logarithm take a few."""
+    n = 12
+    p = Paged([1] * n, [1] * n, 1, hd, 16, dtype, True, seed=4, garbage=False)
+    codes = p.pages[0].view(torch.uint8)
+    codes &= 0x7F                                     # positive keys
+    codes[..., 0] = 0
+    q = rows_tensor(n, 2, hd, dtype, 5)
+    q.copy_((0.45 + 0.45 * torch.rand(q.shape, device="cuda")) * 2.0 ** -10)
+    q[..., 0] = 192
+    out, lse, status = run_attention(p, q, scale=1.0)
+    assert status == 0
+    kp, _, ks, _ = p.host()
+    e = 2.0 ** -24
+    for b in range(n):
+        k = ot.sequence(kp, ks, p.table_np[b], 1, 16, True)[0, 0]
+        want = to64(q)[b] @ k
+        bound = left * k.sum() + (2 * (hd + 4) + 8) * e * np.abs(want) + 8 * e
+        assert (np.abs(to64(lse)[b] - want) <= bound).all()
+        assert (bound < 0.5 * want).all()             # what terms of 4 bits alone would lose
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_attention_of_queries_that_are_zero_under_a_tiny_scale(e4m3):
     """All scores vanish: the plain mean of what a row sees, masked keys out."""
