@@ -257,7 +257,7 @@ struct Ctrl {
 };
 template <bool E4M3>
 constexpr int kCtrlBytes = (int)((sizeof(Ctrl<E4M3>) + 1023) / 1024 * 1024);
-static_assert(kCtrlBytes<false> <= 3072, "control block: six 32 KiB slots beside one Q tile");
+static_assert(kCtrlBytes<false> <= 3 * 1024, "control block: six 32 KiB slots beside one Q tile");
 
 // -------------------------------------------------------------- PTX helpers
 
