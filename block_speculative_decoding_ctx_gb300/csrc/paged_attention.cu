@@ -74,7 +74,9 @@
 //     what a library product sustains;
 //   one token, context 1,000: latency.  12 us, of them 6 in this kernel (setting up
 //     0.7, finding its part 1.2, queries to the last weights 2.6, the end 1.8), 2
-//     in the join.
+//     to 4 in the join.
+//   Where most items are cut the join is a share: 15 of 113 us for prompt chunks
+//     of 200 to 700 rows, 8 of 24 for short windowed ones.
 #include <atomic>
 #include <cstddef>
 #include <mutex>
