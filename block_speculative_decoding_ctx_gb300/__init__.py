@@ -540,6 +540,8 @@ def dflash_paged_attention(cache, q, out, row_start, kv_len, page_table, max_row
         raise ValueError(f"q and out: expected [rows, n_q_heads, {hd}] of one type")
     if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise ValueError(f"no rows of {q.dtype}")
+    if not (0 <= max_rows < 1 << 31 and 0 <= window < 1 << 31):
+        raise ValueError(f"max_rows and window: expected 0 to 2^31 - 1, got {max_rows} and {window}")
     stream = _current(index, stream)
     maps = cache._maps
     code = lib().dflash_paged_attention(

@@ -190,3 +190,12 @@ def test_binding_checks_shapes_and_types():
         dfl.dflash_paged_append(c, torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 64, dtype=torch.bfloat16),
                                 torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int64),
                                 torch.zeros(1, 1, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("window,max_rows", [(1 << 32, 1), ((1 << 32) + 5, 1), (-1, 1), (0, (1 << 32) + 1), (0, -1)])
+def test_binding_refuses_what_a_c_int_does_not_hold(window, max_rows):
+    """ctypes would pass the lower 32 bits on: another window."""
+    c = dfl.PagedCache(cache(), (), 0)
+    q = torch.zeros(1, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="max_rows and window"):
+        dfl.dflash_paged_attention(c, q, q.clone(), None, None, None, max_rows, None, window=window)
