@@ -53,8 +53,9 @@
 //     all 2^-13 for bf16 and 2^-16 for fp16, 2^-20 and 2^-23 of the row's
 //     largest.  (E4M3 terms throughout leave 2^-17 of it.)
 //   P as E5M2 terms of 3 bits each, cut from its fp16 value (an E5M2 is the
-//     upper byte of an fp16): 3 for bf16 outputs (9 bits, one more than a bf16
-//     weight), 4 for fp16 (all 11); exact down to 2^-16 absolute.
+//     upper byte of an fp16): 3 for bf16 outputs (9 bits at least, one more
+//     than a bf16 weight: off by 7e-4 rms where that is off by 1.7e-3), 4 for
+//     fp16 (all 11); exact down to 2^-16 absolute.
 // The key scale multiplies the score and the value scale the weight, both in
 // float32; a weight is taken relative to the largest value scale so far and
 // times 2^8, so its terms reach 2^-24 of the largest weight.
@@ -1071,10 +1072,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!E4M3) {
               tmem_st(ta + q * 32, pw);
             } else {
-              // three terms keep 9 bits: round there first (positive values)
+              // Three terms hold the upper 9 of fp16's 11 bits, more where
+              // zeros follow a term.  Cut off like that the weights would be
+              // 3.2e-4 too small on average, with a unit in the last place
+              // added first 3.8e-4 too large: every other key has it added
+              // (positive values; rounding to 9 bits by adding half of the
+              // last, without clearing what is behind it, made all 1.1e-3 too
+              // large).
               if (C::kPTerms == 3) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) pw[e] += 0x00020002u;
+                for (int e = 0; e < 16; ++e) pw[e] += 0x00010000u;
               }
 #pragma unroll
               for (int term = 0; term < C::kPTerms; ++term) {

@@ -9,7 +9,7 @@ import torch
 
 import block_speculative_decoding_ctx_gb300 as dfl
 from oracle import target as ot
-from target_testutil import (F8, Paged, attention_reference, check_attention, rows_tensor, run_attention,
+from target_testutil import (HALF_STEP, F8, Paged, attention_reference, check_attention, rows_tensor, run_attention,
                              to64)
 
 pytestmark = pytest.mark.gpu
@@ -259,6 +259,25 @@ def test_attention_over_codes_keeps_queries_far_below_the_largest_of_their_row(d
         bound = left * k.sum() + (2 * (hd + 4) + 8) * e * np.abs(want) + 8 * e
         assert (np.abs(to64(lse)[b] - want) <= bound).all()
         assert (bound < 0.5 * want).all()             # what terms of 4 bits alone would lose
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_outputs_are_not_too_large_or_small_on_average(dtype, e4m3):
+    """Roundings of weights and outputs go either way.  A rounding's error is
+    evenly spread over half a step, its mean over the 1,024 softmaxes of this
+    call about 0.6 u / 32, u / 50 a standard deviation for the weights and less
+    for the outputs.  Over codes the weights of one key, which many rows may
+    heed most, lean by up to 3.8e-4 one way, u / 10 in bf16.  Within u / 8 of
+    the formula's size, then, whichever type."""
+    p = Paged([500, 300], [128, 128], 4, 128, 64, dtype, e4m3, seed=8, garbage=False)
+    q = rows_tensor(p.n_rows, 4, 128, dtype, 3)
+    out, lse, status = run_attention(p, q, causal=False)
+    assert status == 0
+    check_attention(p, q, out, lse, causal=False)
+    want = attention_reference(p, q, False, 0, 128 ** -0.5)[0]
+    got = to64(out)
+    assert abs((got * want).sum() / (want * want).sum() - 1.0) <= HALF_STEP[dtype] / 8
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
