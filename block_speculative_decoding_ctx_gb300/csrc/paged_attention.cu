@@ -415,11 +415,14 @@ struct Cfg {
   static constexpr int kQTile = kMT * kRow * kQTerms;
   // Growth of a row's reference (log2) before O is rescaled: as much as the
   // weights' type holds beside the factors on them (fp16 to 2^15: E4M3 has 2^8
-  // and up to 2 of a value scale there).  A bf16 has float32's exponents, so
-  // that only the sums of weights and values must stay finite: 2^30 leaves
-  // values up to 2^80 for 2^18 keys (mid-size prompt chunk: 112.7 us with
-  // 2^60, 112.9 with 2^30, 115.4 with 2^15).
+  // and up to 2 of a value scale there).  A bf16 has float32's exponents (mid-size
+  // prompt chunk: 112.7 us with 2^60, 112.9 with 2^30, 115.4 with 2^15).
   static constexpr float kHeadroom = E4M3 ? 6.0f : BF16 ? 30.0f : 15.0f;
+  // log2 of the factor on the weights.  A bf16 weight is at most 1, whatever its
+  // reference has grown by since, so that the sums of weights and values stay
+  // finite as far as the formula's do (2^30 let values above 2^80 overflow); what
+  // is lost for it lies 2^96 below the largest.
+  static constexpr float kShift = !E4M3 && BF16 ? -kHeadroom : 0.0f;
   // Operand layouts.  A row of K or Q is kRow bytes cut into spans of at most
   // 128; a span of all rows is one swizzled tile (128-byte swizzle, or 64 for
   // 64-byte rows), spans kKT x span bytes apart.
@@ -909,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float cs = !real ? 0.0f : E4M3 ? fmaxf(a.scale_log2 * x0[t], 0x1p-126f) : a.scale_log2;
 
       float m_ref = -INFINITY, l = 0.0f;
-      float vref = 0.0f, cv = 0.0f;  // E4M3: reference of the value scales, log2 of the weights' factor
+      float vref = 0.0f, cv = C::kShift;  // E4M3: reference of the value scales; log2 of the weights' factor
       const int step = s.split ? 2 : 1, j0 = s.split ? wg : 0, nt = s.nt, t0 = s.t0;
       // E4M3: scales of key t of the next tile, and the page of the one after
       // it, so that neither load is waited for in its own tile

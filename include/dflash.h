@@ -481,7 +481,9 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  * n_q_heads is a multiple of n_kv_heads.  Cache rows that no row of a request
  * sees (behind its length, before its window, in pages it does not list) may
  * hold anything, NaN included.  A visible row that is not finite makes the
- * outputs of that request and KV head undefined, no other's. */
+ * outputs of that request and KV head undefined, no other's.  Sums are float32:
+ * bf16 values of any finite size do, but what adds less than 2^-96 to an output
+ * may be lost. */
 size_t dflash_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim,
                                               int max_rows);
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_batch* batch,
