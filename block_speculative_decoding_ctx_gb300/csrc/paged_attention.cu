@@ -33,8 +33,8 @@
 //               for both streams made each wait for the other's: blocks of 8
 //               203 us against 178) and
 //               O += P V (P from tensor memory, V MN-major as TMA left it), and
-//               zero the V rows that no row of the item sees (a weight of 0
-//               times whatever lies there must not become NaN)
+//               (16-bit caches) zero the V rows that no row of the item sees (a
+//               weight of 0 times whatever lies there must not become NaN)
 //   warps 4-7   softmax of stream 0, one query row per thread; warps 8-11
 //               stream 1.  P overwrites S in place.  O is rescaled only when a
 //               row's reference grows by more than a headroom, a few times a
@@ -42,23 +42,27 @@
 // Tensor memory: S0 | S1 | O0 | O1, 128 columns each (S two halves of 64), all
 // 512 of it; the shared memory of a CTA keeps any other off its SM.
 //
-// E4M3 caches: the codes go to the tensor cores as they lie in the cache
-// (kind::f8f6f4, twice the rate of 16 bits).  The other operand is a sum of
-// 8-bit terms that holds what 16 bits would:
-//   Q, times a power of two per row that brings its largest value to
-//     [128, 256), as an E4M3 term of 4 bits and E5M2 ones of 3 bits, 1 for
-//     bf16 and 2 for fp16, each rounded to nearest.  That is exact for values
-//     of at least 2^-6.  Of a smaller one the first term leaves up to 2^-10
-//     and each further one an eighth of what it finds, down to 2^-17: all in
-//     all 2^-13 for bf16 and 2^-16 for fp16, 2^-20 and 2^-23 of the row's
-//     largest.  (E4M3 terms throughout leave 2^-17 of it.)
-//   P as E5M2 terms of 3 bits each, cut from its fp16 value (an E5M2 is the
-//     upper byte of an fp16): 3 for bf16 outputs (9 bits at least, one more
-//     than a bf16 weight: off by 7e-4 rms where that is off by 1.7e-3), 4 for
-//     fp16 (all 11); exact down to 2^-16 absolute.
-// The key scale multiplies the score and the value scale the weight, both in
-// float32; a weight is taken relative to the largest value scale so far and
-// times 2^8, so its terms reach 2^-24 of the largest weight.
+// E4M3 caches.  The scores' products take the codes as they lie in the cache
+// (kind::f8f6f4, twice the rate of 16 bits); Q, times a power of two per row
+// that brings its largest value to [128, 256), is a sum of an E4M3 term of 4
+// bits and E5M2 ones of 3 bits, 1 for bf16 and 2 for fp16, each rounded to
+// nearest.  That is exact for values of at least 2^-6.  Of a smaller one the
+// first term leaves up to 2^-10 and each further one an eighth of what it finds,
+// down to 2^-17: all in all 2^-13 for bf16 and 2^-16 for fp16, 2^-20 and 2^-23 of
+// the row's largest.  (E4M3 terms throughout leave 2^-17 of it.)  The key scale
+// multiplies the score in float32.
+//   The weights, times the value scales in float32, need the exponents of a
+// float32: a first position that takes nine tenths of a row over 131,072 keys
+// leaves the others 2^-20 of its weight, a value row much larger than the rest
+// pushes them further down, and all of them together are the output.  (Sums of
+// E5M2 terms end at 2^-24 of the reference; such outputs came out a tenth too
+// small and worse.)  So they are bf16, and V is widened to bf16, which is exact:
+// the softmax warpgroup of a stream, its weights made, widens the half tile that
+// they weigh into a buffer of its own (widen_v).  fp16 outputs take the weights
+// as two bf16 terms, 16 bits.  Their error is a 16-bit cache's.
+//   If a small item has no more than 64 rows, its two softmax warps without rows
+// widen all of V, for the two with rows set the pace (32 x 8 rows: 182 us, where
+// all four widen 203).
 //
 // All waits are bounded.  When one gives up, the softmax warps run on without
 // waiting (their barriers stay matched, results are void, the status word says
@@ -67,9 +71,9 @@
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16):
 //   32 requests, blocks of 8, context 8,192: HBM.  171 us for 1.08 GB, 6.3 TB/s,
 //     0.93 of the measured copy;
-//   the same over an E4M3 cache: 187 us for 0.56 GB.  Softmax: scales, two
-//     products more per weight and the terms of P; 124 us with the softmax
-//     taken out, 24 us of it the terms, 20 the barriers and scale loads;
+//   the same over an E4M3 cache: 182 us for 0.56 GB.  Softmax warps (scales and
+//     their barriers, two products more per weight); prompt chunks 1,655 us, where
+//     each stream widens V for itself, 1.8 times the bf16 cache's;
 //   prompt chunk, 2 x 2,048 rows, context up to 16,384: the tensor cores under
 //     the power limit, 911 us, 1.32 PFLOP/s at 1.75 GHz and 1,390 W, 0.77 of
 //     what a library product sustains;
@@ -103,7 +107,6 @@ constexpr int kJoinBlocks = 32;    // see paged_join_kernel
 constexpr int kSmem = 227 * 1024;  // all that a CTA may have
 constexpr uint32_t kColO = 256;    // O of stream 0; S of stream s at 128 s
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kVShiftLog2 = 8.0f;  // E4M3: factor on the weights
 
 // Where an item that this CTA starts but does not finish continues.
 struct Rec {
@@ -253,7 +256,6 @@ struct Ctrl {
   int more[2][2];
   int abort_flag;
   uint32_t tmem;
-  alignas(16) float vmax[2][3][4];
   // per warpgroup: key and value scales; (m, l) of the join; row scales of Q.
   // Before the roles start: scratch of the scan
   alignas(16) float x[2][kScaleTurns<E4M3> * 256];
@@ -378,32 +380,49 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
   }
 }
-template <bool E4M3>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if (!E4M3) {
-    tc_mma_f16_ta(d, a, b, idesc, accumulate);
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
+// Four E4M3 codes as bf16 values, exactly, the first and third in one word and
+// the second and fourth in the other: the sign and, four places lower, exponent
+// and mantissa are a bf16 2^120 too small, subnormal where the code is.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  const uint32_t e = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
+  const uint32_t o = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+  const __nv_bfloat162 f(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));
+  const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e), f);
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o), f);
+  even = *reinterpret_cast<const uint32_t*>(&x);
+  odd = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// The fp16 pairs h0 (values 0, 1) and h1 (2, 3): their E5M2 parts, one byte
-// each in order; h0 and h1 keep the rest, which is exact.
-__device__ __forceinline__ uint32_t take_e5m2(uint32_t& h0, uint32_t& h1) {
-  const uint32_t bytes = __byte_perm(h0, h1, 0x7531);
-  auto rest = [](uint32_t h) {
-    const uint32_t top = h & 0xFF00FF00u;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&top));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
-  h0 = rest(h0);
-  h1 = rest(h1);
-  return bytes;
+// Half a tile's V, kHK rows of codes as TMA left them, as bf16 in the layout of
+// a 16-bit tile (spans of 64 columns, 128-byte swizzle) but for the second and
+// third of every four columns, which change places (e4m3x4_to_bf16), by the
+// threads t = 0 .. N - 1; rows outside [lo, hi) as zeros: no row of the item
+// sees them, and a weight of 0 times whatever lies there must not become NaN.
+// Eight threads read 4 chunks of 16 codes from either of two rows whose chunks
+// lie in different banks, as they come and as they go: r and r ^ 5 for rows of
+// 128 codes, r and r ^ 1 for rows of 64.
+template <int HD, int N>
+__device__ __forceinline__ void widen_v(const uint8_t* codes, uint8_t* wide, int lo, int hi, int t) {
+  constexpr int kRows = N * 16 / HD;  // at once
+  const int other = (t >> 2) & 1;
+  const int r0 = HD == 128 ? (t >> 6) * 8 + (((t >> 3) & 3) ^ (other * 5)) : (t >> 3) * 2 + other;
+  const int ch = HD == 128 ? ((t >> 5) & 1) * 4 + (t & 3) : t & 3;
+  // all that the rows' swizzle depends on repeats with kRows
+  const uint8_t* from = codes + r0 * HD + (HD == 128 ? ch ^ (r0 & 7) : ch ^ ((r0 >> 1) & 3)) * 16;
+  uint8_t* to = wide + (ch >> 2) * (kHK * 128) + r0 * 128;
+  const int at = (2 * ch) & 7;
+  uint8_t *const to0 = to + ((at ^ (r0 & 7)) << 4), *const to1 = to + (((at + 1) ^ (r0 & 7)) << 4);
+#pragma unroll
+  for (int r = 0; r < kHK; r += kRows) {
+    uint4 c = make_uint4(0u, 0u, 0u, 0u), w;
+    if (r0 + r >= lo && r0 + r < hi) c = *reinterpret_cast<const uint4*>(from + r * HD);
+    e4m3x4_to_bf16(c.x, w.x, w.y);
+    e4m3x4_to_bf16(c.y, w.z, w.w);
+    *reinterpret_cast<uint4*>(to0 + r * 128) = w;
+    e4m3x4_to_bf16(c.z, w.x, w.y);
+    e4m3x4_to_bf16(c.w, w.z, w.w);
+    *reinterpret_cast<uint4*>(to1 + r * 128) = w;
+  }
 }
 
 template <int HD, bool E4M3, bool BF16>
@@ -411,37 +430,65 @@ struct Cfg {
   static constexpr int kRow = E4M3 ? HD : HD * 2;          // bytes of a cached row
   static constexpr int kTile = kKT * kRow;                 // of a K or V tile
   static constexpr int kQTerms = E4M3 ? (BF16 ? 2 : 3) : 1;
-  static constexpr int kPTerms = E4M3 ? (BF16 ? 3 : 4) : 1;
+  static constexpr int kPTerms = E4M3 && !BF16 ? 2 : 1;
+  static constexpr bool kPBf16 = E4M3 || BF16;             // type of the weights
   static constexpr int kQTile = kMT * kRow * kQTerms;
+  static constexpr int kWide = E4M3 ? kHK * HD * 2 : 0;    // V of half a tile, widened
   // Growth of a row's reference (log2) before O is rescaled: as much as the
-  // weights' type holds beside the factors on them (fp16 to 2^15: E4M3 has 2^8
-  // and up to 2 of a value scale there).  A bf16 has float32's exponents (mid-size
+  // weights' type holds (fp16 to 2^15).  A bf16 has float32's exponents (mid-size
   // prompt chunk: 112.7 us with 2^60, 112.9 with 2^30, 115.4 with 2^15).
-  static constexpr float kHeadroom = E4M3 ? 6.0f : BF16 ? 30.0f : 15.0f;
+  static constexpr float kHeadroom = kPBf16 ? 30.0f : 15.0f;
   // log2 of the factor on the weights.  A bf16 weight is at most 1, whatever its
   // reference has grown by since, so that the sums of weights and values stay
   // finite as far as the formula's do (2^30 let values above 2^80 overflow); what
   // is lost for it lies 2^96 below the largest.
-  static constexpr float kShift = !E4M3 && BF16 ? -kHeadroom : 0.0f;
+  static constexpr float kShift = kPBf16 ? -kHeadroom : 0.0f;
   // Operand layouts.  A row of K or Q is kRow bytes cut into spans of at most
   // 128; a span of all rows is one swizzled tile (128-byte swizzle, or 64 for
   // 64-byte rows), spans kKT x span bytes apart.
   static constexpr int kSpan = kRow < 128 ? kRow : 128;
   static constexpr int kStepsPerSpan = kSpan / 32;         // an MMA takes 32 bytes of K and Q
   static constexpr int kQkSteps = kRow / 32;
-  static constexpr int kPvSteps = E4M3 ? kHK / 32 : kHK / 16;  // keys per MMA: 32 codes, 16 halves
-  static constexpr int kVStep = (E4M3 ? 32 : 16) * kSpan;      // bytes of V to the next MMA's keys
+  static constexpr int kPvSteps = kHK / 16;  // keys per MMA
+  static constexpr int kVStep = 16 * 128;    // bytes of V to the next MMA's keys
   // Column of the weights of MMA kk (and term) in S: the weights of 32 keys lie
   // in the 32 columns that held those keys' scores.
   static __host__ __device__ constexpr uint32_t p_col(int term, int kk) {
-    return E4M3 ? kk * 32 + term * 8 : (kk >> 1) * 32 + (kk & 1) * 8;
+    return (kk >> 1) * 32 + term * 16 + (kk & 1) * 8;
   }
   static constexpr uint32_t kDescHi = (uint32_t)((8 * kSpan) >> 4) | (1u << 14) | ((kSpan == 64 ? 4u : 2u) << 29);
-  static constexpr uint32_t kVDescLo = (uint32_t)((kKT * kSpan) >> 4) << 16;  // next span of V along N
+  // V, 16-bit spans of 128 bytes: next span along N in the lower word
+  static constexpr uint32_t kVDescHi = (uint32_t)((8 * 128) >> 4) | (1u << 14) | (2u << 29);
+  static constexpr uint32_t kVDescLo = (uint32_t)(((E4M3 ? kHK : kKT) * 128) >> 4) << 16;
   static __host__ __device__ constexpr uint32_t id_qk(int term) {
     return E4M3 ? idesc_f8(kMT, kHK, term > 0) : idesc_f32acc(kMT, kHK, BF16);
   }
-  static constexpr uint32_t kIdPv = (E4M3 ? idesc_f8(kMT, HD, 1) : idesc_f32acc(kMT, HD, BF16)) | (1u << 16);  // V MN-major
+  static constexpr uint32_t kIdPv = idesc_f32acc(kMT, HD, kPBf16) | (1u << 16);  // V MN-major
+};
+
+// Where a reader stands in the two rings of slots: the first slot of the
+// segment in either, and the phase it waits for there.
+struct Rings {
+  int at[2] = {0, 0};
+  uint32_t phase[2] = {0, 0};
+
+  static __device__ __forceinline__ void advance(int half, int& at, uint32_t& phase, int n) {
+    at += n;
+    if (at >= half) {
+      at -= half;
+      phase ^= 1u;
+    }
+  }
+  // past a segment of nt tiles: of K in one ring and V in the other, or (split)
+  // of both in the ring of the stream that has every other tile
+  __device__ __forceinline__ void leave(int half, bool split, int nt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = at[i] + (split ? 2 * ((nt + 1 - i) / 2) : nt);
+      at[i] = n % half;
+      phase[i] ^= (uint32_t)(n / half) & 1u;
+    }
+  }
 };
 
 // ------------------------------------------------------------------ Q tile
@@ -524,7 +571,9 @@ __device__ __forceinline__ void load_q(const PagedAttnArgs& a, const Item& it, i
 
 // ------------------------------------------------------------------ kernel
 
-template <int HD, bool E4M3, bool BF16>
+// WIDES: E4M3, buffers of widened V that a stream has: one for either half of a
+// tile, or one for both.
+template <int HD, bool E4M3, bool BF16, int WIDES>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                            const KernelArgs k) {
@@ -534,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PagedAttnArgs& a = k.a;
   uint8_t* ring_s = smem;
   uint8_t* q_s = ring_s + 2 * k.half * C::kTile;
+  uint8_t* wide_s = q_s + k.q_tiles * C::kQTile;  // E4M3: widened V, [stream][buffer]
   auto* c = reinterpret_cast<Ctrl<E4M3>*>(smem + kSmem - kCtrlBytes<E4M3>);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
@@ -636,15 +686,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       Seg s;
       walk.begin(c->start, w1 - w0);
       const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
-      auto advance = [&](int& at, uint32_t& phase, int n) {
-        at += n;
-        if (at >= k.half) {
-          at -= k.half;
-          phase ^= 1u;
-        }
-      };
-      int at0 = 0, at1 = 0;  // first slot of the segment in either ring
-      uint32_t ph0 = 0, ph1 = 0, used = 0, parity = 0;  // per slot: in use, phase of its last load
+      auto advance = [&](int& at, uint32_t& phase, int n) { Rings::advance(k.half, at, phase, n); };
+      Rings rings;
+      uint32_t used = 0, parity = 0;  // per slot: in use, phase of its last load
       bool ok = true;
       while (ok && walk.next(k, &s)) {
         const int32_t* table = a.batch.table + s.it.b * a.batch.table_stride;
@@ -659,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ids = look_up(ids_at);
           ids_next = look_up(ids_at + 32);
         }
-        int s0 = at0, s1 = at1;
-        uint32_t q0 = ph0, q1 = ph1;
+        int s0 = rings.at[0], s1 = rings.at[1];
+        uint32_t q0 = rings.phase[0], q1 = rings.phase[1];
         if (s.split) {
           advance(s0, q0, side);
           advance(s1, q1, side);
@@ -702,11 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             advance(s0, q0, s.split ? 2 : 1);
         }
-        const int n0 = at0 + (s.split ? 2 * ((s.nt + 1) / 2) : s.nt), n1 = at1 + (s.split ? 2 * (s.nt / 2) : s.nt);
-        at0 = n0 % k.half;
-        ph0 ^= (uint32_t)(n0 / k.half) & 1u;
-        at1 = n1 % k.half;
-        ph1 ^= (uint32_t)(n1 / k.half) & 1u;
+        rings.leave(k.half, s.split, s.nt);
       }
       if (!ok && lead) {
         // a wait gave up: let the copies in flight land before the CTA leaves
@@ -726,10 +766,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_d = smem_u32(q_s) >> 4;
       constexpr uint32_t kTileD = C::kTile >> 4;
       const uint32_t tS = tmem + st * kKT, tO = tmem + kColO + st * 128;
-      constexpr uint32_t kHalfD = (kHK * C::kSpan) >> 4;  // a tile's second half of K or V rows
+      constexpr uint32_t kHalfD = (kHK * C::kSpan) >> 4;  // a tile's second half of K rows
+      constexpr uint32_t kHalfV = E4M3 ? (WIDES - 1) * (C::kWide >> 4) : kHalfD;  // of V
       uint32_t seg = 0, p_phase = 0;
-      int at0 = 0, at1 = 0;  // first slot of the segment in either ring
-      uint32_t ph0 = 0, ph1 = 0;
+      Rings rings;
       bool ok = true;
       while (true) {
         ok = warp_wait_on(&c->q_full[0], seg & 1u, stop, a.status) &&
@@ -742,22 +782,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = s.nt, lo = s.it.lo, hi = s.it.hi;
         const int stride = split ? 2 : 1, first = split ? st : 0;
         int k0 = (s.t0 + first) * kKT;  // first key of the job
-        auto advance = [&](int& at, uint32_t& phase, int n) {
-          at += n;
-          if (at >= k.half) {
-            at -= k.half;
-            phase ^= 1u;
-          }
-        };
+        auto advance = [&](int& at, uint32_t& phase, int n) { Rings::advance(k.half, at, phase, n); };
         // K and V slots: of the stream's own ring in turn, or of the K and the V ring
         const bool kr = split && st, vr = !split || st;
         uint8_t* const k_s = ring_s + (kr ? k.half * C::kTile : 0);
         uint8_t* const v_s = ring_s + (vr ? k.half * C::kTile : 0);
         uint64_t *const k_full = c->full + (kr ? k.half : 0), *const k_empty = c->empty + (kr ? k.half : 0);
         uint64_t *const v_full = c->full + (vr ? k.half : 0), *const v_empty = c->empty + (vr ? k.half : 0);
-        const uint32_t k_d = smem_u32(k_s) >> 4, v_d = smem_u32(v_s) >> 4;
-        int ks = kr ? at1 : at0, vs = vr ? at1 : at0;
-        uint32_t kp = kr ? ph1 : ph0, vp = vr ? ph1 : ph0;
+        const uint32_t k_d = smem_u32(k_s) >> 4;
+        const uint32_t v_d = smem_u32(E4M3 ? wide_s + st * WIDES * C::kWide : v_s) >> 4;
+        int ks = rings.at[kr], vs = rings.at[vr];
+        uint32_t kp = rings.phase[kr], vp = rings.phase[vr];
         if (split) advance(vs, vp, 1);
         const uint32_t qd = q_d + (split ? 0u : (uint32_t)st * (C::kQTile >> 4)) + (1u << 16);
         // every slot is given back twice: by both streams, or twice by one
@@ -792,8 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         for (int t = first; ok && t < nt; t += stride, k0 += stride * kKT) {
-          ok = warp_wait_on(&v_full[vs], vp, stop, a.status);
-          if (k0 < lo || k0 + kKT > hi) {
+          if (!E4M3) ok = warp_wait_on(&v_full[vs], vp, stop, a.status);
+          if (!E4M3 && (k0 < lo || k0 + kKT > hi)) {
             // V rows that no row of the item sees
             uint4* v = reinterpret_cast<uint4*>(v_s + vs * C::kTile);
             for (int idx = lane; idx < kKT * (C::kRow / 16); idx += 32) {
@@ -805,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const bool more = t + stride < nt;
           bool early = false;  // the next tile's first scores are on their way
-          const uint32_t vd = v_d + vs * kTileD + C::kVDescLo;
+          const uint32_t vd = v_d + (E4M3 ? 0u : vs * kTileD) + C::kVDescLo;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             ok = ok && warp_wait_on(&c->p_full[st][h], p_phase, stop, a.status);
@@ -817,11 +852,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int kk = 0; kk < C::kPvSteps; ++kk)
 #pragma unroll
                 for (int term = 0; term < C::kPTerms; ++term)
-                  mma_ts<E4M3>(tO, tS + h * kHK + C::p_col(term, kk),
-                               desc64(vd + h * kHalfD + kk * (C::kVStep >> 4), C::kDescHi), C::kIdPv,
-                               (term > 0 || kk > 0) ? 1u : keep);
+                  tc_mma_f16_ta(tO, tS + h * kHK + C::p_col(term, kk),
+                                desc64(vd + h * kHalfV + kk * (C::kVStep >> 4), C::kVDescHi), C::kIdPv,
+                                (term > 0 || kk > 0) ? 1u : keep);
               tc_commit(&c->pv_done[st][h]);
-              if (h) give_back(&v_empty[vs]);
+              if (h && !E4M3) give_back(&v_empty[vs]);
+              if (h && E4M3) {  // its codes have been read: P came after them
+                mbar_arrive(&v_empty[vs]);
+                if (split) mbar_arrive(&v_empty[vs]);
+              }
             }
             __syncwarp();
             // P of a job overwrites its S: the half's next scores follow its
@@ -844,11 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (lead) tc_commit(&c->o_full);
         __syncwarp();
-        const int n0 = at0 + (split ? 2 * ((nt + 1) / 2) : nt), n1 = at1 + (split ? 2 * (nt / 2) : nt);
-        at0 = n0 % k.half;
-        ph0 ^= (uint32_t)(n0 / k.half) & 1u;
-        at1 = n1 % k.half;
-        ph1 ^= (uint32_t)(n1 / k.half) & 1u;
+        rings.leave(k.half, split, nt);
       }
       if (lead) tc_commit(&c->fin);  // every MMA this thread issued
       __syncwarp();
@@ -860,6 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + wg * kKT, tO = tmem + lane_off + kColO;
     float* const x0 = c->x[wg];
     uint32_t tiles = 0, seg = 0;
+    Rings rings;  // E4M3
     // the next segment's description, a segment ahead
     auto describe = [&](uint32_t turn) {
       Seg* n = &c->seg[wg][turn & 1u];
@@ -912,7 +948,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float cs = !real ? 0.0f : E4M3 ? fmaxf(a.scale_log2 * x0[t], 0x1p-126f) : a.scale_log2;
 
       float m_ref = -INFINITY, l = 0.0f;
-      float vref = 0.0f, cv = C::kShift;  // E4M3: reference of the value scales; log2 of the weights' factor
       const int step = s.split ? 2 : 1, j0 = s.split ? wg : 0, nt = s.nt, t0 = s.t0;
       // E4M3: scales of key t of the next tile, and the page of the one after
       // it, so that neither load is waited for in its own tile
@@ -933,14 +968,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           nvs = __ldg(a.v_scale + o);
         }
       };
-      // what was fetched into one of the buffers, and the largest value scale
-      // of each warp's keys
+      // what was fetched into one of the buffers
       auto put = [&](int turn) {
         x0[turn * 256 + t] = nks;
         x0[turn * 256 + 128 + t] = nvs;
-        const float wm = warp_max_f(nvs);
-        if (lane == 0) c->vmax[wg][turn][warp & 3] = wm;
       };
+      // no more than 64 rows: the two warps without any widen all of V
+      const bool idle = s.split && it.rows <= 64;
+      // E4M3: this stream's V slots, as its MMA warp would follow them
+      const bool vr = !s.split || wg;
+      int vs = rings.at[vr];
+      uint32_t vp = rings.phase[vr];
+      if (s.split) Rings::advance(k.half, vs, vp, 1);
       int turn = 0;
       if (E4M3) {
         look_up(t0 + j0);
@@ -952,7 +991,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         look_up(t0 + j0 + 2 * step);
       }
       for (int j = j0; j < nt; j += step) {
-        float fv = 1.0f;  // E4M3: change of the value reference
         const float* x = x0 + turn * 256;
         if (E4M3) {
           // the next tile's scales go where the last but one's were; after the
@@ -962,14 +1000,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           fetch(t0 + j + 2 * step);
           look_up(t0 + j + 3 * step);
           named_sync(1 + wg, 128);
-          const float4 vm4 = *reinterpret_cast<const float4*>(c->vmax[wg][turn]);
-          const float vm = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
-          if (vm > 2.0f * vref || vref == 0.0f) {
-            const float nv = fmaxf(vm, 0x1p-60f);
-            fv = vref / nv;
-            vref = nv;
-            cv = kVShiftLog2 - log2f(vref);
-          }
           turn = next;
         }
         const uint32_t phase = tiles++ & 1u;
@@ -977,9 +1007,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
           (void)warp_wait_on(&c->s_full[wg][h], phase, stop, a.status);
           tc_fence_after();
+          // E4M3: this half of V for the tensor cores.  Its buffer's last reader
+          // was the P V before these scores (two jobs ago) or, with one buffer,
+          // the last one.
+          auto widen = [&] {
+            if (!E4M3) return;
+            const int slot = (vr ? k.half : 0) + vs, at = (t0 + j) * kKT + h * kHK;
+            if (h) Rings::advance(k.half, vs, vp, step);
+            if (idle && t < 64) return;
+            if (h == 0) (void)warp_wait_on(&c->full[slot], vp, stop, a.status);
+            if (WIDES == 1 && (j > j0 || h))
+              (void)warp_wait_on(&c->pv_done[wg][h ^ 1], h ? phase : phase ^ 1u, stop, a.status);
+            const uint8_t* codes = ring_s + slot * C::kTile + h * (kHK * C::kRow);
+            uint8_t* wide = wide_s + (wg * WIDES + h * (WIDES - 1)) * C::kWide;
+            if (idle)
+              widen_v<HD, 64>(codes, wide, it.lo - at, it.hi - at, t - 64);
+            else
+              widen_v<HD, 128>(codes, wide, it.lo - at, it.hi - at, t);
+            fence_proxy_async_smem();
+          };
           if (!live) {
             // no query row in this warp's lanes: whatever their P holds only
             // reaches lanes of O that nobody reads
+            widen();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->p_full[wg][h]);
             continue;
@@ -1024,9 +1074,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
           const bool grow = m_tile > m_ref + C::kHeadroom || (m_ref == -INFINITY && m_tile > -INFINITY);
-          if (__any_sync(0xffffffffu, grow || fv != 1.0f)) {
+          if (__any_sync(0xffffffffu, grow)) {
             const float m_new = grow ? m_tile : m_ref;
-            const float fo = (grow ? ex2_approx(m_ref - m_new) : 1.0f) * fv;  // 0 while nothing was seen
+            const float fo = grow ? ex2_approx(m_ref - m_new) : 1.0f;  // 0 while nothing was seen
             if (j > j0 || h) {
               // O holds the stream's earlier jobs: wait for the last one's
               // P V; the next one waits for this P
@@ -1049,14 +1099,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             l *= fo;
             m_ref = m_new;
-            fv = 1.0f;
           }
-          // ---- weights 2^(z - m_ref + cv); l and O carry the factor, too
-          const float nb = m_ref == -INFINITY ? 0.0f : cv - m_ref;
+          // ---- weights 2^(z - m_ref + kShift); l and O carry the factor, too
+          const float nb = m_ref == -INFINITY ? 0.0f : C::kShift - m_ref;
           const float2 cs2 = make_float2(cs, cs), nb2 = make_float2(nb, nb);
           float2 ls0 = make_float2(0.0f, 0.0f), ls1 = ls0;
           auto weigh = [&](int q, const float (&v)[32]) {
-            uint32_t pw[16];  // 16-bit weights of 32 keys
+            uint32_t pw[16], rest[16];  // 16-bit weights of 32 keys, and what they leave
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               float2 p0 = fma2(make_float2(v[e], v[e + 1]), cs2, nb2), p1 = fma2(make_float2(v[e + 2], v[e + 3]), cs2, nb2);
@@ -1069,35 +1118,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p0 = mul2(p0, make_float2(f.x, f.y));
                 p1 = mul2(p1, make_float2(f.z, f.w));
               }
-              pw[e / 2] = pack16<!E4M3 && BF16>(p0.x, p0.y);
-              pw[e / 2 + 1] = pack16<!E4M3 && BF16>(p1.x, p1.y);
-            }
-            if (!E4M3) {
-              tmem_st(ta + q * 32, pw);
-            } else {
-              // Three terms hold the upper 9 of fp16's 11 bits, more where
-              // zeros follow a term.  Cut off like that the weights would be
-              // 3.2e-4 too small on average, with a unit in the last place
-              // added first 3.8e-4 too large: every other key has it added
-              // (positive values; rounding to 9 bits by adding half of the
-              // last, without clearing what is behind it, made all 1.1e-3 too
-              // large).
-              if (C::kPTerms == 3) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) pw[e] += 0x00010000u;
-              }
-#pragma unroll
-              for (int term = 0; term < C::kPTerms; ++term) {
-                uint32_t b[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) b[e] = take_e5m2(pw[2 * e], pw[2 * e + 1]);
-                tmem_st(ta + q * 32 + term * 8, b);
+              pw[e / 2] = pack16<C::kPBf16>(p0.x, p0.y);
+              pw[e / 2 + 1] = pack16<C::kPBf16>(p1.x, p1.y);
+              if (C::kPTerms == 2) {
+                const float2 r0 = unpack16<true>(pw[e / 2]), r1 = unpack16<true>(pw[e / 2 + 1]);
+                rest[e / 2] = pack16<true>(p0.x - r0.x, p0.y - r0.y);
+                rest[e / 2 + 1] = pack16<true>(p1.x - r1.x, p1.y - r1.y);
               }
             }
+            tmem_st(ta + q * 32, pw);
+            if (C::kPTerms == 2) tmem_st(ta + q * 32 + 16, rest);
           };
           weigh(0, v0);
           weigh(1, v1);
           l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
+          widen();
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -1110,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool whole = s.first && s.last;
       // factors of O0 and O1 (a row-split item: of its own O)
-      float f0 = 1.0f, f1 = 0.0f, M = m_ref - cv, L = l;
+      float f0 = 1.0f, f1 = 0.0f, M = m_ref - C::kShift, L = l;
       if (s.split) {
         named_sync(1 + wg, 128);  // scales are no longer read
         x0[t] = M;
@@ -1146,6 +1181,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (have1) o[e] = fmaf(o1[e], f1, o[e]);
           }
           if (!real) continue;
+          if (E4M3) {  // columns as widen_v laid them out
+#pragma unroll
+            for (int e = 1; e < 32; e += 4) {
+              const float x = o[e];
+              o[e] = o[e + 1];
+              o[e + 1] = x;
+            }
+          }
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(out + col * 2);
 #pragma unroll
@@ -1166,6 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
+      if (E4M3) rings.leave(k.half, s.split, s.nt);
     }
   }
 
@@ -1324,10 +1368,10 @@ Layout layout(void* ws, int group, int hd, int max_rows) {
   return l;
 }
 
-template <int HD, bool E4M3, bool BF16>
+template <int HD, bool E4M3, bool BF16, int WIDES>
 int launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, void* ws, cudaStream_t s) {
   using C = Cfg<HD, E4M3, BF16>;
-  auto kern = paged_attention_kernel<HD, E4M3, BF16>;
+  auto kern = paged_attention_kernel<HD, E4M3, BF16, WIDES>;
   int dev = 0, sms = 0;
   DFL_CUDA_TRY(cudaGetDevice(&dev));
   static std::atomic<int> known[64];  // SMs of the devices the attribute is set on
@@ -1348,7 +1392,7 @@ int launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
   k.rts = (int)rts;
   k.part_rows = part_rows(a.group, a.max_rows);
   k.q_tiles = k.part_rows / kMT;
-  k.half = min(kMaxSlots, (kSmem - kCtrlBytes<E4M3> - k.q_tiles * C::kQTile) / C::kTile) / 2;
+  k.half = min(kMaxSlots, (kSmem - kCtrlBytes<E4M3> - k.q_tiles * C::kQTile - 2 * WIDES * C::kWide) / C::kTile) / 2;
   // Cost of an item beside its tiles, for the cut of the line: setting out, the
   // queries (terms of them for E4M3), the end.  Of 0 / 1 / 2 / 4 / 8 tiles: ragged
   // E4M3 blocks 294 / 267 / 253 / 217 / 196 us; bf16 prompt chunks of 200 to 700
@@ -1376,12 +1420,17 @@ int encode_paged_maps(const dflash_paged_cache& c, CUtensorMap* k, CUtensorMap* 
 int launch_paged_attention(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnArgs& a, int head_dim,
                            int format, int type, void* ws, cudaStream_t s) {
   const bool bf = type == DFLASH_TYPE_BF16, e = format == DFLASH_CACHE_E4M3;
+  // Three terms of two Q tiles leave the rings one slot each beside four widened
+  // halves of V: two then.  (Elsewhere four: with two, ragged blocks took 235 us
+  // against 216, a prompt chunk 1,696 against 1,709.)
+  const bool two = part_rows(a.group, a.max_rows) > kMT;
   if (head_dim == 128) {
-    if (e) return bf ? launch<128, true, true>(k, v, a, ws, s) : launch<128, true, false>(k, v, a, ws, s);
-    return bf ? launch<128, false, true>(k, v, a, ws, s) : launch<128, false, false>(k, v, a, ws, s);
+    if (e && bf) return launch<128, true, true, 2>(k, v, a, ws, s);
+    if (e) return two ? launch<128, true, false, 1>(k, v, a, ws, s) : launch<128, true, false, 2>(k, v, a, ws, s);
+    return bf ? launch<128, false, true, 2>(k, v, a, ws, s) : launch<128, false, false, 2>(k, v, a, ws, s);
   }
-  if (e) return bf ? launch<64, true, true>(k, v, a, ws, s) : launch<64, true, false>(k, v, a, ws, s);
-  return bf ? launch<64, false, true>(k, v, a, ws, s) : launch<64, false, false>(k, v, a, ws, s);
+  if (e) return bf ? launch<64, true, true, 2>(k, v, a, ws, s) : launch<64, true, false, 2>(k, v, a, ws, s);
+  return bf ? launch<64, false, true, 2>(k, v, a, ws, s) : launch<64, false, false, 2>(k, v, a, ws, s);
 }
 
 }  // namespace dfl

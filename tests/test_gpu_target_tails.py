@@ -79,6 +79,83 @@ def bound(out, lse, mean, size, n, hd, dtype, q64, k64, e4m3):
     return rel * mean + u * np.abs(out) * (1 + u), b_lse
 
 
+def tail_case(n, part, rows, n_q, hd, dtype, e4m3, flat, large, seed=3):
+    """A request of n positions whose first key takes `part` of every row's
+    weight and holds values a hundredth of the others'.  flat: all other keys
+    are alike, so that their weights' roundings are, too.  large: one other
+    value row is 16 times the rest."""
+    p = Paged([n], [rows], 1, hd, 64, dtype, e4m3, garbage=False)
+    share(p, rows)
+    rng = np.random.default_rng(seed)
+    q = rows_tensor(p.n_rows, n_q, hd, dtype, seed)
+    q[..., 0] = 4.0
+    k = rng.normal(size=(n, 1, hd)).astype(np.float32) * (0.0 if flat else 0.5)
+    k[:, :, 0] = 0.0
+    k[0] = 0.0
+    k[0, 0, 0] = (np.log(part / (1 - part)) + np.log(n)) * hd ** 0.5 / 4
+    v = rng.uniform(0.5, 1.5, size=(n, 1, hd)) * np.exp(0.5 * rng.normal(size=(n, 1, 1)))
+    v[0] *= 0.01
+    if large:
+        v[n // 2] *= 16
+    k64, v64 = put(p, 0, k), put(p, 1, v.astype(np.float32))
+    return p, q, k64, v64
+
+
+def compare(p, q, k64, v64, out, lse, part=None):
+    n, _, hd = k64.shape
+    rows = np.concatenate([np.arange(p.start_np[b], p.start_np[b + 1]) for b in LOOK])
+    q64 = to64(q)[rows]
+    want, want_l, mean, size = ot.attention(q64, k64, v64, n, False, 0, hd ** -0.5)
+    if part:                                          # the case is what it says
+        assert (np.exp((q64 @ k64[0, 0]) * hd ** -0.5 - want_l) > 0.4 * part).all()
+    b_out, b_lse = bound(want, want_l, mean, size, n, hd, p.dtype, q64, k64, p.e4m3)
+    worst = (np.abs(to64(out)[rows] - want) / b_out).max()
+    worst_l = (np.abs(to64(lse)[rows] - want_l) / b_lse).max()
+    assert worst <= 1.0 and worst_l <= 1.0, f"out {worst:.2f}, lse {worst_l:.2f} of their bounds off"
+
+
+CASES = [
+    # keys, share, new rows, query heads, head_dim, flat, one large value row
+    (8192, 0.5, 1, 5, 128, False, False),
+    (8192, 0.9, 8, 5, 128, True, False),
+    (8192, 0.9, 8, 5, 64, False, True),
+    (8192, 0.99, 33, 4, 128, True, True),
+    (32768, 0.8, 8, 2, 128, False, False),
+    (32768, 0.9, 33, 4, 64, True, False),
+    (32768, 0.9, 1, 3, 64, False, True),
+    (131072, 0.9, 2, 2, 128, True, False),
+    (131072, 0.99, 2, 1, 128, False, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("n,part,rows,n_q,hd,flat,large", CASES)
+def test_attention_over_codes_keeps_the_tail_behind_one_dominant_key(n, part, rows, n_q, hd, flat, large, dtype):
+    p, q, k64, v64 = tail_case(n, part, rows, n_q, hd, dtype, True, flat, large)
+    out, lse, status = run_attention(p, q, causal=False)
+    assert status == 0
+    compare(p, q, k64, v64, out, lse, part)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, FH])
+def test_attention_returns_every_code_of_a_single_visible_row(hd, dtype):
+    """One key: the output is the value row itself, all finite codes of E4M3
+    under a scale that is a power of two, exactly."""
+    codes = np.array([c for c in range(256) if c & 0x7F != 0x7F], dtype=np.uint8)
+    codes = np.resize(codes, (256 // hd, 1, hd))
+    n = codes.shape[0]
+    p = Paged([1] * n, [1] * n, 1, hd, 16, dtype, True, garbage=False)
+    for b in range(n):
+        p.pages[1].view(torch.uint8)[int(p.table_np[b, 0]), :, 0] = torch.from_numpy(codes[b]).cuda()
+        p.scale[1][int(p.table_np[b, 0]), :, 0] = 0.25
+    q = rows_tensor(n, 3, hd, dtype, 3)
+    out, _, status = run_attention(p, q)
+    assert status == 0
+    want = np.repeat(quant.e4m3_value(codes) * 0.25, 3, axis=1)
+    np.testing.assert_array_equal(to64(out), want)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("size", [2.0 ** 112, 2.0 ** 119])
 def test_attention_of_very_large_values_under_scores_that_grow(e4m3, size):
