@@ -435,14 +435,21 @@ struct Cfg {
   static constexpr int kQTile = kMT * kRow * kQTerms;
   static constexpr int kWide = E4M3 ? kHK * HD * 2 : 0;    // V of half a tile, widened
   // Growth of a row's reference (log2) before O is rescaled: as much as the
-  // weights' type holds (fp16 to 2^15).  A bf16 has float32's exponents (mid-size
-  // prompt chunk: 112.7 us with 2^60, 112.9 with 2^30, 115.4 with 2^15).
-  static constexpr float kHeadroom = kPBf16 ? 30.0f : 15.0f;
+  // weights' type holds beside the factor on them (fp16 to 2^15).  A bf16 has
+  // float32's exponents (mid-size prompt chunk: 112.7 us with 2^60, 112.9 with
+  // 2^30, 115.4 with 2^15).
+  static constexpr float kHeadroom = kPBf16 ? 30.0f : 4.0f;
   // log2 of the factor on the weights.  A bf16 weight is at most 1, whatever its
   // reference has grown by since, so that the sums of weights and values stay
   // finite as far as the formula's do (2^30 let values above 2^80 overflow); what
-  // is lost for it lies 2^96 below the largest.
-  static constexpr float kShift = kPBf16 ? -kHeadroom : 0.0f;
+  // is lost for it lies 2^96 below the largest.  An fp16 ends at 2^-24: the weights
+  // of a long tail behind one dominant key need the range more than rescaling
+  // needs headroom.  Their last place is 2^-35 of the reference (2^-24 before, of
+  // which 131,072 keys that share a hundredth of a row are a quarter and more
+  // each).  2^0 / 2^7 / 2^9 / 2^11 / 2^13, the headroom what they leave of 2^15:
+  // mid-size fp16 prompt chunk 137.8 / 142.2 / 143.5 / 144.8 / 146.4 us, long one
+  // 860 / 878 / 880 / 890 / 899, blocks alike.
+  static constexpr float kShift = kPBf16 ? -kHeadroom : 11.0f;
   // Operand layouts.  A row of K or Q is kRow bytes cut into spans of at most
   // 128; a span of all rows is one swizzled tile (128-byte swizzle, or 64 for
   // 64-byte rows), spans kKT x span bytes apart.
