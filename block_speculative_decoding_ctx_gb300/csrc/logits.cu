@@ -340,6 +340,9 @@ __global__ void __launch_bounds__(kLT, 4) logits_adjust_kernel(const LogitsArgs 
       for (int j = 0; j < e; ++j) first = first && b_ids[j] != b_ids[e];
       if (!first) continue;
       for (int i = i0; i < i1; ++i) {
+        // what is not allowed stays -infinity, whatever would be added
+        const uint32_t* m = allowed(i);
+        if (m && !bit(m, b_ids[e])) continue;
         float* out = a.out + b * a.o_b + i * a.o_i;
         float y = out[b_ids[e]];
         for (int j = e; j < nb; ++j)
