@@ -71,27 +71,39 @@ struct Place {
   int at;
 };
 
-// First request that ends after row n0, found by the whole block.
-__device__ __forceinline__ int first_request(const PagedBatch& p, int n0, int* status) {
-  __shared__ int b0;
-  if (threadIdx.x == 0) b0 = p.B;
+// What a block learns from the requests that fit the call.
+struct Found {
+  int b0;    // the first one that ends after the block's first row
+  int odd;   // some request does not fit: row_start need not rise
+};
+__device__ __forceinline__ void look_through(const PagedBatch& p, int n0, int* status, Found* found) {
+  if (threadIdx.x == 0) *found = {p.B, 0};
   __syncthreads();
-  int mine = p.B;
+  int b0 = p.B, odd = 0;
   for (int b = threadIdx.x; b < p.B; b += kMoveThreads) {
-    if (__ldg(p.row_start + b + 1) > n0) mine = min(mine, b);
     RequestSpan r;
-    if (blockIdx.x == 0 && !request_span(p, b, &r)) report_status(status, DFLASH_ERR_SHAPE);
+    if (!request_span(p, b, &r)) {
+      odd = 1;
+      if (blockIdx.x == 0) report_status(status, DFLASH_ERR_SHAPE);
+    } else if (r.n > 0 && r.s0 + r.n > n0) {
+      b0 = min(b0, b);
+    }
   }
-  if (mine < p.B) atomicMin(&b0, mine);
+  if (b0 < p.B) atomicMin(&found->b0, b0);
+  if (odd) found->odd = 1;
   __syncthreads();
-  return b0;
 }
 
-__device__ __forceinline__ Place find_row(const PagedBatch& p, int b, int n, int* status) {
+__device__ __forceinline__ Place find_row(const PagedBatch& p, const Found& found, int n, int* status) {
   Place r = {false, false, 0, 0};
-  while (b < p.B && __ldg(p.row_start + b + 1) <= n) ++b;
   RequestSpan sp;
-  if (b >= p.B || !request_span(p, b, &sp) || n < sp.s0) return r;
+  int b = found.b0;
+  for (;; ++b) {
+    if (b >= p.B) return r;
+    if (__ldg(p.row_start + b + 1) <= n || !request_span(p, b, &sp)) continue;
+    if (n >= sp.s0) break;
+    if (!found.odd) return r;  // rows before the first request's
+  }
   r.owned = true;
   const int pos = sp.len - sp.n + (n - sp.s0);
   if (pos < 0) {
@@ -117,9 +129,12 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
   constexpr int kUnits = kMoveThreads / kLanes;     // (row, head, side) at once
   constexpr int kCell = E4M3 ? 1 : 2;               // bytes of a cached value
   __shared__ Place places[kMoveThreads];
+  __shared__ Found found;
   const int n0 = blockIdx.x * rows, lane = threadIdx.x % kLanes;
   const uint32_t per_row = 2u * a.n_kv;
-  const uint32_t units = min(rows, a.batch.rows - n0) * per_row;
+  look_through(a.batch, n0, a.status, &found);
+  const int mine = min(rows, a.batch.rows - n0);
+  const uint32_t units = mine * per_row;
 
   struct Piece {
     int row, head, side;  // row of the block
@@ -147,12 +162,9 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
       }
     }
   };
-  // the rows exist whoever owns them: the first are on their way while the
-  // places are looked up
+  // the first rows are on their way while the places are looked up
   if (APPEND) load_rows(threadIdx.x / kLanes);
-  const int b0 = first_request(a.batch, min(n0, a.batch.rows), a.status);
-  if ((int)threadIdx.x < rows && n0 + (int)threadIdx.x < a.batch.rows)
-    places[threadIdx.x] = find_row(a.batch, b0, n0 + threadIdx.x, a.status);
+  if ((int)threadIdx.x < mine) places[threadIdx.x] = find_row(a.batch, found, n0 + threadIdx.x, a.status);
   __syncthreads();
 
   // whole warps stay together: pieces past the last take part in the shuffles
