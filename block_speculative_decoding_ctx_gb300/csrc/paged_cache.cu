@@ -74,22 +74,25 @@ struct Place {
 // What a block learns from the requests that fit the call.
 struct Found {
   int b0;    // the first one that ends after the block's first row
+  int end;   // the row behind the last that any of them owns: none from there on is touched
   int odd;   // some request does not fit: row_start need not rise
 };
 __device__ __forceinline__ void look_through(const PagedBatch& p, int n0, int* status, Found* found) {
-  if (threadIdx.x == 0) *found = {p.B, 0};
+  if (threadIdx.x == 0) *found = {p.B, 0, 0};
   __syncthreads();
-  int b0 = p.B, odd = 0;
+  int b0 = p.B, end = 0, odd = 0;
   for (int b = threadIdx.x; b < p.B; b += kMoveThreads) {
     RequestSpan r;
     if (!request_span(p, b, &r)) {
       odd = 1;
       if (blockIdx.x == 0) report_status(status, DFLASH_ERR_SHAPE);
-    } else if (r.n > 0 && r.s0 + r.n > n0) {
-      b0 = min(b0, b);
+    } else if (r.n > 0) {
+      if (r.s0 + r.n > n0) b0 = min(b0, b);
+      end = max(end, r.s0 + r.n);
     }
   }
   if (b0 < p.B) atomicMin(&found->b0, b0);
+  if (end) atomicMax(&found->end, end);
   if (odd) found->odd = 1;
   __syncthreads();
 }
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
   const int n0 = blockIdx.x * rows, lane = threadIdx.x % kLanes;
   const uint32_t per_row = 2u * a.n_kv;
   look_through(a.batch, n0, a.status, &found);
-  const int mine = min(rows, a.batch.rows - n0);
+  const int mine = max(0, min(rows, found.end - n0));
   const uint32_t units = mine * per_row;
 
   struct Piece {

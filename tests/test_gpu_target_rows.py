@@ -1,5 +1,6 @@
-"""Appends and reads back of batches whose rows are not one full list: rows
-before the first request's, requests that do not fit in front of ones that do."""
+"""Appends and reads back of batches whose rows are not one full list: padding
+behind the last request, rows before the first, requests that do not fit in
+front of ones that do."""
 
 import numpy as np
 import pytest
@@ -20,6 +21,7 @@ def _lib():
 
 BATCHES = [
     # row_start, rows of the tensors, requests that fit, new rows of each, status
+    ([0, 3, 5, 9], 400, {0: (0, 3), 1: (3, 2), 2: (5, 4)}, 0),       # padded
     ([6, 8, 8, 12], 12, {0: (6, 2), 2: (8, 4)}, 0),                  # rows before the first
     ([0, 25, 5, 10], 12, {2: (5, 5)}, -2),                           # past the tensors, then decreasing
     ([5, 10, 0, 3], 12, {0: (5, 5), 2: (0, 3)}, -2),                 # decreasing in the middle
