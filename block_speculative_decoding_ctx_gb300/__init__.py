@@ -433,6 +433,12 @@ def _fit(name, t, dtype, shape, index):
     _misfit(name, t, dtype, shape, index)
 
 
+def _c_ints(what, *values):
+    """ctypes passes the lower 32 bits of what a C int does not hold."""
+    if min(values) < -1 << 31 or max(values) >= 1 << 31:
+        raise ValueError(f"{what}: expected less than 2^31, got {values}")
+
+
 def _current(index, stream):
     """The stream to launch on; the tensors' device must be the current one."""
     if index < 0:
@@ -527,6 +533,7 @@ def dflash_paged_gather(cache, k, v, row_start, kv_len, page_table, ws, stream=N
 
 
 def dflash_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_rows):
+    _c_ints("heads, head_dim and max_rows", n_q_heads, n_kv_heads, head_dim, max_rows)
     return int(lib().dflash_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_rows))
 
 
@@ -572,6 +579,7 @@ def dflash_logits_adjust(logits, out, ws, counts=None, prompt_mask=None, req_slo
             out.dtype is not torch.float32 or out.get_device() != index:
         raise ValueError("logits and out: expected [B, G, V], out float32, on one device")
     B, G, V = shape
+    _c_ints("B, G and V", B, G, V)
     l_b, l_i, l_v = logits.stride()
     o_b, o_i, o_v = out.stride()
     if V > 1 and (l_v != 1 or o_v != 1):
