@@ -580,6 +580,8 @@ def dflash_logits_adjust(logits, out, ws, counts=None, prompt_mask=None, req_slo
         raise ValueError("logits and out: expected [B, G, V], out float32, on one device")
     B, G, V = shape
     _c_ints("B, G and V", B, G, V)
+    if not (bias_start is None) == (bias_ids is None) == (bias_vals is None):
+        raise ValueError("bias_start, bias_ids and bias_vals come together")
     l_b, l_i, l_v = logits.stride()
     o_b, o_i, o_v = out.stride()
     if V > 1 and (l_v != 1 or o_v != 1):
