@@ -402,8 +402,9 @@ enum { DFLASH_TYPE_BF16 = 0, DFLASH_TYPE_F16 = 1, DFLASH_TYPE_F32 = 2 };
 enum { DFLASH_CACHE_BF16 = 0, DFLASH_CACHE_F16 = 1, DFLASH_CACHE_E4M3 = 2 };
 
 /* One layer's cache (host struct).  Constraints: page_size 16, 32, 64 or 128;
- * head_dim 64 or 128; pages 16-byte aligned; page strides multiples of 16
- * bytes and at least n_kv_heads * page_size * head_dim elements. */
+ * head_dim 64 or 128; n_kv_heads at most 4,096; pages 16-byte aligned; page
+ * strides multiples of 16 bytes, at least n_kv_heads * page_size * head_dim and
+ * at most 2^38 elements. */
 typedef struct dflash_paged_cache {
   void* k_pages;           /* [n_pages][n_kv_heads, page_size, head_dim], pages k_page_stride apart */
   void* v_pages;
@@ -434,14 +435,14 @@ typedef struct dflash_paged_batch {
   const int64_t* kv_len;     /* [B] */
   const int32_t* page_table; /* [B, max_pages], rows table_stride apart */
   long long table_stride;    /* elements, >= max_pages */
-  int B;
+  int B;                     /* 1 to 65,535 */
   int max_pages;             /* max_pages * page_size < 2^30 */
-  int rows;                  /* rows the row tensors hold */
+  int rows;                  /* rows the row tensors hold, at most 2^30 */
 } dflash_paged_batch;
 
 /* A tensor of rows (host struct): [rows, heads, head_dim], head_dim
  * contiguous; 16-byte aligned, strides (in elements) multiples of 8, at least
- * head_dim.  Rows that are written must not overlap one another, nor anything
+ * head_dim and at most 2^40.  Rows that are written must not overlap one another, nor anything
  * else that the call reads or writes. */
 typedef struct dflash_rows {
   void* ptr;
@@ -478,7 +479,9 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  *   max_rows  no request has more new rows than this; at most `rows`; 0: nothing
  *             is launched
  *   scale     finite and > 0;  causal 0 or 1;  window >= 0, 0 = none
- * n_q_heads is a multiple of n_kv_heads.  Cache rows that no row of a request
+ * n_q_heads is a multiple of n_kv_heads, at most 65,535.  With R = max_rows *
+ * n_q_heads / n_kv_heads, R and B * ceil(R / 256) are at most 2^30, and
+ * (max_pages * page_size / 128 + 16) * n_kv_heads is below 2^31.  Cache rows that no row of a request
  * sees (behind its length, before its window, in pages it does not list) may
  * hold anything, NaN included.  A visible row that is not finite makes the
  * outputs of that request and KV head undefined, no other's.  Sums are float32:
@@ -514,13 +517,17 @@ typedef struct dflash_logit_rules {
  * before it as produced, as they are if position i is reached:
  *   c  = counts[slot][v] + #{j < i : draft[b][j] = v}
  *   l1 = l / r if l > 0 else l * r, where c > 0 or v is in the prompt; else l
+ *        (the quotient as l * (1 / r): two roundings)
  *   l2 = l1 - (f * c + (c > 0 ? p : 0))
  *   l3 = l2 + the request's biases of v
  *   out[b, i, v] = l3 if allowed, else -infinity
  * in float32.  A position whose mask allows nothing is all -infinity (greedy
  * verification then takes id 0; dflash_probs has no distribution to return).
  *   type     DFLASH_TYPE_F32, _BF16 or _F16: logits [B, G, V] with strides
- *            l_b and l_i between requests and positions, V contiguous
+ *            l_b and l_i between requests and positions, V contiguous;
+ *            G at most 64 (2 at least if there are drafts), B * G at most
+ *            65,535, V at most 2^18 as for dflash_probs and dflash_verify;
+ *            strides 0 to 2^40
  *   out      float32 [B, G, V], strides o_b and o_i; out may be logits itself
  *            (float32, equal strides) and may not overlap it otherwise
  * Device status: DFLASH_ERR_ARG if a slot is outside [0, slots) (its counts and
