@@ -492,7 +492,7 @@ def _rows(name, t, index):
 def _batch(row_start, kv_len, page_table, rows, index):
     B = kv_len.shape[0]
     if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not torch.int32 or \
-            page_table.get_device() != index or (page_table.stride(1) != 1 and page_table.numel()):
+            page_table.get_device() != index or (page_table.stride(1) != 1 and page_table.shape[1] > 1 and B):
         raise ValueError(f"page_table: expected int32 [{B}, max_pages] on cuda:{index}")
     pages = page_table.shape[1]
     return _PACK_BATCH(_fit("row_start", row_start, torch.int32, (B + 1,), index),

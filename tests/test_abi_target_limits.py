@@ -65,3 +65,14 @@ def test_limits_that_the_header_names_are_the_ones_that_are_kept():
                      (dict(V=1 << 18), dict(V=(1 << 18) + 1)), (dict(l=1 << 40), dict(l=(1 << 40) + 1)),
                      (dict(G=2, draft=4096), dict(G=1, draft=4096))):
         assert adjust(**at) == -7 and adjust(**past) == -2, past
+
+
+def test_binding_takes_a_page_table_of_one_column_whatever_its_stride():
+    """A column's stride says nothing where there is one column."""
+    start, lens = torch.zeros(4, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)
+    table = torch.tensor([[3, 0, 2]], dtype=torch.int32)
+    assert table.t().stride() == (1, 3)
+    packed = dfl._batch(start, lens, table.t(), 5, -1)
+    assert packed == dfl._PACK_BATCH(start.data_ptr(), lens.data_ptr(), table.data_ptr(), 1, 3, 1, 5)
+    with pytest.raises(ValueError):
+        dfl._batch(start, lens, torch.zeros(2, 3, dtype=torch.int32).t(), 5, -1)
