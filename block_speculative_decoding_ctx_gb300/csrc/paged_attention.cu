@@ -18,7 +18,7 @@
 // keys) run side by side, each with its own S and O in tensor memory and its
 // own softmax warpgroup, so that one's softmax runs under the other's products,
 // and a stream's scores of one half are made while the other half is weighed
-// (prompt chunk: 992 us with whole tiles of 128 keys, 925 so):
+// (prompt chunk: 992 us with whole tiles of 128 keys, 925 so, when that was tried):
 //   an item of more than 128 rows: its two Q tiles, both over every key tile
 //     (each K/V byte feeds 256 rows);
 //   a smaller one: even and odd key tiles of its one Q tile, joined at the end.
@@ -31,7 +31,7 @@
 //               wait whose previous phase is still open returns at once.)
 //   warps 1, 2  issue their stream's S = Q K^T (both from shared memory; a warp
 //               for both streams made each wait for the other's: blocks of 8
-//               203 us against 178) and
+//               203 us against 178, when that was tried) and
 //               O += P V (P from tensor memory, V MN-major as TMA left it), and
 //               (16-bit caches) zero the V rows that no row of the item sees (a
 //               weight of 0 times whatever lies there must not become NaN)
@@ -51,18 +51,22 @@
 // down to 2^-17: all in all 2^-13 for bf16 and 2^-16 for fp16, 2^-20 and 2^-23 of
 // the row's largest.  (E4M3 terms throughout leave 2^-17 of it.)  The key scale
 // multiplies the score in float32.
-//   The weights, times the value scales in float32, need the exponents of a
-// float32: a first position that takes nine tenths of a row over 131,072 keys
-// leaves the others 2^-20 of its weight, a value row much larger than the rest
-// pushes them further down, and all of them together are the output.  (Sums of
-// E5M2 terms end at 2^-24 of the reference; such outputs came out a tenth too
-// small and worse.)  So they are bf16, and V is widened to bf16, which is exact:
-// the softmax warpgroup of a stream, its weights made, widens the half tile that
-// they weigh into a buffer of its own (widen_v).  fp16 outputs take the weights
-// as two bf16 terms, 16 bits.  Their error is a 16-bit cache's.
+//   The weights, times the value scales in float32, and V are fp16: the softmax
+// warpgroup of a stream, its weights made, widens the codes of the half tile that
+// they weigh into a buffer of its own, exactly (widen_v).  A first position that
+// takes nine tenths of a row over 131,072 keys leaves the others 2^-20 of its
+// weight, and they are the output if its values are small, as such positions'
+// are.  So what a row's reference follows is weight times value scale: the
+// largest score of four neighbouring keys and the largest of their value scales
+// (a key's own: 201 us for the ragged blocks where four take 196), and the last
+// place of a weight is 2^-35 of that.  (Weights as three E5M2 terms for
+// kind::f8f6f4 end at 2^-24; outputs behind a dominant key came out a tenth too
+// small and worse.  bf16 weights and values need no such care, but the weights'
+// rounding is as large as the output's: errors of 2.3e-3 to 2.5e-3 where these
+// have 1.6e-3.)
 //   If a small item has no more than 64 rows, its two softmax warps without rows
-// widen all of V, for the two with rows set the pace (32 x 8 rows: 182 us, where
-// all four widen 203).
+// widen all of V, for the two with rows set the pace (32 x 8 rows with bf16
+// weights: 182 us, where all four widen 219).
 //
 // All waits are bounded.  When one gives up, the softmax warps run on without
 // waiting (their barriers stay matched, results are void, the status word says
@@ -71,8 +75,8 @@
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16):
 //   32 requests, blocks of 8, context 8,192: HBM.  171 us for 1.08 GB, 6.3 TB/s,
 //     0.93 of the measured copy;
-//   the same over an E4M3 cache: 182 us for 0.56 GB.  Softmax warps (scales and
-//     their barriers, two products more per weight); prompt chunks 1,655 us, where
+//   the same over an E4M3 cache: 177 us for 0.56 GB.  Softmax warps (scales and
+//     their barriers, two products more per weight); prompt chunks 1,622 us, where
 //     each stream widens V for itself, 1.8 times the bf16 cache's;
 //   prompt chunk, 2 x 2,048 rows, context up to 16,384: the tensor cores under
 //     the power limit, 911 us, 1.32 PFLOP/s at 1.75 GHz and 1,390 W, 0.77 of
@@ -174,6 +178,31 @@ __device__ __forceinline__ bool find_item(const KernelArgs& k, int* pair, int en
   return false;
 }
 
+// Where a reader stands in the two rings of slots: the first slot of the
+// segment in either, and the phase it waits for there.
+struct Rings {
+  int at[2];
+  uint32_t phase[2];
+
+  static __device__ __forceinline__ void advance(int half, int& at, uint32_t& phase, int n) {
+    at += n;
+    if (at >= half) {
+      at -= half;
+      phase ^= 1u;
+    }
+  }
+  // past a segment of nt tiles: of K in one ring and V in the other, or (split)
+  // of both in the ring of the stream that has every other tile
+  __device__ __forceinline__ void leave(int half, bool split, int nt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = at[i] + (split ? 2 * ((nt + 1 - i) / 2) : nt);
+      at[i] = n % half;
+      phase[i] ^= (uint32_t)(n / half) & 1u;
+    }
+  }
+};
+
 // The CTA's part of the line as segments of items.
 struct Seg {
   Item it;
@@ -183,6 +212,8 @@ struct Seg {
   bool first, last;
   int slot;        // partial slot
   int pair;
+  int v_at;        // E4M3: the stream's first V slot in its ring, and its phase
+  uint32_t v_phase;
   long long end;   // where the item ends on the line, from the CTA's first unit on
 };
 
@@ -242,8 +273,8 @@ struct Walk {
 
 // E4M3 scales of a tile: this one's, the next one's, and the last one's that a
 // slower warp may still be reading.
-template <bool E4M3>
-constexpr int kScaleTurns = E4M3 ? 3 : 1;
+constexpr int kScaleTurns = 3;
+constexpr int kScales = 2 * kKT + kKT / 4;  // key scales, value scales, log2 of the largest of every four of these
 
 template <bool E4M3>
 struct Ctrl {
@@ -252,13 +283,14 @@ struct Ctrl {
   uint64_t q_full[2], o_full, fin;
   Start start;
   Walk walk[2];  // of the softmax warpgroups: kept here, not in every thread's registers
+  Rings rings[2];  // theirs too (E4M3)
   Seg seg[2][2];  // [warpgroup][turn]
   int more[2][2];
   int abort_flag;
   uint32_t tmem;
-  // per warpgroup: key and value scales; (m, l) of the join; row scales of Q.
+  // per warpgroup: scales; (m, l) of the join; row scales of Q.
   // Before the roles start: scratch of the scan
-  alignas(16) float x[2][kScaleTurns<E4M3> * 256];
+  alignas(16) float x[2][E4M3 ? kScaleTurns * kScales : 256];
 };
 template <bool E4M3>
 constexpr int kCtrlBytes = (int)((sizeof(Ctrl<E4M3>) + 1023) / 1024 * 1024);
@@ -380,23 +412,9 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
   }
 }
-// Four E4M3 codes as bf16 values, exactly, the first and third in one word and
-// the second and fourth in the other: the sign and, four places lower, exponent
-// and mantissa are a bf16 2^120 too small, subnormal where the code is.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& even, uint32_t& odd) {
-  const uint32_t e = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
-  const uint32_t o = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
-  const __nv_bfloat162 f(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));
-  const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&e), f);
-  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o), f);
-  even = *reinterpret_cast<const uint32_t*>(&x);
-  odd = *reinterpret_cast<const uint32_t*>(&y);
-}
-
-// Half a tile's V, kHK rows of codes as TMA left them, as bf16 in the layout of
-// a 16-bit tile (spans of 64 columns, 128-byte swizzle) but for the second and
-// third of every four columns, which change places (e4m3x4_to_bf16), by the
-// threads t = 0 .. N - 1; rows outside [lo, hi) as zeros: no row of the item
+// Half a tile's V, kHK rows of codes as TMA left them, as fp16 in the layout of
+// a 16-bit tile (spans of 64 columns, 128-byte swizzle), by the threads t = 0 ..
+// N - 1; rows outside [lo, hi) as zeros: no row of the item
 // sees them, and a weight of 0 times whatever lies there must not become NaN.
 // Eight threads read 4 chunks of 16 codes from either of two rows whose chunks
 // lie in different banks, as they come and as they go: r and r ^ 5 for rows of
@@ -416,11 +434,11 @@ __device__ __forceinline__ void widen_v(const uint8_t* codes, uint8_t* wide, int
   for (int r = 0; r < kHK; r += kRows) {
     uint4 c = make_uint4(0u, 0u, 0u, 0u), w;
     if (r0 + r >= lo && r0 + r < hi) c = *reinterpret_cast<const uint4*>(from + r * HD);
-    e4m3x4_to_bf16(c.x, w.x, w.y);
-    e4m3x4_to_bf16(c.y, w.z, w.w);
+    w = make_uint4(e4m3x2_to_f16x2((uint16_t)c.x), e4m3x2_to_f16x2((uint16_t)(c.x >> 16)),
+                   e4m3x2_to_f16x2((uint16_t)c.y), e4m3x2_to_f16x2((uint16_t)(c.y >> 16)));
     *reinterpret_cast<uint4*>(to0 + r * 128) = w;
-    e4m3x4_to_bf16(c.z, w.x, w.y);
-    e4m3x4_to_bf16(c.w, w.z, w.w);
+    w = make_uint4(e4m3x2_to_f16x2((uint16_t)c.z), e4m3x2_to_f16x2((uint16_t)(c.z >> 16)),
+                   e4m3x2_to_f16x2((uint16_t)c.w), e4m3x2_to_f16x2((uint16_t)(c.w >> 16)));
     *reinterpret_cast<uint4*>(to1 + r * 128) = w;
   }
 }
@@ -430,10 +448,9 @@ struct Cfg {
   static constexpr int kRow = E4M3 ? HD : HD * 2;          // bytes of a cached row
   static constexpr int kTile = kKT * kRow;                 // of a K or V tile
   static constexpr int kQTerms = E4M3 ? (BF16 ? 2 : 3) : 1;
-  static constexpr int kPTerms = E4M3 && !BF16 ? 2 : 1;
-  static constexpr bool kPBf16 = E4M3 || BF16;             // type of the weights
+  static constexpr bool kPBf16 = !E4M3 && BF16;            // type of the weights and of V
   static constexpr int kQTile = kMT * kRow * kQTerms;
-  static constexpr int kWide = E4M3 ? kHK * HD * 2 : 0;    // V of half a tile, widened
+  static constexpr int kWide = E4M3 ? kHK * HD * 2 : 0;    // V of half a tile, widened to fp16
   // Growth of a row's reference (log2) before O is rescaled: as much as the
   // weights' type holds beside the factor on them (fp16 to 2^15).  A bf16 has
   // float32's exponents (mid-size prompt chunk: 112.7 us with 2^60, 112.9 with
@@ -448,8 +465,12 @@ struct Cfg {
   // which 131,072 keys that share a hundredth of a row are a quarter and more
   // each).  2^0 / 2^7 / 2^9 / 2^11 / 2^13, the headroom what they leave of 2^15:
   // mid-size fp16 prompt chunk 137.8 / 142.2 / 143.5 / 144.8 / 146.4 us, long one
-  // 860 / 878 / 880 / 890 / 899, blocks alike.
-  static constexpr float kShift = kPBf16 ? -kHeadroom : 11.0f;
+  // 860 / 878 / 880 / 890 / 899, blocks alike.  Over codes 2^7 / 2^9 / 2^11: ragged
+  // blocks 192.5 / 193.9 / 195.9 us, long prompt chunk 1,611 / 1,615 / 1,622.
+  static constexpr float kShift = kPBf16 ? -kHeadroom : 15.0f - kHeadroom;
+  // log2 of the smallest value scale that a reference follows: weights without
+  // their scales, at most 2^15 over it, stay far from float32's end.
+  static constexpr float kLeastScale = -64.0f;
   // Operand layouts.  A row of K or Q is kRow bytes cut into spans of at most
   // 128; a span of all rows is one swizzled tile (128-byte swizzle, or 64 for
   // 64-byte rows), spans kKT x span bytes apart.
@@ -458,11 +479,9 @@ struct Cfg {
   static constexpr int kQkSteps = kRow / 32;
   static constexpr int kPvSteps = kHK / 16;  // keys per MMA
   static constexpr int kVStep = 16 * 128;    // bytes of V to the next MMA's keys
-  // Column of the weights of MMA kk (and term) in S: the weights of 32 keys lie
-  // in the 32 columns that held those keys' scores.
-  static __host__ __device__ constexpr uint32_t p_col(int term, int kk) {
-    return (kk >> 1) * 32 + term * 16 + (kk & 1) * 8;
-  }
+  // Column of the weights of MMA kk in S: the weights of 32 keys lie in the first
+  // of the 32 columns that held those keys' scores.
+  static __host__ __device__ constexpr uint32_t p_col(int kk) { return (kk >> 1) * 32 + (kk & 1) * 8; }
   static constexpr uint32_t kDescHi = (uint32_t)((8 * kSpan) >> 4) | (1u << 14) | ((kSpan == 64 ? 4u : 2u) << 29);
   // V, 16-bit spans of 128 bytes: next span along N in the lower word
   static constexpr uint32_t kVDescHi = (uint32_t)((8 * 128) >> 4) | (1u << 14) | (2u << 29);
@@ -471,31 +490,6 @@ struct Cfg {
     return E4M3 ? idesc_f8(kMT, kHK, term > 0) : idesc_f32acc(kMT, kHK, BF16);
   }
   static constexpr uint32_t kIdPv = idesc_f32acc(kMT, HD, kPBf16) | (1u << 16);  // V MN-major
-};
-
-// Where a reader stands in the two rings of slots: the first slot of the
-// segment in either, and the phase it waits for there.
-struct Rings {
-  int at[2] = {0, 0};
-  uint32_t phase[2] = {0, 0};
-
-  static __device__ __forceinline__ void advance(int half, int& at, uint32_t& phase, int n) {
-    at += n;
-    if (at >= half) {
-      at -= half;
-      phase ^= 1u;
-    }
-  }
-  // past a segment of nt tiles: of K in one ring and V in the other, or (split)
-  // of both in the ring of the stream that has every other tile
-  __device__ __forceinline__ void leave(int half, bool split, int nt) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int n = at[i] + (split ? 2 * ((nt + 1 - i) / 2) : nt);
-      at[i] = n % half;
-      phase[i] ^= (uint32_t)(n / half) & 1u;
-    }
-  }
 };
 
 // ------------------------------------------------------------------ Q tile
@@ -694,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk.begin(c->start, w1 - w0);
       const int shift = a.batch.page_shift, page_rows = 1 << shift, per_tile = kKT >> shift;
       auto advance = [&](int& at, uint32_t& phase, int n) { Rings::advance(k.half, at, phase, n); };
-      Rings rings;
+      Rings rings = {};
       uint32_t used = 0, parity = 0;  // per slot: in use, phase of its last load
       bool ok = true;
       while (ok && walk.next(k, &s)) {
@@ -776,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kHalfD = (kHK * C::kSpan) >> 4;  // a tile's second half of K rows
       constexpr uint32_t kHalfV = E4M3 ? (WIDES - 1) * (C::kWide >> 4) : kHalfD;  // of V
       uint32_t seg = 0, p_phase = 0;
-      Rings rings;
+      Rings rings = {};
       bool ok = true;
       while (true) {
         ok = warp_wait_on(&c->q_full[0], seg & 1u, stop, a.status) &&
@@ -857,11 +851,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t keep = t > first || h > 0;  // O holds earlier jobs
 #pragma unroll
               for (int kk = 0; kk < C::kPvSteps; ++kk)
-#pragma unroll
-                for (int term = 0; term < C::kPTerms; ++term)
-                  tc_mma_f16_ta(tO, tS + h * kHK + C::p_col(term, kk),
-                                desc64(vd + h * kHalfV + kk * (C::kVStep >> 4), C::kVDescHi), C::kIdPv,
-                                (term > 0 || kk > 0) ? 1u : keep);
+                tc_mma_f16_ta(tO, tS + h * kHK + C::p_col(kk),
+                              desc64(vd + h * kHalfV + kk * (C::kVStep >> 4), C::kVDescHi), C::kIdPv,
+                              kk > 0 ? 1u : keep);
               tc_commit(&c->pv_done[st][h]);
               if (h && !E4M3) give_back(&v_empty[vs]);
               if (h && E4M3) {  // its codes have been read: P came after them
@@ -902,12 +894,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + wg * kKT, tO = tmem + lane_off + kColO;
     float* const x0 = c->x[wg];
     uint32_t tiles = 0, seg = 0;
-    Rings rings;  // E4M3
     // the next segment's description, a segment ahead
     auto describe = [&](uint32_t turn) {
       Seg* n = &c->seg[wg][turn & 1u];
       const bool more = c->walk[wg].next(k, n);
       c->more[wg][turn & 1u] = more;
+      if (E4M3 && more) {
+        Rings& rings = c->rings[wg];
+        const int vr = !n->split || wg;
+        n->v_at = rings.at[vr];
+        n->v_phase = rings.phase[vr];
+        if (n->split) Rings::advance(k.half, n->v_at, n->v_phase, 1);
+        rings.leave(k.half, n->split, n->nt);
+      }
       if (wg == 0 && more && n->first && !n->last) {
         const long long u = w0 + n->end - 1;  // the item's last unit
         const int last = few ? ((int)(u + 1) * ctas - 1) / (int)W : (int)(((u + 1) * ctas - 1) / W);
@@ -916,6 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (t == 0) {
       c->walk[wg].begin(c->start, w1 - w0);
+      c->rings[wg] = {};
       if (wg == 0) k.rec[cta].pair = -1;
       describe(0);
     }
@@ -977,16 +977,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // what was fetched into one of the buffers
       auto put = [&](int turn) {
-        x0[turn * 256 + t] = nks;
-        x0[turn * 256 + 128 + t] = nvs;
+        x0[turn * kScales + t] = nks;
+        x0[turn * kScales + kKT + t] = nvs;
+        float top = fabsf(nvs);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if ((t & 3) == 0) x0[turn * kScales + 2 * kKT + t / 4] = fmaxf(__log2f(top), C::kLeastScale);
       };
       // no more than 64 rows: the two warps without any widen all of V
       const bool idle = s.split && it.rows <= 64;
       // E4M3: this stream's V slots, as its MMA warp would follow them
-      const bool vr = !s.split || wg;
-      int vs = rings.at[vr];
-      uint32_t vp = rings.phase[vr];
-      if (s.split) Rings::advance(k.half, vs, vp, 1);
+      int vs = s.v_at;
+      uint32_t vp = s.v_phase;
       int turn = 0;
       if (E4M3) {
         look_up(t0 + j0);
@@ -998,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         look_up(t0 + j0 + 2 * step);
       }
       for (int j = j0; j < nt; j += step) {
-        const float* x = x0 + turn * 256;
+        const float* x = x0 + turn * kScales;
         if (E4M3) {
           // the next tile's scales go where the last but one's were; after the
           // barrier this tile's are there and nobody reads the last one's
@@ -1019,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the last one.
           auto widen = [&] {
             if (!E4M3) return;
-            const int slot = (vr ? k.half : 0) + vs, at = (t0 + j) * kKT + h * kHK;
+            const int slot = (s.split && !wg ? 0 : k.half) + vs, at = (t0 + j) * kKT + h * kHK;
             if (h) Rings::advance(k.half, vs, vp, step);
             if (idle && t < 64) return;
             if (h == 0) (void)warp_wait_on(&c->full[slot], vp, stop, a.status);
@@ -1072,14 +1074,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_ld(v1);
           ready(0, v0);
           ready(1, v1);
-          // ---- the row's largest score
+          // ---- the row's largest score; E4M3: of score and value scale
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
+            if (E4M3) {
+              // a score times its scale is at most the largest of four times theirs
+              const float* l4 = x + 2 * kKT + (h * kHK + e) / 4;
+              mx[0] = fmaxf(mx[0], fmaf(fmaxf(fmaxf(v0[e], v0[e + 1]), fmaxf(v0[e + 2], v0[e + 3])), cs, l4[0]));
+              mx[1] = fmaxf(mx[1], fmaf(fmaxf(fmaxf(v1[e], v1[e + 1]), fmaxf(v1[e + 2], v1[e + 3])), cs, l4[8]));
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(v0[e + i], v1[e + i]));
+              for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(v0[e + i], v1[e + i]));
+            }
           }
-          const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
+          const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (E4M3 ? 1.0f : cs);
           const bool grow = m_tile > m_ref + C::kHeadroom || (m_ref == -INFINITY && m_tile > -INFINITY);
           if (__any_sync(0xffffffffu, grow)) {
             const float m_new = grow ? m_tile : m_ref;
@@ -1112,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 cs2 = make_float2(cs, cs), nb2 = make_float2(nb, nb);
           float2 ls0 = make_float2(0.0f, 0.0f), ls1 = ls0;
           auto weigh = [&](int q, const float (&v)[32]) {
-            uint32_t pw[16], rest[16];  // 16-bit weights of 32 keys, and what they leave
+            uint32_t pw[16];  // 16-bit weights of 32 keys
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               float2 p0 = fma2(make_float2(v[e], v[e + 1]), cs2, nb2), p1 = fma2(make_float2(v[e + 2], v[e + 3]), cs2, nb2);
@@ -1121,20 +1130,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               ls0 = add2(ls0, p0);
               ls1 = add2(ls1, p1);
               if (E4M3) {
-                const float4 f = *reinterpret_cast<const float4*>(x + 128 + h * kHK + q * 32 + e);
+                const float4 f = *reinterpret_cast<const float4*>(x + kKT + h * kHK + q * 32 + e);
                 p0 = mul2(p0, make_float2(f.x, f.y));
                 p1 = mul2(p1, make_float2(f.z, f.w));
               }
               pw[e / 2] = pack16<C::kPBf16>(p0.x, p0.y);
               pw[e / 2 + 1] = pack16<C::kPBf16>(p1.x, p1.y);
-              if (C::kPTerms == 2) {
-                const float2 r0 = unpack16<true>(pw[e / 2]), r1 = unpack16<true>(pw[e / 2 + 1]);
-                rest[e / 2] = pack16<true>(p0.x - r0.x, p0.y - r0.y);
-                rest[e / 2 + 1] = pack16<true>(p1.x - r1.x, p1.y - r1.y);
-              }
             }
             tmem_st(ta + q * 32, pw);
-            if (C::kPTerms == 2) tmem_st(ta + q * 32 + 16, rest);
           };
           weigh(0, v0);
           weigh(1, v1);
@@ -1188,14 +1191,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (have1) o[e] = fmaf(o1[e], f1, o[e]);
           }
           if (!real) continue;
-          if (E4M3) {  // columns as widen_v laid them out
-#pragma unroll
-            for (int e = 1; e < 32; e += 4) {
-              const float x = o[e];
-              o[e] = o[e + 1];
-              o[e + 1] = x;
-            }
-          }
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(out + col * 2);
 #pragma unroll
@@ -1216,7 +1211,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      if (E4M3) rings.leave(k.half, s.split, s.nt);
     }
   }
 
@@ -1428,8 +1422,8 @@ int launch_paged_attention(const CUtensorMap& k, const CUtensorMap& v, const Pag
                            int format, int type, void* ws, cudaStream_t s) {
   const bool bf = type == DFLASH_TYPE_BF16, e = format == DFLASH_CACHE_E4M3;
   // Three terms of two Q tiles leave the rings one slot each beside four widened
-  // halves of V: two then.  (Elsewhere four: with two, ragged blocks took 235 us
-  // against 216, a prompt chunk 1,696 against 1,709.)
+  // halves of V: two then.  (Elsewhere four: with two, when that was tried, ragged
+  // blocks took 235 us against 216, a prompt chunk 1,696 against 1,709.)
   const bool two = part_rows(a.group, a.max_rows) > kMT;
   if (head_dim == 128) {
     if (e && bf) return launch<128, true, true, 2>(k, v, a, ws, s);

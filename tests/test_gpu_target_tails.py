@@ -14,7 +14,7 @@ import torch
 import block_speculative_decoding_ctx_gb300 as dfl
 from oracle import quant
 from oracle import target as ot
-from target_testutil import HALF_STEP, Paged, rows_tensor, run_attention, to64
+from target_testutil import HALF_STEP, Paged, check_attention, rows_tensor, run_attention, to64
 
 pytestmark = pytest.mark.gpu
 BF, FH = torch.bfloat16, torch.float16
@@ -64,8 +64,11 @@ def bound(out, lse, mean, size, n, hd, dtype, q64, k64, e4m3):
                truncate) of Z = scale sum |q||k|, the reference taken off and
                2^x: d = 2 (hd + 4) e Z + 4 e Z + 8 e, a softmax mean is off by
                2 d A;
-      weights  rounded to 16 bits: u A.  They have an exponent for every weight
-               that counts, so there is nothing absolute beside it;
+      weights  rounded to 16 bits: u A.  In fp16 (over codes, and over fp16 rows)
+               a weight's last place is at most 2^-35 of the row's largest part,
+               half of it is left out: over codes that largest part is a key's
+               weight times its value scale, and the dominant key's values are
+               small here, so that there is nothing beside u A;
       sums     an accumulator takes 16 keys at a time, 2 e of it each: n / 8 e A;
                the weights' own sum 32 at a time and e: n / 32 e A; a few joins;
       output   u of itself."""
@@ -185,3 +188,22 @@ def test_attention_of_very_large_values_under_scores_that_grow(e4m3, size):
     out, lse, status = run_attention(p, q, causal=False)
     assert status == 0
     compare(p, q, k64, v64, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+def test_attention_over_codes_takes_scales_of_any_size_and_sign(dtype):
+    """value = code * scale, whoever filled the cache: zeros, negative scales,
+    scales that differ by 2^40."""
+    p = Paged([700, 90, 300], [8, 20, 3], 2, 128, 32, dtype, True, seed=6, garbage=False)
+    g = torch.Generator().manual_seed(1)
+    for i in range(2):
+        kind = torch.randint(0, 6, p.scale[i].shape, generator=g).cuda()
+        f = torch.tensor([1.0, -1.0, 0.0, 2.0 ** -40, -(2.0 ** -20), 2.0 ** -3], device="cuda")
+        p.scale[i] *= f[kind]
+    for b in range(3):                                   # a dominant key beside a value row a thousand times larger
+        p.scale[0][int(p.table_np[b, 0]), :, 5] *= 4.0
+        p.scale[1][int(p.table_np[b, 0]), :, 6] *= 1000.0
+    q = rows_tensor(p.n_rows, 6, 128, dtype, 3, size=1.5)
+    out, lse, status = run_attention(p, q)
+    assert status == 0
+    check_attention(p, q, out, lse)
