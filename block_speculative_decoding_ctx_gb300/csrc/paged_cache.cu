@@ -13,9 +13,10 @@
 //
 // Measured on GB300 (8 KV heads of 128), bytes at the measured copy's rate in
 // brackets: E4M3 prefixes read back (776 MB) 119 us [0.96]; 16-bit prompts
-// written 57 us [0.92]; the same quantised on the way (274 MB) 59 us [0.69],
-// which the instructions of the quotients and conversions bound (65% of the
-// issue slots); a step's 256 rows 8 us, latency.
+// written 57 us [0.92]; the same quantised on the way (274 MB) 58 us [0.70],
+// which instructions bound (66% of the issue slots; 250 a warp for 16 values a
+// thread, some 80 of them quotients, conversions, maxima and packing, most others
+// addresses); a step's 256 rows 8 us, latency.
 #include <cuda_fp8.h>
 
 #include "paged_util.cuh"

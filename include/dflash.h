@@ -484,9 +484,12 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  * (max_pages * page_size / 128 + 16) * n_kv_heads is below 2^31.  Cache rows that no row of a request
  * sees (behind its length, before its window, in pages it does not list) may
  * hold anything, NaN included.  A visible row that is not finite makes the
- * outputs of that request and KV head undefined, no other's.  Sums are float32:
- * bf16 values of any finite size do, but what adds less than 2^-96 to an output
- * may be lost. */
+ * outputs of that request and KV head undefined, no other's.
+ * Precision: statistics and sums are float32.  Weights are rounded to bf16 over a
+ * BF16 cache, to fp16 over the others, where one that is below 2^-25 of the row's
+ * largest (E4M3: times the value scales) keeps fewer bits, the last at 2^-35.
+ * bf16 values of any finite size do; what adds less than 2^-96 to an output (2^-64
+ * for value scales of E4M3) may be lost. */
 size_t dflash_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim,
                                               int max_rows);
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_batch* batch,
