@@ -414,11 +414,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 // Half a tile's V, kHK rows of codes as TMA left them, as fp16 in the layout of
 // a 16-bit tile (spans of 64 columns, 128-byte swizzle), by the threads t = 0 ..
-// N - 1; rows outside [lo, hi) as zeros: no row of the item
-// sees them, and a weight of 0 times whatever lies there must not become NaN.
-// Eight threads read 4 chunks of 16 codes from either of two rows whose chunks
-// lie in different banks, as they come and as they go: r and r ^ 5 for rows of
-// 128 codes, r and r ^ 1 for rows of 64.
+// N - 1; rows outside [lo, hi) as zeros: no row of the item sees them, and a
+// weight of 0 times whatever lies there must not become NaN.  Eight threads read
+// 4 chunks of 16 codes from either of two rows whose chunks lie in different
+// banks, as they come and as they go: r and r ^ 5 for rows of 128 codes, r and
+// r ^ 1 for rows of 64.
 template <int HD, int N>
 __device__ __forceinline__ void widen_v(const uint8_t* codes, uint8_t* wide, int lo, int hi, int t) {
   constexpr int kRows = N * 16 / HD;  // at once
@@ -461,9 +461,9 @@ struct Cfg {
   // finite as far as the formula's do (2^30 let values above 2^80 overflow); what
   // is lost for it lies 2^96 below the largest.  An fp16 ends at 2^-24: the weights
   // of a long tail behind one dominant key need the range more than rescaling
-  // needs headroom.  Their last place is 2^-35 of the reference (2^-24 before, of
-  // which 131,072 keys that share a hundredth of a row are a quarter and more
-  // each).  2^0 / 2^7 / 2^9 / 2^11 / 2^13, the headroom what they leave of 2^15:
+  // needs headroom.  Their last place is 2^-35 of the reference; without the factor
+  // it is 2^-24, no less than each of 131,072 keys weighs that share a hundredth of
+  // a row.  2^0 / 2^7 / 2^9 / 2^11 / 2^13, the headroom what they leave of 2^15:
   // mid-size fp16 prompt chunk 137.8 / 142.2 / 143.5 / 144.8 / 146.4 us, long one
   // 860 / 878 / 880 / 890 / 899, blocks alike.  Over codes 2^7 / 2^9 / 2^11: ragged
   // blocks 192.5 / 193.9 / 195.9 us, long prompt chunk 1,611 / 1,615 / 1,622.
