@@ -1,6 +1,6 @@
 """Appends and reads back of batches whose rows are not one full list: padding
 behind the last request, rows before the first, requests that do not fit in
-front of ones that do."""
+front of ones that do; attention of items of very different sizes."""
 
 import numpy as np
 import pytest
@@ -8,7 +8,7 @@ import torch
 
 import block_speculative_decoding_ctx_gb300 as dfl
 from oracle import target as ot
-from target_testutil import Paged, rows_tensor, to64
+from target_testutil import Paged, check_attention, rows_tensor, run_attention, to64
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -65,3 +65,27 @@ def test_requests_that_fit_are_moved_whatever_stands_before_them(start, rows, fi
     for got, w in zip(p.host(), want):
         if w is not None:
             np.testing.assert_array_equal(got, w)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, torch.float16])
+def test_attention_of_small_and_large_items_in_turn_over_codes(dtype, hd):
+    """Items of one and of two query tiles, of 1 to 8 key tiles, in one call and
+    so many that a CTA meets several of either kind: every depth of the rings of
+    slots, each left at an odd place by some item before."""
+    rng = np.random.default_rng(7)
+    lens, rows = [], []
+    for i in range(110):
+        n = int(rng.choice([0, 1, 3, 10, 17, 40, 90]))
+        rows.append(n)
+        lens.append(n + int(rng.choice([0, 1, 127, 128, 300, 900])))
+    p = Paged(lens, rows, 3, hd, 32, dtype, True, seed=11)
+    q = rows_tensor(p.n_rows, 12, hd, dtype, 3, extra=1, size=1.5)
+    first = None
+    for _ in range(3):
+        out, lse, status = run_attention(p, q, window=500)
+        assert status == 0
+        if first is None:
+            first = (out.clone(), lse.clone())
+            check_attention(p, q, out, lse, window=500)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
