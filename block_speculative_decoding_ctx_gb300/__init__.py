@@ -69,7 +69,8 @@ class dflash_sampling(ctypes.Structure):
 
 
 DFLASH_TYPE_BF16, DFLASH_TYPE_F16, DFLASH_TYPE_F32 = 0, 1, 2
-DFLASH_CACHE_BF16, DFLASH_CACHE_F16, DFLASH_CACHE_E4M3 = 0, 1, 2
+DFLASH_CACHE_BF16, DFLASH_CACHE_F16, DFLASH_CACHE_E4M3, DFLASH_CACHE_E2M1 = 0, 1, 2, 4
+DFLASH_ROPE_HALF, DFLASH_ROPE_INTERLEAVED = 0, 1
 
 _TYPES = {torch.bfloat16: DFLASH_TYPE_BF16, torch.float16: DFLASH_TYPE_F16,
           torch.float32: DFLASH_TYPE_F32}
@@ -99,6 +100,11 @@ class dflash_rows(ctypes.Structure):
                 ("head_stride", ctypes.c_longlong)]
 
 
+class dflash_rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_ulonglong * 64), ("factor", ctypes.c_float)] + [
+        (n, ctypes.c_int) for n in ("rotary_dim", "layout", "reserved")]
+
+
 class dflash_logit_rules(ctypes.Structure):
     _fields_ = [("counts", ctypes.c_void_p), ("prompt_mask", ctypes.c_void_p),
                 ("req_slot", ctypes.c_void_p), ("slots", ctypes.c_int)] + [
@@ -116,6 +122,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_D = ctypes.c_double
 
 
 def lib():
@@ -155,6 +162,9 @@ def lib():
         "dflash_paged_workspace_bytes": (_SZ, []),
         "dflash_paged_append": (_I, [_P, _P, _I, _P, _P, _P, _SZ, _P]),
         "dflash_paged_gather": (_I, [_P, _P, _I, _P, _P, _P, _SZ, _P]),
+        "dflash_rope_frequencies": (_I, [_I, _D, _D, _D, _D, _D, _P]),
+        "dflash_rope_init": (_I, [_I, _I, _P, ctypes.c_float, _P]),
+        "dflash_paged_append_rope": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
         "dflash_paged_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
         "dflash_paged_attention": (_I, [_P, _P, _I, _I, _P, _P, _P, _I, ctypes.c_float, _I, _I, _P,
                                         _SZ, _P]),
@@ -454,11 +464,14 @@ def _workspace(ws, index):
     return ws.data_ptr()
 
 
-def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None):
+def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None, format=None):
     """A cache for the dflash_paged_* calls: pages [n_pages, n_kv_heads,
     page_size, head_dim] of bfloat16, float16, or E4M3 codes (float8_e4m3fn or
     uint8) with float32 scales [n_pages, n_kv_heads, page_size].  A page is
-    contiguous; pages may lie further apart (a slice of a larger tensor)."""
+    contiguous; pages may lie further apart (a slice of a larger tensor).
+    With format=DFLASH_CACHE_E2M1 pages are uint8 records [n_pages, n_kv_heads,
+    page_size, head_dim * 5 / 8] and hold their scales; format is otherwise told
+    by the type."""
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or \
             v_pages.device != k_pages.device:
         raise ValueError("k_pages and v_pages: expected [n_pages, n_kv_heads, page_size, head_dim], alike in "
@@ -470,6 +483,12 @@ def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None):
         if n and not t[0].is_contiguous():
             raise ValueError("a page is not contiguous")
     fmt = _CACHES[k_pages.dtype]
+    if format == DFLASH_CACHE_E2M1:
+        if k_pages.dtype is not torch.uint8 or hd % 5 or k_scale is not None or v_scale is not None:
+            raise ValueError("E2M1 pages are uint8 records of head_dim * 5 / 8 bytes and come without k_scale and v_scale")
+        fmt = format
+    elif format is not None and format != fmt:
+        raise ValueError(f"{k_pages.dtype} pages are not of format {format}")
     if (fmt == DFLASH_CACHE_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
         raise ValueError("E4M3 pages come with k_scale and v_scale, 16-bit pages without")
     index = k_pages.get_device()
@@ -479,7 +498,7 @@ def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None):
                            _fit("k_scale", k_scale, torch.float32, shape, index),
                            _fit("v_scale", v_scale, torch.float32, shape, index),
                            k_pages.stride(0) if n > 1 else page, v_pages.stride(0) if n > 1 else page,
-                           n, heads, size, hd, fmt, None)
+                           n, heads, size, hd * 8 // 5 if fmt == DFLASH_CACHE_E2M1 else hd, fmt, None)
     return PagedCache(c, (k_pages, v_pages, k_scale, v_scale), index)
 
 
@@ -530,6 +549,54 @@ def dflash_paged_gather(cache, k, v, row_start, kv_len, page_table, ws, stream=N
     back into k, v [rows, n_kv_heads, head_dim]."""
     _paged_move(lib().dflash_paged_gather, "dflash_paged_gather", cache, k, v, row_start, kv_len, page_table, ws,
                 stream)
+
+
+def dflash_rope_frequencies(rotary_dim, theta, stretch=1.0, trained=0.0, slow=1.0, fast=4.0):
+    """Radians per position of every pair, a list of rotary_dim / 2 floats."""
+    _c_ints("rotary_dim", rotary_dim)
+    f = (ctypes.c_double * max(1, rotary_dim // 2))()
+    _check(lib().dflash_rope_frequencies(rotary_dim, theta, stretch, trained, slow, fast, f), "dflash_rope_frequencies")
+    return list(f)
+
+
+def dflash_rope_init(frequencies, layout=DFLASH_ROPE_HALF, factor=1.0):
+    """A rotation of 2 * len(frequencies) values of a head, for
+    dflash_paged_append_rope."""
+    n = len(frequencies)
+    rope = dflash_rope()
+    _check(lib().dflash_rope_init(2 * n, layout, (ctypes.c_double * max(1, n))(*frequencies), factor, ctypes.byref(rope)),
+           "dflash_rope_init")
+    return rope
+
+
+def dflash_paged_append_rope(cache, k, v, row_start, kv_len, page_table, rope, ws, q=None, q_out=None,
+                             positions=None, stream=None):
+    """dflash_paged_append with keys (and queries, q to q_out [rows, n_q_heads,
+    head_dim]; q_out may be q) rotated; positions int64 [rows] or None: the
+    cache's."""
+    index = cache.index
+    if k.shape != v.shape or k.dtype is not v.dtype or k.shape[1:] != cache._rows:
+        raise ValueError("k and v: expected [rows, %d, %d] of one type" % cache._rows)
+    if k.dtype is not torch.bfloat16 and k.dtype is not torch.float16:
+        raise ValueError(f"no rows of {k.dtype}")
+    n, n_q = k.shape[0], 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        n_q = q.shape[1] if q.dim() == 3 else 0
+        if q.shape != (n, n_q, cache._rows[1]) or not n_q or q_out.shape != q.shape or q.dtype is not k.dtype or \
+                q_out.dtype is not k.dtype:
+            raise ValueError(f"q and q_out: expected [{n}, n_q_heads, {cache._rows[1]}] of the type of k")
+    if not isinstance(rope, dflash_rope):
+        raise ValueError("rope: expected what dflash_rope_init returns")
+    stream = _current(index, stream)
+    code = lib().dflash_paged_append_rope(
+        cache._bytes, _batch(row_start, kv_len, page_table, n, index), _TYPES[k.dtype], _rows("k", k, index),
+        _rows("v", v, index), n_q, _rows("q", q, index) if n_q else None, _rows("q_out", q_out, index) if n_q else None,
+        ctypes.addressof(rope), _fit("positions", positions, torch.int64, (n,), index) or None, _workspace(ws, index),
+        ws.numel(), stream)
+    if code:
+        raise DflashError(code, "dflash_paged_append_rope")
 
 
 def dflash_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_rows):

@@ -1,5 +1,5 @@
-// Internal interface of the paged-cache operators (paged_cache.cu,
-// paged_attention.cu) and of the logit adjustment (logits.cu).
+// Internal interface of the paged-cache operators (paged_cache.cu, paged_rope.cu,
+// paged_attention.cu, paged_attention_e2m1.cu) and of the logit adjustment (logits.cu).
 #pragma once
 
 #include <cuda.h>
@@ -31,6 +31,22 @@ struct PagedMoveArgs {
   int* status;
 };
 
+// Bytes of a row's record in an E2M1 cache: codes, then scales.
+constexpr int e2m1_record(int head_dim) { return head_dim * 5 / 8; }
+
+// With rotation (rope.rotary_dim > 0), with queries (n_q > 0), or both.
+struct PagedRopeArgs {
+  PagedMoveArgs m;
+  const uint8_t* q;
+  uint8_t* q_out;
+  long long q_row, q_head, o_row, o_head;
+  int n_q;
+  const int64_t* positions;  // or nullptr: the cache's
+  dflash_rope rope;
+};
+
+// E2M1 caches, and all formats with rotation.
+int launch_paged_append_rope(const PagedRopeArgs& a, int head_dim, int format, int type, cudaStream_t s);
 int launch_paged_append(const PagedMoveArgs& a, int head_dim, int format, int type, cudaStream_t s);
 int launch_paged_gather(const PagedMoveArgs& a, int head_dim, int format, int type, cudaStream_t s);
 
@@ -60,6 +76,9 @@ struct PagedAttnArgs {
 size_t paged_attention_workspace(int n_q, int n_kv, int head_dim, int max_rows);
 int launch_paged_attention(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnArgs& a, int head_dim,
                            int format, int type, void* workspace, cudaStream_t s);
+// Over an E2M1 cache.
+int launch_paged_attention_e2m1(const dflash_paged_cache& c, const PagedAttnArgs& a, int type, void* workspace,
+                                cudaStream_t s);
 
 struct LogitsArgs {
   const void* logits;

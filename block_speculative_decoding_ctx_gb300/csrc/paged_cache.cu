@@ -17,9 +17,7 @@
 // which instructions bound (66% of the issue slots; 250 a warp for 16 values a
 // thread, some 80 of them quotients, conversions, maxima and packing, most others
 // addresses); a step's 256 rows 8 us, latency.
-#include <cuda_fp8.h>
-
-#include "paged_util.cuh"
+#include "paged_rows.cuh"
 
 namespace dfl {
 namespace {
@@ -35,100 +33,27 @@ constexpr int kPieces = 2;
 constexpr int kMostUnits = 256, kBlocks = 608;
 
 // E4M3 codes of 16 values over s: x / s rounded to float32, then to E4M3.
-// The quotient's rounding matters, since values that lie exactly half way
-// between two codes are common (0.75 of the largest value is one).  It is
-// made from the correctly rounded y = 1 / s: q = x y is a unit or two in the
-// last place off, r = x - q s is exact in a fused operation, and q + r y
-// rounded once is the quotient (P. Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990), three operations
-// where a division takes ten or more.  A scale so small that y or r could leave
-// float32's range takes the division.
 template <bool BF16>
 __device__ __forceinline__ uint4 quantize16(const uint32_t (&v)[8], float s) {
   const float y = __fdiv_rn(1.0f, s);
-  const float2 y2 = make_float2(y, y), ms = make_float2(-s, -s);
   uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 x = unpack16<BF16>(v[i]);
-    float2 q = mul2(x, y2);
-    q = fma2(fma2(q, ms, x), y2, q);
-    c[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-  }
-  if (s < 0x1p-100f) {
+  for (int i = 0; i < 8; ++i)
+    c[i] = __nv_cvt_float2_to_fp8x2(quotients(unpack16<BF16>(v[i]), s, y), __NV_SATFINITE, __NV_E4M3);
+  if (quotients_small(s)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 x = unpack16<BF16>(v[i]);
-      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)), __NV_SATFINITE, __NV_E4M3);
-    }
+    for (int i = 0; i < 8; ++i)
+      c[i] = __nv_cvt_float2_to_fp8x2(quotients_slow(unpack16<BF16>(v[i]), s), __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint4(c[0] | (c[1] << 16), c[2] | (c[3] << 16), c[4] | (c[5] << 16), c[6] | (c[7] << 16));
 }
 
-struct Place {
-  bool owned;  // some request owns the row
-  bool there;  // and its position has a row of the cache
-  long long page;
-  int at;
-};
-
-// What a block learns from the requests that fit the call.
-struct Found {
-  int b0;    // the first one that ends after the block's first row
-  int end;   // the row behind the last that any of them owns: none from there on is touched
-  int odd;   // some request does not fit: row_start need not rise
-};
-__device__ __forceinline__ void look_through(const PagedBatch& p, int n0, int* status, Found* found) {
-  if (threadIdx.x == 0) *found = {p.B, 0, 0};
-  __syncthreads();
-  int b0 = p.B, end = 0, odd = 0;
-  for (int b = threadIdx.x; b < p.B; b += kMoveThreads) {
-    RequestSpan r;
-    if (!request_span(p, b, &r)) {
-      odd = 1;
-      if (blockIdx.x == 0) report_status(status, DFLASH_ERR_SHAPE);
-    } else if (r.n > 0) {
-      if (r.s0 + r.n > n0) b0 = min(b0, b);
-      end = max(end, r.s0 + r.n);
-    }
-  }
-  if (b0 < p.B) atomicMin(&found->b0, b0);
-  if (end) atomicMax(&found->end, end);
-  if (odd) found->odd = 1;
-  __syncthreads();
-}
-
-__device__ __forceinline__ Place find_row(const PagedBatch& p, const Found& found, int n, int* status) {
-  Place r = {false, false, 0, 0};
-  RequestSpan sp;
-  int b = found.b0;
-  for (;; ++b) {
-    if (b >= p.B) return r;
-    if (__ldg(p.row_start + b + 1) <= n || !request_span(p, b, &sp)) continue;
-    if (n >= sp.s0) break;
-    if (!found.odd) return r;  // rows before the first request's
-  }
-  r.owned = true;
-  const int pos = sp.len - sp.n + (n - sp.s0);
-  if (pos < 0) {
-    report_status(status, DFLASH_ERR_SHAPE);
-    return r;
-  }
-  const int page = __ldg(p.table + b * p.table_stride + (pos >> p.page_shift));
-  if (page < 0 || page >= p.n_pages) {
-    report_status(status, DFLASH_ERR_ARG);
-    return r;
-  }
-  r.there = true;
-  r.page = page;
-  r.at = pos & ((1 << p.page_shift) - 1);
-  return r;
-}
-
 // rows: of a block, at most kMoveThreads.
-template <int HD, bool E4M3, bool BF16, bool APPEND>
+template <int HD, int FORMAT, bool BF16, bool APPEND>
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMoveArgs a, int rows) {
   pdl_enter();
+  constexpr bool E4M3 = FORMAT == DFLASH_CACHE_E4M3, E2M1 = FORMAT == DFLASH_CACHE_E2M1;
+  static_assert(!(E2M1 && APPEND), "paged_rope.cu writes those");
   constexpr int kLanes = HD / 16;                   // threads per (row, head, side)
   constexpr int kUnits = kMoveThreads / kLanes;     // (row, head, side) at once
   constexpr int kCell = E4M3 ? 1 : 2;               // bytes of a cached value
@@ -136,7 +61,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
   __shared__ Found found;
   const int n0 = blockIdx.x * rows, lane = threadIdx.x % kLanes;
   const uint32_t per_row = 2u * a.n_kv;
-  look_through(a.batch, n0, a.status, &found);
+  look_through<kMoveThreads>(a.batch, n0, a.status, &found);
   const int mine = max(0, min(rows, found.end - n0));
   const uint32_t units = mine * per_row;
 
@@ -187,7 +112,8 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
       owned[q] = pl.owned && u < units;
       there[q] = pl.there && u < units;
       const size_t row = ((size_t)p.head << a.batch.page_shift) + pl.at;
-      cell[q] = a.pages[p.side] + ((size_t)pl.page * a.page_stride[p.side] + row * HD + lane * 16) * kCell;
+      cell[q] = E2M1 ? a.pages[p.side] + (size_t)pl.page * a.page_stride[p.side] + row * e2m1_record(HD) + lane * 8
+                     : a.pages[p.side] + ((size_t)pl.page * a.page_stride[p.side] + row * HD + lane * 16) * kCell;
       scale[q] = a.scale[p.side] + (((size_t)pl.page * a.n_kv) << a.batch.page_shift) + row;
     }
     if (APPEND) {
@@ -223,7 +149,11 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
       for (int q = 0; q < kPieces; ++q) {
         w[q][0] = w[q][1] = make_uint4(0u, 0u, 0u, 0u);
         if (!there[q]) continue;
-        if (E4M3) {
+        if (E2M1) {
+          const uint2 w8 = __ldg(reinterpret_cast<const uint2*>(cell[q]));
+          c[q] = make_uint4(w8.x, w8.y, 0u, 0u);
+          s[q] = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(cell[q] + HD / 2 - lane * 6)) << 16);
+        } else if (E4M3) {
           c[q] = __ldg(reinterpret_cast<const uint4*>(cell[q]));
           s[q] = __ldg(scale[q]);
         } else {
@@ -234,6 +164,18 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
 #pragma unroll
       for (int q = 0; q < kPieces; ++q) {
         if (!owned[q]) continue;
+        if (E2M1 && there[q]) {
+          uint32_t f[8], o[8];
+          e2m1x8_to_f16x2(c[q].x, reinterpret_cast<uint32_t(&)[4]>(f[0]));
+          e2m1x8_to_f16x2(c[q].y, reinterpret_cast<uint32_t(&)[4]>(f[4]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 x2 = unpack16<false>(f[i]);
+            o[i] = pack16<BF16>(x2.x * s[q], x2.y * s[q]);
+          }
+          w[q][0] = make_uint4(o[0], o[1], o[2], o[3]);
+          w[q][1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
         if (E4M3 && there[q]) {
           const uint32_t v[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
           uint32_t o[8];
@@ -252,34 +194,38 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const PagedMov
   }
 }
 
-template <int HD, bool E4M3, bool BF16, bool APPEND>
+template <int HD, int FORMAT, bool BF16, bool APPEND>
 int launch_move(const PagedMoveArgs& a, cudaStream_t s) {
   const int per_row = 2 * a.n_kv, at_once = kMoveThreads / (HD / 16);
   const long long units = (long long)a.batch.rows * per_row;
   const long long each = min((long long)kMostUnits, max((long long)at_once, units / kBlocks));
   const int rows = min(kMoveThreads, max(1, (int)(each / per_row)));
   const int grid = max(1, ceil_div(a.batch.rows, rows));
-  return launch_pdl(paged_move_kernel<HD, E4M3, BF16, APPEND>, dim3(grid), dim3(kMoveThreads), 0, s, a, rows);
+  return launch_pdl(paged_move_kernel<HD, FORMAT, BF16, APPEND>, dim3(grid), dim3(kMoveThreads), 0, s, a, rows);
 }
 
-template <bool APPEND>
-int dispatch(const PagedMoveArgs& a, int head_dim, int format, int type, cudaStream_t s) {
-  const bool bf = type == DFLASH_TYPE_BF16, e = format == DFLASH_CACHE_E4M3;
-  if (head_dim == 128) {
-    if (!e) return launch_move<128, false, false, APPEND>(a, s);
-    return bf ? launch_move<128, true, true, APPEND>(a, s) : launch_move<128, true, false, APPEND>(a, s);
+// The 16-bit formats move alike.
+template <int HD, bool APPEND>
+int dispatch(const PagedMoveArgs& a, int format, int type, cudaStream_t s) {
+  const bool bf = type == DFLASH_TYPE_BF16;
+  if (format == DFLASH_CACHE_E4M3)
+    return bf ? launch_move<HD, DFLASH_CACHE_E4M3, true, APPEND>(a, s)
+              : launch_move<HD, DFLASH_CACHE_E4M3, false, APPEND>(a, s);
+  if constexpr (!APPEND) {
+    if (format == DFLASH_CACHE_E2M1)
+      return bf ? launch_move<HD, DFLASH_CACHE_E2M1, true, APPEND>(a, s)
+                : launch_move<HD, DFLASH_CACHE_E2M1, false, APPEND>(a, s);
   }
-  if (!e) return launch_move<64, false, false, APPEND>(a, s);
-  return bf ? launch_move<64, true, true, APPEND>(a, s) : launch_move<64, true, false, APPEND>(a, s);
+  return launch_move<HD, DFLASH_CACHE_F16, false, APPEND>(a, s);
 }
 
 }  // namespace
 
 int launch_paged_append(const PagedMoveArgs& a, int head_dim, int format, int type, cudaStream_t s) {
-  return dispatch<true>(a, head_dim, format, type, s);
+  return head_dim == 128 ? dispatch<128, true>(a, format, type, s) : dispatch<64, true>(a, format, type, s);
 }
 int launch_paged_gather(const PagedMoveArgs& a, int head_dim, int format, int type, cudaStream_t s) {
-  return dispatch<false>(a, head_dim, format, type, s);
+  return head_dim == 128 ? dispatch<128, false>(a, format, type, s) : dispatch<64, false>(a, format, type, s);
 }
 
 }  // namespace dfl

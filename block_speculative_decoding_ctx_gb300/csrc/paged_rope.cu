@@ -1,0 +1,243 @@
+// Writing rows of keys and values into a paged cache with positions rotated into
+// the keys, and into queries beside them (dflash_paged_append_rope), and writing
+// E2M1 caches with or without (dflash_paged_append); the rules are in
+// include/dflash.h.
+//
+//   a' = f (a cos t - b sin t),  b' = f (b cos t + a sin t),  t = P w_j
+//
+// Every byte is moved once and a value takes a handful of operations, so memory
+// bounds it (or, for a step's few rows, the latency of row_start -> kv_len ->
+// page_table).  A block has a few rows.  It finds their places and makes their
+// sines and cosines once for all heads: P times w_j / (2 pi) in 2^-64ths of a
+// turn is a product of integers modulo 2^64, exact for any position; what is left
+// of it beside the nearest quarter turn is at most an eighth of a turn and becomes
+// a float32.
+//   Then a thread moves 16 values of one (row, head of q, k or v) at a time, two
+// such pieces on their way: two runs of 8 values, for a rotated row of layout
+// HALF the two whose values are each other's pairs (values 8 l and rotary_dim / 2
+// + 8 l on), else neighbours.  rotary_dim is a multiple of 32, so that a block of
+// 16 values (E2M1) is two lanes' lower runs, two lanes' upper runs or one lane's
+// both, and one shuffle finds its largest magnitude.
+#include "paged_rows.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 2;  // of a thread on their way
+constexpr int kMaxRows = 8; // of a block
+
+// Sine and cosine of `turns` 2^-64ths of a turn, times f.
+__device__ __forceinline__ float2 cos_sin(unsigned long long turns, float f) {
+  const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62);
+  const long long rest = (long long)(turns - ((unsigned long long)quarter << 62));
+  const float half_turns = (float)(int)(rest >> 32) * 0x1p-31f;
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+  // quarter 0: (c, s)  1: (-s, c)  2: (-c, -s)  3: (s, -c)
+  return make_float2(quarter == 1 || quarter == 2 ? -x * f : x * f, quarter >= 2 ? -y * f : y * f);
+}
+
+struct Piece {
+  int row, slot;        // of the block; head of q, then k, then v
+  int c0, c1;           // first columns of its two runs
+  bool turned;
+  const uint8_t* x;
+};
+
+template <int HD, int FORMAT, bool BF16>
+__global__ void __launch_bounds__(kThreads) paged_rope_kernel(const PagedRopeArgs a, int rows) {
+  pdl_enter();
+  constexpr bool E4M3 = FORMAT == DFLASH_CACHE_E4M3, E2M1 = FORMAT == DFLASH_CACHE_E2M1;
+  constexpr int kLanes = HD / 16;              // threads per (row, head)
+  constexpr int kUnits = kThreads / kLanes;    // (row, head) at once
+  __shared__ Place places[kMaxRows];
+  __shared__ Found found;
+  __shared__ float2 turn_s[kMaxRows][64];      // cosine and sine
+  const PagedMoveArgs& m = a.m;
+  const int n0 = blockIdx.x * rows, lane = threadIdx.x % kLanes;
+  const int half = a.rope.rotary_dim / 2;      // pairs
+  const uint32_t per_row = a.n_q + 2u * m.n_kv;
+  look_through<kThreads>(m.batch, n0, m.status, &found);
+  const int mine = max(0, min(rows, found.end - n0));
+  const uint32_t units = mine * per_row;
+
+  auto piece = [&](uint32_t u) {
+    Piece p;
+    p.row = (int)(u / per_row);
+    p.slot = (int)(u - p.row * per_row);
+    const size_t n = n0 + p.row;
+    p.turned = p.slot < a.n_q + m.n_kv && lane * 8 < half;
+    p.c0 = p.turned ? lane * 8 : lane * 16;
+    p.c1 = p.turned ? half + lane * 8 : lane * 16 + 8;
+    if (p.slot < a.n_q) {
+      p.x = a.q + (n * a.q_row + (size_t)p.slot * a.q_head) * 2;
+    } else {
+      const int side = p.slot >= a.n_q + m.n_kv, head = p.slot - a.n_q - side * m.n_kv;
+      p.x = m.x[side] + (n * m.row_stride[side] + (size_t)head * m.head_stride[side]) * 2;
+    }
+    return p;
+  };
+  uint4 w[kPieces][2] = {};
+  auto load_rows = [&](uint32_t u0) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t u = u0 + i * kUnits;
+      if (u < units) {
+        const Piece p = piece(u);
+        w[i][0] = *reinterpret_cast<const uint4*>(p.x + p.c0 * 2);
+        w[i][1] = *reinterpret_cast<const uint4*>(p.x + p.c1 * 2);
+      }
+    }
+  };
+  // the first rows are on their way while places and angles are made
+  load_rows(threadIdx.x / kLanes);
+  if ((int)threadIdx.x < mine) places[threadIdx.x] = find_row(m.batch, found, n0 + threadIdx.x, m.status);
+  __syncthreads();
+  for (int i = threadIdx.x; i < mine * half; i += kThreads) {
+    const int row = i / half, j = i - row * half;
+    const long long pos = a.positions ? (long long)__ldg(a.positions + n0 + row) : places[row].pos;
+    turn_s[row][j] = cos_sin((unsigned long long)pos * a.rope.turns[j], a.rope.factor);
+  }
+  __syncthreads();
+
+  // whole warps stay together: pieces past the last take part in the shuffles
+  const uint32_t turns = (units + kUnits * kPieces - 1) / (kUnits * kPieces);
+  for (uint32_t turn = 0; turn < turns; ++turn) {
+    const uint32_t u0 = turn * (kUnits * kPieces) + threadIdx.x / kLanes;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t u = u0 + i * kUnits;
+      const Piece p = piece(min(u, units - 1));
+      const Place pl = places[p.row];
+      const uint32_t v[8] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w, w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+      float2 f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = unpack16<BF16>(v[e]);
+      if (p.turned) {
+        const float2* t = turn_s[p.row];
+        if (a.rope.layout == DFLASH_ROPE_HALF) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 cs = *reinterpret_cast<const float4*>(t + p.c0 + 2 * e);
+            const float2 x = f[e], y = f[4 + e];
+            f[e] = make_float2(x.x * cs.x - y.x * cs.y, x.y * cs.z - y.y * cs.w);
+            f[4 + e] = make_float2(y.x * cs.x + x.x * cs.y, y.y * cs.z + x.y * cs.w);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 cs = t[(e < 4 ? p.c0 : p.c1) / 2 + (e & 3)], x = f[e];
+            f[e] = make_float2(x.x * cs.x - x.y * cs.y, x.y * cs.x + x.x * cs.y);
+          }
+        }
+      }
+      uint32_t o[8];
+      if (p.slot < a.n_q || (!E4M3 && !E2M1)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = pack16<BF16>(f[e].x, f[e].y);
+      }
+      // magnitudes of float32 order like their bits, NaN above infinity
+      uint32_t m0 = 0, m1 = 0;
+      if (E4M3 || E2M1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          m0 = max(m0, max(__float_as_uint(f[e].x) & 0x7FFFFFFFu, __float_as_uint(f[e].y) & 0x7FFFFFFFu));
+          m1 = max(m1, max(__float_as_uint(f[4 + e].x) & 0x7FFFFFFFu, __float_as_uint(f[4 + e].y) & 0x7FFFFFFFu));
+        }
+        if (E4M3) {
+          m0 = max(m0, m1);
+#pragma unroll
+          for (int s = kLanes / 2; s > 0; s >>= 1) m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, s));
+        } else {
+          const uint32_t n0_ = __shfl_xor_sync(0xffffffffu, m0, 1), n1_ = __shfl_xor_sync(0xffffffffu, m1, 1);
+          const uint32_t both = max(m0, m1);
+          m0 = p.turned ? max(m0, n0_) : both;
+          m1 = p.turned ? max(m1, n1_) : both;
+        }
+      }
+      if (u >= units) continue;
+      if (p.slot < a.n_q) {
+        if (!pl.owned || pl.pos < 0) continue;
+        uint8_t* q = a.q_out + ((size_t)(n0 + p.row) * a.o_row + (size_t)p.slot * a.o_head) * 2;
+        *reinterpret_cast<uint4*>(q + p.c0 * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(q + p.c1 * 2) = make_uint4(o[4], o[5], o[6], o[7]);
+        continue;
+      }
+      if (!pl.there) continue;
+      const int side = p.slot >= a.n_q + m.n_kv, head = p.slot - a.n_q - side * m.n_kv;
+      const size_t row = ((size_t)head << m.batch.page_shift) + pl.at;
+      uint8_t* page = m.pages[side] + (size_t)pl.page * m.page_stride[side] * (E4M3 || E2M1 ? 1 : 2);
+      if (E2M1) {
+        uint8_t* rec = page + row * e2m1_record(HD);
+        const bool finite0 = m0 < 0x7F800000u, finite1 = m1 < 0x7F800000u;
+        auto scale = [](uint32_t top, bool finite) {
+          const float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 6.0f)));
+          return !finite ? __uint_as_float(0x7FC00000u) : s == 0.0f ? 1.0f : s;
+        };
+        const float s0 = scale(m0, finite0), s1 = scale(m1, finite1);
+        const float y0 = __fdiv_rn(1.0f, s0), y1 = __fdiv_rn(1.0f, s1);
+        uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // (a zero keeps its sign, which quotients() loses)
+          auto code = [](float2 x, float s, float y) {
+            const float2 q = quotients_small(s) ? quotients_slow(x, s) : quotients(x, s, y);
+            return e2m1x2(make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y)));
+          };
+          c0 |= code(f[e], s0, y0) << (8 * e);
+          c1 |= code(f[4 + e], s1, y1) << (8 * e);
+        }
+        *reinterpret_cast<uint32_t*>(rec + p.c0 / 2) = c0;
+        *reinterpret_cast<uint32_t*>(rec + p.c1 / 2) = c1;
+        // a block's scale by the lane with its first run
+        uint16_t* scales = reinterpret_cast<uint16_t*>(rec + HD / 2);
+        if (p.c0 % 16 == 0) scales[p.c0 / 16] = (uint16_t)(__float_as_uint(s0) >> 16);
+        if (p.c1 % 16 == 0) scales[p.c1 / 16] = (uint16_t)(__float_as_uint(s1) >> 16);
+      } else if (E4M3) {
+        const bool finite = m0 < 0x7F800000u;
+        const float s = !finite ? __uint_as_float(0x7FC00000u) : m0 ? __fdiv_rn(__uint_as_float(m0), 448.0f) : 1.0f;
+        const float y = __fdiv_rn(1.0f, s);
+        uint32_t c[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          c[e] = __nv_cvt_float2_to_fp8x2(quotients_small(s) ? quotients_slow(f[e], s) : quotients(f[e], s, y),
+                                          __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint2*>(page + row * HD + p.c0) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        *reinterpret_cast<uint2*>(page + row * HD + p.c1) = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
+        if (lane == 0) m.scale[side][(((size_t)pl.page * m.n_kv) << m.batch.page_shift) + row] = s;
+      } else {
+        *reinterpret_cast<uint4*>(page + (row * HD + p.c0) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(page + (row * HD + p.c1) * 2) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+    if (turn + 1 < turns) load_rows(u0 + kUnits * kPieces);
+  }
+}
+
+template <int HD, int FORMAT, bool BF16>
+int launch_rope(const PagedRopeArgs& a, cudaStream_t s) {
+  const long long each = a.m.batch.rows / 608;  // 4 blocks for each of 152 SMs come first
+  const int rows = (int)min((long long)kMaxRows, max(1ll, each));
+  const int grid = max(1, ceil_div(a.m.batch.rows, rows));
+  return launch_pdl(paged_rope_kernel<HD, FORMAT, BF16>, dim3(grid), dim3(kThreads), 0, s, a, rows);
+}
+
+template <int HD>
+int dispatch(const PagedRopeArgs& a, int format, int type, cudaStream_t s) {
+  const bool bf = type == DFLASH_TYPE_BF16;
+  if (format == DFLASH_CACHE_E2M1)
+    return bf ? launch_rope<HD, DFLASH_CACHE_E2M1, true>(a, s) : launch_rope<HD, DFLASH_CACHE_E2M1, false>(a, s);
+  if (format == DFLASH_CACHE_E4M3)
+    return bf ? launch_rope<HD, DFLASH_CACHE_E4M3, true>(a, s) : launch_rope<HD, DFLASH_CACHE_E4M3, false>(a, s);
+  return bf ? launch_rope<HD, DFLASH_CACHE_BF16, true>(a, s) : launch_rope<HD, DFLASH_CACHE_F16, false>(a, s);
+}
+
+}  // namespace
+
+int launch_paged_append_rope(const PagedRopeArgs& a, int head_dim, int format, int type, cudaStream_t s) {
+  return head_dim == 128 ? dispatch<128>(a, format, type, s) : dispatch<64>(a, format, type, s);
+}
+
+}  // namespace dfl

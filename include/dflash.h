@@ -383,6 +383,17 @@ int dflash_quantize_e4m3(const void* w, int rows, int cols, void* codes, float* 
  *              scale = max|row| / 448 (1 for a row of zeros; NaN for a row
  *              that holds a NaN or an infinity, which then reads back as NaN),
  *              code = value / scale rounded to nearest, ties to even.
+ *   E2M1       4-bit codes (1 sign, 2 exponent bits with bias 1, 1 mantissa bit:
+ *              0, 0.5, 1, 1.5, 2, 3, 4, 6) with one bfloat16 scale for every 16
+ *              neighbouring values of a row: value = code * scale, scale =
+ *              max|block| / 6 (a float32 quotient) rounded to bfloat16 (1 where
+ *              that is 0; NaN for a block that holds a NaN or an infinity, which
+ *              then reads back as NaN), code = value / scale (likewise) rounded to
+ *              nearest, ties to even, at most 6 in magnitude, the sign kept on
+ *              values that become 0.
+ *              A row is one record of head_dim * 5 / 8 bytes: head_dim / 2 bytes
+ *              of codes (value 2i in the lower, 2i + 1 in the upper half of byte
+ *              i), then its head_dim / 16 scales.
  *
  * Rows.  q, k, v and the outputs hold the new rows of all requests one after
  * another: request b owns rows row_start[b] .. row_start[b + 1] - 1, and its
@@ -399,12 +410,14 @@ int dflash_quantize_e4m3(const void* w, int rows, int cols, void* codes, float* 
  * rows are not written, and read as zeros.
  */
 enum { DFLASH_TYPE_BF16 = 0, DFLASH_TYPE_F16 = 1, DFLASH_TYPE_F32 = 2 };
-enum { DFLASH_CACHE_BF16 = 0, DFLASH_CACHE_F16 = 1, DFLASH_CACHE_E4M3 = 2 };
+enum { DFLASH_CACHE_BF16 = 0, DFLASH_CACHE_F16 = 1, DFLASH_CACHE_E4M3 = 2,
+       DFLASH_CACHE_E2M1 = 4 }; /* 3 is no format */
 
 /* One layer's cache (host struct).  Constraints: page_size 16, 32, 64 or 128;
  * head_dim 64 or 128; n_kv_heads at most 4,096; pages 16-byte aligned; page
  * strides multiples of 16 bytes, at least n_kv_heads * page_size * head_dim and
- * at most 2^38 elements. */
+ * at most 2^38 elements.  Of an E2M1 cache a page is [n_kv_heads, page_size]
+ * records and its strides count bytes. */
 typedef struct dflash_paged_cache {
   void* k_pages;           /* [n_pages][n_kv_heads, page_size, head_dim], pages k_page_stride apart */
   void* v_pages;
@@ -423,7 +436,8 @@ typedef struct dflash_paged_cache {
 /* The TMA descriptors that attention needs of a cache (host memory owned by
  * the caller, 384 bytes).  Making them takes a few microseconds of the host's
  * time; a caller that keeps them beside the cache saves that in every call.
- * Attention refuses (DFLASH_ERR_ARG) maps whose cache had any other field. */
+ * Attention refuses (DFLASH_ERR_ARG) maps whose cache had any other field.  An
+ * E2M1 cache needs none: its maps only hold its fields. */
 typedef struct dflash_paged_maps {
   unsigned long long opaque[48];
 } dflash_paged_maps;
@@ -452,7 +466,8 @@ typedef struct dflash_rows {
 
 size_t dflash_paged_workspace_bytes(void); /* for append and gather */
 
-/* Write the new rows' keys and values into the cache, quantised if it is E4M3.
+/* Write the new rows' keys and values into the cache, quantised if it is E4M3
+ * or E2M1.
  *   type  DFLASH_TYPE_BF16 or _F16, the type of k and v; a 16-bit cache has
  *         the same type.
  * Two rows of one call must not share a (page, row): which one stays would be
@@ -460,6 +475,63 @@ size_t dflash_paged_workspace_bytes(void); /* for append and gather */
 int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_batch* batch, int type,
                         const dflash_rows* k, const dflash_rows* v, void* workspace,
                         size_t ws_bytes, dflash_stream_t stream);
+
+/* Rotary positions.  A row of a head at position P has its first rotary_dim
+ * values turned in pairs (a, b) by the angle P w_j, j < rotary_dim / 2:
+ *   a' = factor (a cos - b sin),  b' = factor (b cos + a sin);
+ *   HALF         pair j is values j and j + rotary_dim / 2;
+ *   INTERLEAVED  pair j is values 2j and 2j + 1.
+ * The other values stay as they are.  Angles are exact to 2^-31 of a turn for
+ * any position below 2^32 in magnitude (counted in 2^-64ths of a turn, modulo one); the rest
+ * is float32. */
+enum { DFLASH_ROPE_HALF = 0, DFLASH_ROPE_INTERLEAVED = 1 };
+
+/* Host struct, filled by dflash_rope_init and only read afterwards; a call
+ * copies it, so it need not outlive the call or a graph that captured it. */
+typedef struct dflash_rope {
+  unsigned long long turns[64]; /* w_j / (2 pi) modulo 1, times 2^64 */
+  float factor;
+  int rotary_dim;
+  int layout; /* DFLASH_ROPE_* */
+  int reserved;
+} dflash_rope;
+
+/* The frequencies w_j = theta^(-2j / rotary_dim), in radians per position, for
+ * positions scaled by `stretch` (host array [rotary_dim / 2]):
+ *   trained = 0:  w_j / stretch;
+ *   trained > 0:  by parts.  Pair j turns r = trained w_j / (2 pi) times over the
+ *     context that the model was trained on; with g = (r - slow) / (fast - slow)
+ *     cut to [0, 1] its frequency is g w_j + (1 - g) w_j / stretch: fast pairs
+ *     stay, slow ones are stretched (B. Peng et al., "YaRN: Efficient context
+ *     window extension of large language models", 2023, section 3.2).
+ * rotary_dim a multiple of 32 from 32 to 128; theta > 0; stretch > 0; trained
+ * >= 0; slow < fast where trained > 0; all finite. */
+int dflash_rope_frequencies(int rotary_dim, double theta, double stretch, double trained, double slow,
+                            double fast, double* frequencies);
+
+/* A rotation by given frequencies (host array [rotary_dim / 2], finite, of any
+ * sign, at most 2^20 in magnitude); rotary_dim as above, factor finite. */
+int dflash_rope_init(int rotary_dim, int layout, const double* frequencies, float factor,
+                     dflash_rope* rope);
+
+/* dflash_paged_append with the keys rotated on the way, and queries beside them.
+ * Keys and queries of row j of request b turn by position kv_len[b] - n_b + j, or
+ * by positions[row_start[b] + j] where positions are given: these set the angle
+ * alone, never the place in the cache.  Rotated keys are rounded once, into the
+ * cache's format (E4M3, E2M1: scales and codes from the float32 values; a value
+ * beyond float32's range counts as infinite); rotated queries to `type`.
+ *   q, q_out   [rows, n_q_heads, head_dim], both NULL with n_q_heads = 0: keys
+ *              only.  q_out may be q itself (equal strides) and may not overlap it
+ *              otherwise.  n_q_heads at most 65,535; it need not be a multiple of
+ *              the KV heads.  Rows that append leaves out because of their page
+ *              id still have their queries rotated; rows before position 0 do not.
+ *   positions  int64 [rows] or NULL
+ * rotary_dim is at most the cache's head_dim. */
+int dflash_paged_append_rope(const dflash_paged_cache* cache, const dflash_paged_batch* batch, int type,
+                             const dflash_rows* k, const dflash_rows* v, int n_q_heads,
+                             const dflash_rows* q, const dflash_rows* q_out, const dflash_rope* rope,
+                             const int64_t* positions, void* workspace, size_t ws_bytes,
+                             dflash_stream_t stream);
 
 /* Read the same positions back: k and v (written here) get rows
  * kv_len[b] - n_b .. kv_len[b] - 1 of every request, code * scale rounded to
@@ -489,7 +561,10 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  * BF16 cache, to fp16 over the others, where one that is below 2^-25 of the row's
  * largest (E4M3: times the value scales) keeps fewer bits, the last at 2^-35.
  * bf16 values of any finite size do; what adds less than 2^-96 to an output (2^-64
- * for value scales of E4M3) may be lost. */
+ * for value scales of E4M3 and E2M1) may be lost.  Over E2M1 the queries become
+ * fp16 times a power of two per row (2^-39 of a row's largest may be lost), keys
+ * and values fp16 times one per row (2^-36 of a row's largest scale); the largest
+ * weight that is followed is that of weight times value scale, as over E4M3. */
 size_t dflash_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim,
                                               int max_rows);
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_batch* batch,

@@ -35,6 +35,9 @@ What it computes, and where each step comes from:
                 token masks on logits (the library's own rules; the pages
                 leave the target's kernels to the serving stack).
 
+* ``e2m1``      rows of that cache in 4 bits.
+* ``rotary``    rotary positions: layouts, part of the head, scaled frequencies.
+
 Floating point is accumulated in float64 throughout.  Integer decisions
 (argmax, accept, inverse-CDF index) are taken exactly as the function
 docstrings state so that a second implementation can match them bit for bit.
@@ -44,4 +47,4 @@ parity with these readings): RoPE placement and base, the pre-norm layer
 layout, the RMSNorm epsilon, the MASK token id, and the Philox counter layout.
 """
 
-from . import philox, fixedpoint, sampling, verify, model, quant, target  # noqa: F401
+from . import philox, fixedpoint, sampling, verify, model, quant, target, e2m1, rotary  # noqa: F401
