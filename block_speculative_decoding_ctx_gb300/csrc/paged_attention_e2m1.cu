@@ -61,11 +61,14 @@ constexpr int kAltRows = 64;   // items of so many rows at most: see Modes
 constexpr uint32_t kColO = 256, kColK = 384;
 constexpr int kScaleExp = 12;  // of a row's largest scale
 constexpr float kUnscale = 0x1p-12f;
-#ifndef FRESH
-#define FRESH 4.0f
-#endif
 constexpr float kUnseen = 0x1p100f;  // minus the reference of a column that has seen no key
-constexpr float kMaxWeight = 15.0f, kFreshWeight = FRESH;  // log2
+// Weights, log2: the largest there may be, and what a reference that grows makes of its
+// tile's largest.
+constexpr float kMaxWeight = 15.0f, kFreshWeight = 4.0f;
+// A weight that makes its column's reference grow once some other column's has to: all
+// that are about to do so at once (prompt chunk with 15 / 13 / 10 / 6: 1,671 / 1,642 /
+// 1,608 / 1,581 us, blocks alike).
+constexpr float kRenewWeight = 6.0f;
 // Exponents (biased) that rows of K and V are scaled by: so that the factors stay
 // normal numbers.  Of V 2^-64 at least: the sums l, in which that power is taken
 // off the weights again, stay finite.
@@ -273,8 +276,8 @@ __device__ __forceinline__ void grow_references(const KernelArgs& k, Ctrl* c, co
   int* const high = c->high[wg] + 2 * (st.lane & 3);
 #pragma unroll
   for (int g = 0; g < NCH; ++g) {
-    max_shared_if(top[g].x + nb[g].x > kMaxWeight, high + g * 8, ordered(__float_as_int(top[g].x)));
-    max_shared_if(top[g].y + nb[g].y > kMaxWeight, high + g * 8 + 1, ordered(__float_as_int(top[g].y)));
+    max_shared_if(top[g].x + nb[g].x > kRenewWeight, high + g * 8, ordered(__float_as_int(top[g].x)));
+    max_shared_if(top[g].y + nb[g].y > kRenewWeight, high + g * 8 + 1, ordered(__float_as_int(top[g].y)));
   }
   named_sync(1 + wg, 128);
   if (st.w4 < 2) {
@@ -648,22 +651,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
           }
           __syncwarp();
         };
-        // Whatever is ready goes next, values before scores: in a fixed order either
-        // waits for what the other's operands wait for.
+        // Whatever is ready goes next: in a fixed order either waits for what the other's
+        // operands wait for (blocks of 8: 219 us against 178, when that was tried).
+        // Scores before values: prompt chunk 1,558 us, 1,583 the other way.
         const int buffers = alt ? 4 : 2;  // of S
         int ns = 0, nv = 0;               // scores and values issued
         unsigned long long since = 0;
 #pragma unroll 1
         for (uint32_t polls = 1; ok && nv < nt; ++polls) {
           const uint32_t us = T + ns, uv = T + nv;
-          if (nv < ns && __all_sync(0xffffffffu, mbar_test(&c->p_full[uv & 1u], (uv >> 1) & 1u)) &&
-              __all_sync(0xffffffffu, mbar_test(&c->v_full[uv & 1u], (uv >> 1) & 1u))) {
-            values(uv, nv >= (alt ? 2 : 1));  // O holds tiles before this one
-            ++nv;
-            polls = since = 0;
-          } else if (ns < nt && ns - nv < buffers && __all_sync(0xffffffffu, mbar_test(&c->k_full[us & 1u], (us >> 1) & 1u))) {
+          if (ns < nt && ns - nv < buffers && __all_sync(0xffffffffu, mbar_test(&c->k_full[us & 1u], (us >> 1) & 1u))) {
             scores(us);
             ++ns;
+            polls = since = 0;
+          } else if (nv < ns && __all_sync(0xffffffffu, mbar_test(&c->p_full[uv & 1u], (uv >> 1) & 1u)) &&
+                     __all_sync(0xffffffffu, mbar_test(&c->v_full[uv & 1u], (uv >> 1) & 1u))) {
+            values(uv, nv >= (alt ? 2 : 1));  // O holds tiles before this one
+            ++nv;
             polls = since = 0;
           } else if ((polls & 63u) == 0) {
             const unsigned long long now = globaltimer_ns();
@@ -985,7 +989,10 @@ int launch(const dflash_paged_cache& cache, const PagedAttnArgs& a, int type, vo
   if (rts * a.batch.B > 1 << 30) return DFLASH_ERR_SHAPE;
   k.rts = (int)rts;
   k.part_rows = part_rows(a.group, a.max_rows);
-  k.seg_cost = 4;
+  // What an item costs beside its tiles, for the cut of the line (queries, their factors,
+  // the first references, the end): of 1 / 4 / 8 / 16 tiles ragged blocks take 223 / 172 /
+  // 147 / 149 us, blocks of 8 149 / 149 / 147 / 154, prompt chunks alike.
+  k.seg_cost = 8;
   k.k_pages = static_cast<const uint8_t*>(cache.k_pages);
   k.v_pages = static_cast<const uint8_t*>(cache.v_pages);
   k.k_stride = cache.k_page_stride;

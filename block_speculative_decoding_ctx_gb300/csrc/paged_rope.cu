@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPieces = 2;  // of a thread on their way
-constexpr int kMaxRows = 8; // of a block
+constexpr int kMaxRows = 32;   // of a block
+constexpr int kMostUnits = 512; // (row, head) of a block, as far as that is no single row
 
 // Sine and cosine of `turns` 2^-64ths of a turn, times f.
 __device__ __forceinline__ float2 cos_sin(unsigned long long turns, float f) {
@@ -46,35 +47,37 @@ struct Piece {
   const uint8_t* x;
 };
 
-template <int HD, int FORMAT, bool BF16>
-__global__ void __launch_bounds__(kThreads) paged_rope_kernel(const PagedRopeArgs a, int rows) {
+// ROPE: else a plain append (an E2M1 cache's).
+template <int HD, int FORMAT, bool BF16, bool ROPE>
+__global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRopeArgs a, int rows, uint32_t magic) {
   pdl_enter();
   constexpr bool E4M3 = FORMAT == DFLASH_CACHE_E4M3, E2M1 = FORMAT == DFLASH_CACHE_E2M1;
   constexpr int kLanes = HD / 16;              // threads per (row, head)
   constexpr int kUnits = kThreads / kLanes;    // (row, head) at once
   __shared__ Place places[kMaxRows];
   __shared__ Found found;
-  __shared__ float2 turn_s[kMaxRows][64];      // cosine and sine
+  __shared__ float2 turn_s[ROPE ? kMaxRows : 1][64];  // cosine and sine
   const PagedMoveArgs& m = a.m;
   const int n0 = blockIdx.x * rows, lane = threadIdx.x % kLanes;
   const int half = a.rope.rotary_dim / 2;      // pairs
-  const uint32_t per_row = a.n_q + 2u * m.n_kv;
+  const int n_q = ROPE ? a.n_q : 0;
+  const uint32_t per_row = n_q + 2u * m.n_kv;
   look_through<kThreads>(m.batch, n0, m.status, &found);
   const int mine = max(0, min(rows, found.end - n0));
   const uint32_t units = mine * per_row;
 
   auto piece = [&](uint32_t u) {
     Piece p;
-    p.row = (int)(u / per_row);
+    p.row = (int)__umulhi(u, magic);  // u / per_row
     p.slot = (int)(u - p.row * per_row);
     const size_t n = n0 + p.row;
-    p.turned = p.slot < a.n_q + m.n_kv && lane * 8 < half;
+    p.turned = ROPE && p.slot < n_q + m.n_kv && lane * 8 < half;
     p.c0 = p.turned ? lane * 8 : lane * 16;
     p.c1 = p.turned ? half + lane * 8 : lane * 16 + 8;
-    if (p.slot < a.n_q) {
+    if (p.slot < n_q) {
       p.x = a.q + (n * a.q_row + (size_t)p.slot * a.q_head) * 2;
     } else {
-      const int side = p.slot >= a.n_q + m.n_kv, head = p.slot - a.n_q - side * m.n_kv;
+      const int side = p.slot >= n_q + m.n_kv, head = p.slot - n_q - side * m.n_kv;
       p.x = m.x[side] + (n * m.row_stride[side] + (size_t)head * m.head_stride[side]) * 2;
     }
     return p;
@@ -95,12 +98,14 @@ __global__ void __launch_bounds__(kThreads) paged_rope_kernel(const PagedRopeArg
   load_rows(threadIdx.x / kLanes);
   if ((int)threadIdx.x < mine) places[threadIdx.x] = find_row(m.batch, found, n0 + threadIdx.x, m.status);
   __syncthreads();
-  for (int i = threadIdx.x; i < mine * half; i += kThreads) {
-    const int row = i / half, j = i - row * half;
-    const long long pos = a.positions ? (long long)__ldg(a.positions + n0 + row) : places[row].pos;
-    turn_s[row][j] = cos_sin((unsigned long long)pos * a.rope.turns[j], a.rope.factor);
+  if (ROPE) {
+    for (int i = threadIdx.x; i < mine * half; i += kThreads) {
+      const int row = i / half, j = i - row * half;
+      const long long pos = a.positions ? (long long)__ldg(a.positions + n0 + row) : places[row].pos;
+      turn_s[row][j] = cos_sin((unsigned long long)pos * a.rope.turns[j], a.rope.factor);
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
   // whole warps stay together: pieces past the last take part in the shuffles
   const uint32_t turns = (units + kUnits * kPieces - 1) / (kUnits * kPieces);
@@ -134,31 +139,36 @@ __global__ void __launch_bounds__(kThreads) paged_rope_kernel(const PagedRopeArg
         }
       }
       uint32_t o[8];
-      if (p.slot < a.n_q || (!E4M3 && !E2M1)) {
+      if (p.slot < n_q || (!E4M3 && !E2M1)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = pack16<BF16>(f[e].x, f[e].y);
       }
-      // magnitudes of float32 order like their bits, NaN above infinity
+      // magnitudes order like their bits, NaN above infinity
       uint32_t m0 = 0, m1 = 0;
-      if (E4M3 || E2M1) {
+      if (!ROPE) {  // as they came, two at a time
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m0 = __vmaxu2(m0, v[e] & 0x7FFF7FFFu);
+        const float2 top = unpack16<BF16>(m0);
+        m0 = m1 = max(__float_as_uint(top.x), __float_as_uint(top.y));
+      } else if (E4M3 || E2M1) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           m0 = max(m0, max(__float_as_uint(f[e].x) & 0x7FFFFFFFu, __float_as_uint(f[e].y) & 0x7FFFFFFFu));
           m1 = max(m1, max(__float_as_uint(f[4 + e].x) & 0x7FFFFFFFu, __float_as_uint(f[4 + e].y) & 0x7FFFFFFFu));
         }
+        const uint32_t both = max(m0, m1);
         if (E4M3) {
-          m0 = max(m0, m1);
+          m0 = both;
 #pragma unroll
           for (int s = kLanes / 2; s > 0; s >>= 1) m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, s));
         } else {
-          const uint32_t n0_ = __shfl_xor_sync(0xffffffffu, m0, 1), n1_ = __shfl_xor_sync(0xffffffffu, m1, 1);
-          const uint32_t both = max(m0, m1);
-          m0 = p.turned ? max(m0, n0_) : both;
-          m1 = p.turned ? max(m1, n1_) : both;
+          const uint32_t o0 = __shfl_xor_sync(0xffffffffu, m0, 1), o1 = __shfl_xor_sync(0xffffffffu, m1, 1);
+          m0 = p.turned ? max(m0, o0) : both;
+          m1 = p.turned ? max(m1, o1) : both;
         }
       }
       if (u >= units) continue;
-      if (p.slot < a.n_q) {
+      if (p.slot < n_q) {
         if (!pl.owned || pl.pos < 0) continue;
         uint8_t* q = a.q_out + ((size_t)(n0 + p.row) * a.o_row + (size_t)p.slot * a.o_head) * 2;
         *reinterpret_cast<uint4*>(q + p.c0 * 2) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -166,31 +176,41 @@ __global__ void __launch_bounds__(kThreads) paged_rope_kernel(const PagedRopeArg
         continue;
       }
       if (!pl.there) continue;
-      const int side = p.slot >= a.n_q + m.n_kv, head = p.slot - a.n_q - side * m.n_kv;
+      const int side = p.slot >= n_q + m.n_kv, head = p.slot - n_q - side * m.n_kv;
       const size_t row = ((size_t)head << m.batch.page_shift) + pl.at;
       uint8_t* page = m.pages[side] + (size_t)pl.page * m.page_stride[side] * (E4M3 || E2M1 ? 1 : 2);
       if (E2M1) {
         uint8_t* rec = page + row * e2m1_record(HD);
-        const bool finite0 = m0 < 0x7F800000u, finite1 = m1 < 0x7F800000u;
-        auto scale = [](uint32_t top, bool finite) {
-          const float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 6.0f)));
-          return !finite ? __uint_as_float(0x7FC00000u) : s == 0.0f ? 1.0f : s;
+        auto scale = [](uint32_t top) {
+          // top / 6 as quotients() makes it
+          const float x = __uint_as_float(top), y = 1.0f / 6.0f, q = x * y;
+          const float by6 = x < 0x1p-100f ? __fdiv_rn(x, 6.0f) : fmaf(fmaf(q, -6.0f, x), y, q);
+          const float s = __bfloat162float(__float2bfloat16_rn(by6));
+          return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : s == 0.0f ? 1.0f : s;
         };
-        const float s0 = scale(m0, finite0), s1 = scale(m1, finite1);
-        const float y0 = __fdiv_rn(1.0f, s0), y1 = __fdiv_rn(1.0f, s1);
-        uint32_t c0 = 0, c1 = 0;
+        auto codes = [&](const float2* x, float s) {
+          const float y = __frcp_rn(s);
+          uint32_t c = 0;
+          if (quotients_small(s)) {
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+              const float2 q = quotients_slow(e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3], s);
+              c |= e2m1x2(make_float2(q.x + 0.0f, q.y + 0.0f)) << (8 * e);  // -0 becomes 0, as below
+            }
+            return c;
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // (a zero keeps its sign, which quotients() loses)
-          auto code = [](float2 x, float s, float y) {
-            const float2 q = quotients_small(s) ? quotients_slow(x, s) : quotients(x, s, y);
-            return e2m1x2(make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y)));
-          };
-          c0 |= code(f[e], s0, y0) << (8 * e);
-          c1 |= code(f[4 + e], s1, y1) << (8 * e);
+          for (int e = 0; e < 4; ++e) c |= e2m1x2(quotients(x[e], s, y)) << (8 * e);
+          return c;
+        };
+        const float s0 = scale(m0), s1 = ROPE ? scale(m1) : s0;
+        const uint32_t c0 = codes(f, s0), c1 = codes(f + 4, s1);
+        if (ROPE) {
+          *reinterpret_cast<uint32_t*>(rec + p.c0 / 2) = c0;
+          *reinterpret_cast<uint32_t*>(rec + p.c1 / 2) = c1;
+        } else {
+          *reinterpret_cast<uint2*>(rec + p.c0 / 2) = make_uint2(c0, c1);
         }
-        *reinterpret_cast<uint32_t*>(rec + p.c0 / 2) = c0;
-        *reinterpret_cast<uint32_t*>(rec + p.c1 / 2) = c1;
         // a block's scale by the lane with its first run
         uint16_t* scales = reinterpret_cast<uint16_t*>(rec + HD / 2);
         if (p.c0 % 16 == 0) scales[p.c0 / 16] = (uint16_t)(__float_as_uint(s0) >> 16);
@@ -216,28 +236,33 @@ __global__ void __launch_bounds__(kThreads) paged_rope_kernel(const PagedRopeArg
   }
 }
 
-template <int HD, int FORMAT, bool BF16>
+template <int HD, int FORMAT, bool BF16, bool ROPE>
 int launch_rope(const PagedRopeArgs& a, cudaStream_t s) {
   const long long each = a.m.batch.rows / 608;  // 4 blocks for each of 152 SMs come first
-  const int rows = (int)min((long long)kMaxRows, max(1ll, each));
+  const int per_row = a.n_q + 2 * a.m.n_kv;
+  const int most = min(kMaxRows, max(1, kMostUnits / per_row));
+  const int rows = (int)min((long long)most, max(1ll, each));
   const int grid = max(1, ceil_div(a.m.batch.rows, rows));
-  return launch_pdl(paged_rope_kernel<HD, FORMAT, BF16>, dim3(grid), dim3(kThreads), 0, s, a, rows);
+  // u / per_row = u * magic / 2^32 for u < rows * per_row: 0 for a single row, else u and
+  // per_row are at most kMostUnits
+  const uint32_t magic = rows == 1 ? 0u : (uint32_t)(((1ull << 32) + per_row - 1) / per_row);
+  return launch_pdl(paged_rope_kernel<HD, FORMAT, BF16, ROPE>, dim3(grid), dim3(kThreads), 0, s, a, rows, magic);
 }
 
-template <int HD>
-int dispatch(const PagedRopeArgs& a, int format, int type, cudaStream_t s) {
-  const bool bf = type == DFLASH_TYPE_BF16;
-  if (format == DFLASH_CACHE_E2M1)
-    return bf ? launch_rope<HD, DFLASH_CACHE_E2M1, true>(a, s) : launch_rope<HD, DFLASH_CACHE_E2M1, false>(a, s);
-  if (format == DFLASH_CACHE_E4M3)
-    return bf ? launch_rope<HD, DFLASH_CACHE_E4M3, true>(a, s) : launch_rope<HD, DFLASH_CACHE_E4M3, false>(a, s);
-  return bf ? launch_rope<HD, DFLASH_CACHE_BF16, true>(a, s) : launch_rope<HD, DFLASH_CACHE_F16, false>(a, s);
+template <int HD, bool BF16>
+int dispatch(const PagedRopeArgs& a, int format, cudaStream_t s) {
+  if (!a.rope.rotary_dim) return launch_rope<HD, DFLASH_CACHE_E2M1, BF16, false>(a, s);
+  if (format == DFLASH_CACHE_E2M1) return launch_rope<HD, DFLASH_CACHE_E2M1, BF16, true>(a, s);
+  if (format == DFLASH_CACHE_E4M3) return launch_rope<HD, DFLASH_CACHE_E4M3, BF16, true>(a, s);
+  return launch_rope<HD, BF16 ? DFLASH_CACHE_BF16 : DFLASH_CACHE_F16, BF16, true>(a, s);
 }
 
 }  // namespace
 
 int launch_paged_append_rope(const PagedRopeArgs& a, int head_dim, int format, int type, cudaStream_t s) {
-  return head_dim == 128 ? dispatch<128>(a, format, type, s) : dispatch<64>(a, format, type, s);
+  const bool bf = type == DFLASH_TYPE_BF16;
+  if (head_dim == 128) return bf ? dispatch<128, true>(a, format, s) : dispatch<128, false>(a, format, s);
+  return bf ? dispatch<64, true>(a, format, s) : dispatch<64, false>(a, format, s);
 }
 
 }  // namespace dfl

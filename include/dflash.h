@@ -390,7 +390,7 @@ int dflash_quantize_e4m3(const void* w, int rows, int cols, void* codes, float* 
  *              that is 0; NaN for a block that holds a NaN or an infinity, which
  *              then reads back as NaN), code = value / scale (likewise) rounded to
  *              nearest, ties to even, at most 6 in magnitude, the sign kept on
- *              values that become 0.
+ *              values that round to 0 (but -0 becomes 0).
  *              A row is one record of head_dim * 5 / 8 bytes: head_dim / 2 bytes
  *              of codes (value 2i in the lower, 2i + 1 in the upper half of byte
  *              i), then its head_dim / 16 scales.

@@ -60,7 +60,7 @@ def pack(x):
     s = scales(x)
     with np.errstate(invalid="ignore", over="ignore"):
         y = x.reshape(s.shape + (BLOCK,)) / s.astype(np.float32)[..., None]
-    c = round_code(y).reshape(x.shape)
+    c = round_code(np.where(y == 0, 0.0, y)).reshape(x.shape)       # -0 becomes 0
     bits = bf16_bits(s.astype(np.float32))
     two = np.stack([bits & 0xFF, bits >> 8], -1).astype(np.uint8).reshape(x.shape[:-1] + (-1,))
     return np.concatenate([c[..., 0::2] | (c[..., 1::2] << 4), two], -1)

@@ -76,7 +76,7 @@ def pack_fast(x):
     c = np.zeros(y.shape, dtype=np.uint8)
     for i, m in enumerate(mids):
         c += (y > m) if i % 2 == 0 else (y >= m)
-    c = c.reshape(x.shape) | (np.signbit(x).astype(np.uint8) << 3)
+    c = c.reshape(x.shape) | ((x < 0).astype(np.uint8) << 3)
     bits = e2m1.bf16_bits(s.astype(np.float32))
     two = np.stack([bits & 0xFF, bits >> 8], -1).astype(np.uint8).reshape(x.shape[:-1] + (-1,))
     return np.concatenate([c[..., 0::2] | (c[..., 1::2] << 4), two], -1)
