@@ -503,9 +503,10 @@ def paged_cache(k_pages, v_pages, k_scale=None, v_scale=None, format=None):
 
 
 def _rows(name, t, index):
-    if t.dim() != 3 or t.get_device() != index or (t.stride(2) != 1 and t.numel()):
+    st = t.stride()
+    if len(st) != 3 or t.get_device() != index or (st[2] != 1 and t.numel()):
         raise ValueError(f"{name}: expected [rows, heads, head_dim] on cuda:{index} with head_dim contiguous")
-    return _PACK_ROWS(t.data_ptr(), t.stride(0), t.stride(1))
+    return _PACK_ROWS(t.data_ptr(), st[0], st[1])
 
 
 def _batch(row_start, kv_len, page_table, rows, index):
@@ -574,27 +575,27 @@ def dflash_paged_append_rope(cache, k, v, row_start, kv_len, page_table, rope, w
     """dflash_paged_append with keys (and queries, q to q_out [rows, n_q_heads,
     head_dim]; q_out may be q) rotated; positions int64 [rows] or None: the
     cache's."""
-    index = cache.index
-    if k.shape != v.shape or k.dtype is not v.dtype or k.shape[1:] != cache._rows:
+    index, shape, dtype = cache.index, k.shape, k.dtype
+    if v.shape != shape or v.dtype is not dtype or shape[1:] != cache._rows:
         raise ValueError("k and v: expected [rows, %d, %d] of one type" % cache._rows)
-    if k.dtype is not torch.bfloat16 and k.dtype is not torch.float16:
-        raise ValueError(f"no rows of {k.dtype}")
-    n, n_q = k.shape[0], 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
-    if q is not None:
-        n_q = q.shape[1] if q.dim() == 3 else 0
-        if q.shape != (n, n_q, cache._rows[1]) or not n_q or q_out.shape != q.shape or q.dtype is not k.dtype or \
-                q_out.dtype is not k.dtype:
-            raise ValueError(f"q and q_out: expected [{n}, n_q_heads, {cache._rows[1]}] of the type of k")
-    if not isinstance(rope, dflash_rope):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"no rows of {dtype}")
+    if rope.__class__ is not dflash_rope:
         raise ValueError("rope: expected what dflash_rope_init returns")
+    n, n_q, q_rows, out_rows = shape[0], 0, None, None
+    if q is not None and q_out is not None:
+        sq = q.shape
+        if len(sq) != 3 or sq[0] != n or sq[2] != shape[2] or not sq[1] or q_out.shape != sq or q.dtype is not dtype or \
+                q_out.dtype is not dtype:
+            raise ValueError(f"q and q_out: expected [{n}, n_q_heads, {shape[2]}] of the type of k")
+        n_q, q_rows, out_rows = sq[1], _rows("q", q, index), _rows("q_out", q_out, index)
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out come together")
     stream = _current(index, stream)
     code = lib().dflash_paged_append_rope(
-        cache._bytes, _batch(row_start, kv_len, page_table, n, index), _TYPES[k.dtype], _rows("k", k, index),
-        _rows("v", v, index), n_q, _rows("q", q, index) if n_q else None, _rows("q_out", q_out, index) if n_q else None,
-        ctypes.addressof(rope), _fit("positions", positions, torch.int64, (n,), index) or None, _workspace(ws, index),
-        ws.numel(), stream)
+        cache._bytes, _batch(row_start, kv_len, page_table, n, index), _TYPES[dtype], _rows("k", k, index),
+        _rows("v", v, index), n_q, q_rows, out_rows, ctypes.addressof(rope),
+        _fit("positions", positions, torch.int64, (n,), index) or None, _workspace(ws, index), ws.numel(), stream)
     if code:
         raise DflashError(code, "dflash_paged_append_rope")
 
