@@ -290,6 +290,8 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_b
   if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads || n_q_heads > 65535) return DFLASH_ERR_SHAPE;
   const int group = n_q_heads / cache->n_kv_heads;
   if (max_rows < 0 || max_rows > batch->rows || (long long)max_rows * group > (1ll << 30)) return DFLASH_ERR_SHAPE;
+  const bool e2m1 = cache->format == DFLASH_CACHE_E2M1;
+  if (e2m1 && ((long long)max_rows * group + 127) / 128 * batch->B > (1ll << 30)) return DFLASH_ERR_SHAPE;
   // key tiles of an item, over all KV heads, are counted in 32 bits
   if (((long long)batch->max_pages * cache->page_size / 128 + 16) * cache->n_kv_heads > 0x7FFFFFFFll)
     return DFLASH_ERR_SHAPE;
@@ -307,7 +309,6 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_b
     if (!same_cache(maps.cache, *cache)) return DFLASH_ERR_ARG;
   }
   if (max_rows == 0) return DFLASH_OK;
-  const bool e2m1 = cache->format == DFLASH_CACHE_E2M1;
   if (!cache->maps && !e2m1 && (rc = encode_paged_maps(*cache, &maps.k, &maps.v))) return rc;
   PagedAttnArgs a;
   a.batch = batch_args(batch, cache);

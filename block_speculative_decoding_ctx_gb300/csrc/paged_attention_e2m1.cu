@@ -8,30 +8,32 @@
 // Everything is transposed: keys lie on the lanes of tensor memory and query rows
 // on its columns,
 //   S^T [128 keys, N rows] = K Q^T,   O^T [128 values, N rows] += V^T P^T,
-// N the item's rows up to a multiple of 16.  So a block of 8 positions or a single
-// token costs the tensor cores and the softmax what its rows are, not 128; a
-// thread of the softmax has one key, whose scales are factors of its own; and the
-// widened K goes from the codes straight to tensor memory as an operand, a row to
-// a lane, without a trip through shared memory.
+// N the item's rows up to a multiple of 16 (above 64: 96 or 128).  So a block of 8
+// positions or a single token costs the softmax what its rows are, not 128, and all
+// its threads have keys; and the widened K goes from the codes straight to tensor
+// memory as an operand, a row to a lane, without a trip through shared memory, which
+// is the busiest part here.
 //
 // Values.  A code times its scale has 10 significant bits.  A row's scales are
 // brought to [2^12, 2^13) by a power of two of the row's largest, so that the
-// products are fp16 values, exact but for those 2^-36 of the largest scale; the
-// power comes back in float32, for K as a factor of the scores, for V added to
-// the exponent of the weights.  Queries become fp16 times a power of two per row.
+// products are fp16 values, exact but for 2^-36 of the largest scale; the power comes
+// back in float32, for K as a factor of the scores, for V added to the exponent of
+// the weights.  Queries become fp16 times a power of two per row.
 //   What a row's reference follows is the largest of weight times the power of its
 // value row, so that the tail behind a dominant key with small values keeps its
-// places: weights are fp16 up to 2^15, at least 2^11 for the largest when the
-// reference is set, and end at 2^-24.
+// places: weights are fp16 up to 2^15, 2^4 at least for the largest when a reference
+// is set, and end at 2^-24, so their last place is 2^-28 of the largest.  (References
+// at 2^11 / 2^8 / 2^4 / 2^0: blocks of 8 155 / 150 / 145 / 141 us, prompt chunk 1,673 /
+// 1,571 / 1,487 / 1,434; the lower, the rarer they grow, and the more of a long tail is
+// rounded away: 2^-28 of 131,072 keys is 2^-11 of the largest, 2^-24 would be 2^-7.)
 //
 // Roles (640 threads, a persistent CTA on its part of the line, see paged_line.cuh;
 // items of at most 128 rows):
-//   warps 0, 3   page table and bulk copies of K and of V: a page's records are one run
-//                of bytes
-//   warp 1       issues the products: of tile t, S(t); then O for tile t - 1
+//   warps 0, 3   page table and bulk copies of K and of V: a page's records are one
+//                run of bytes
+//   warp 1       issues the products, whatever is ready
 //   warp 2       describes the CTA's segments of items, ahead of the others
-//   warps 4-11   softmax: either warpgroup half of the rows (columns), a key per
-//                thread
+//   warps 4-11   softmax: a thread has two columns of every group of 8, of four keys
 //   warps 12-15  widen the codes of K into tensor memory, a key per thread
 //   warps 16-19  widen those of V into shared memory (M-major operand)
 // Modes.  An item of more than 64 rows: the warpgroups share each tile's columns, S
@@ -39,6 +41,20 @@
 // its columns, each with an O of its own, joined at the end, and S has four buffers
 // of 64 columns, so that a warpgroup's next scores are made while it weighs.
 // Tensor memory: S, 256 columns; O, 128; K0 | K1, head_dim / 2 each.
+//
+// What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16):
+//   32 requests, blocks of 8, context 8,192: 142 us for 341 MB, 2.4 TB/s, 0.36 of the
+//     measured copy (a bf16 cache takes 172, E4M3 177).  The tensor cores are at work
+//     for 0.65 of the time, waiting for operands most of it: a product of 48 columns
+//     (16 keys or values deep) alone takes 49 clocks where K comes from tensor memory
+//     and 72 where V comes from shared memory, nearly twice as long beside the widening
+//     and the weights, which keep shared memory busy; issue slots 51 %;
+//   16 blocks of 16, context 512 to 131,072: 140 us, alike (E4M3 196);
+//   prompt chunk, 2 x 2,048 rows, context up to 16,384: 1,485 us, 0.70 PFLOP/s (bf16
+//     909, E4M3 1,622).  Tensor cores 28 % of their rate and busy throughout, shared
+//     memory 50 %, issue slots 53 %; without references that grow it would be 1,208:
+//     each time one does the tile is held up for about 2,000 clocks;
+//   one token, context 1,000: latency, 12 us.
 //
 // All waits are bounded.  When one gives up, the softmax warps run on to the end of
 // their segment without waiting (their barriers stay matched, results are void,
@@ -51,8 +67,9 @@ namespace {
 using namespace line;
 
 constexpr int kThreads = 640;
-// Registers: of the softmax warpgroups, of the others, and what a thread is launched with.
-constexpr int kRegsSoftmax = 144, kRegsOthers = 64, kRegsLaunch = 96;
+// Registers: of the softmax warpgroups, of the others, and what a thread is launched with
+// (softmax 136 / 144 / 152 / 160: prompt chunk 1,554 / 1,513 / 1,485 / 1,544 us).
+constexpr int kRegsSoftmax = 152, kRegsOthers = 56, kRegsLaunch = 96;
 static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOthers <= kThreads * kRegsLaunch, "the block's registers");
 constexpr int kRows = 128;     // of an item at most
 constexpr int kMaxSlots = 8;
@@ -66,8 +83,7 @@ constexpr float kUnseen = 0x1p100f;  // minus the reference of a column that has
 // tile's largest.
 constexpr float kMaxWeight = 15.0f, kFreshWeight = 4.0f;
 // A weight that makes its column's reference grow once some other column's has to: all
-// that are about to do so at once (prompt chunk with 15 / 13 / 10 / 6: 1,671 / 1,642 /
-// 1,608 / 1,581 us, blocks alike).
+// that are about to do so at once (with 15 prompt chunk 1,567 us for 1,487, blocks alike).
 constexpr float kRenewWeight = 6.0f;
 // Exponents (biased) that rows of K and V are scaled by: so that the factors stay
 // normal numbers.  Of V 2^-64 at least: the sums l, in which that power is taken
@@ -169,6 +185,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ void st_shared_x4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_shared(uint32_t at, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -233,8 +255,8 @@ __device__ __forceinline__ int largest_exponent(const Record<HD>& r, int least) 
 template <int HD>
 __device__ __forceinline__ uint32_t scale_pair(const Record<HD>& r, int i, float f) {
   const uint32_t w = r.scale[i / 2];
-  const float s = __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16) * f;
-  return pack16<false>(s, s);
+  const uint32_t both = pack16<false>(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+  return __byte_perm(both, 0u, i & 1 ? 0x3232 : 0x1010);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -266,9 +288,11 @@ __device__ __forceinline__ void wait_fragments(float (&v)[2][4]) {
 // Some column's weight would pass 2^15, or it sees its first key (its reference was
 // kUnseen): its reference becomes the tile's largest, what l and O shrink by is in fac,
 // and O shrinks.  top: of the thread's columns, their largest over its keys.  By all
-// threads of a warpgroup.  Only those that hold such a weight tell it: exchanging the
-// columns' largest values between lanes took 2,000 clocks, shared memory being the
-// busiest part of the machine here.
+// threads of a warpgroup.  Only those that hold such a weight tell it, by a maximum
+// under a predicate: exchanging the columns' largest values between lanes takes 2,000
+// clocks beside everything else that wants shared memory, a branch for each column 800.
+// (Without the second barrier, every warp working references and factors out from the
+// maxima for itself: prompt chunk 1,714 us for 1,667.)
 template <int NCH>
 __device__ __forceinline__ void grow_references(const KernelArgs& k, Ctrl* c, const Stream& st, const float2 (&top)[NCH],
                                                 const float2 (&nb)[NCH], uint32_t tO, uint32_t T, bool held) {
@@ -332,8 +356,9 @@ __device__ __forceinline__ void grow_references(const KernelArgs& k, Ctrl* c, co
 // the sums of its l in red.  A thread has, of every group, two columns of four keys
 // (load_fragments), so that the columns' factors and references stay in its registers:
 // with a key to a thread and all columns, each of them read from shared memory for each
-// tile, those reads alone held shared memory up for a third of the tile's time.
-// Unrolled over the groups without a branch, so that their chains overlap.
+// tile, blocks of 8 took 246 us and 219 so.  Unrolled over the groups without a branch,
+// so that their chains overlap (369 us with one for each group, 252 without).  Weights
+// go out word by word: as fragments (stmatrix) prompt chunk 1,542 us for 1,513.
 template <int HD, int NCH>
 __device__ __forceinline__ void softmax_tiles(const KernelArgs& k, Ctrl* c, const Seg& s, const Stream& st, uint8_t* p_s,
                                               uint32_t& T) {
@@ -421,18 +446,18 @@ __device__ __forceinline__ void softmax_tiles(const KernelArgs& k, Ctrl* c, cons
     // tile its scores came after the last reader of this buffer.)
     if (alt && T >= 2) (void)warp_wait_on(&c->pv_done[i2], ((T - 2) >> 1) & 1u, stop, a.status);
     ++done;
-    uint8_t* const p_at = p_s + i2 * k.spans * Cfg<HD>::kSpan + row * 128 + pair * 4;
+    const uint32_t p_at = smem_u32(p_s) + i2 * k.spans * Cfg<HD>::kSpan + row * 128 + pair * 4;
 #pragma unroll
     for (int g = 0; g < NCH; ++g) {
       const int ch = st.col0 / 8 + g;
-      uint8_t* const to = p_at + (ch >> 3) * Cfg<HD>::kSpan + (((ch ^ row) & 7) << 4);
+      const uint32_t to = p_at + (ch >> 3) * Cfg<HD>::kSpan + (((ch ^ row) & 7) << 4);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const float* const y = &z[u >> 1][g][(u & 1) * 2];
         const float2 x = add2(make_float2(y[0], y[1]), nb[g]);
         const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
         l[g] = fma2(p, make_float2(inv[u], inv[u]), l[g]);
-        *reinterpret_cast<uint32_t*>(to + u * 1024) = pack16<false>(p.x, p.y);
+        st_shared(to + u * 1024, pack16<false>(p.x, p.y));
       }
     }
     fence_proxy_async_smem();
@@ -652,8 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
           __syncwarp();
         };
         // Whatever is ready goes next: in a fixed order either waits for what the other's
-        // operands wait for (blocks of 8: 219 us against 178, when that was tried).
-        // Scores before values: prompt chunk 1,558 us, 1,583 the other way.
+        // operands wait for (prompt chunk 1,927 us for 1,581, when that was tried).
         const int buffers = alt ? 4 : 2;  // of S
         int ns = 0, nv = 0;               // scores and values issued
         unsigned long long since = 0;
@@ -741,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
           const float f = __uint_as_float((uint32_t)(254 + kScaleExp - largest_exponent<HD>(x, kLeastV)) << 23);
           ok = warp_wait_on(&c->pv_done[i], before, stop, a.status);
           if (!ok) break;
-          uint8_t* const to = wide_s + i * C::kWide + r * 128;
+          // (128-byte swizzle: chunk c of row r lies at c ^ r % 8)
+          const uint32_t to = smem_u32(wide_s + i * C::kWide) + r * 128 + ((r & 7) << 4);
 #pragma unroll
           for (int b = 0; b < HD / 16; ++b) {
             const uint32_t s = scale_pair<HD>(x, b, f);
@@ -750,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
               uint32_t w[4];
               e2m1x8_to_f16x2(x.code[2 * b + h], w);
               const int ch = 2 * b + h;
-              *reinterpret_cast<uint4*>(to + (ch >> 3) * C::kSpan + (((ch ^ r) & 7) << 4)) =
-                  make_uint4(hmul2(w[0], s), hmul2(w[1], s), hmul2(w[2], s), hmul2(w[3], s));
+              st_shared_x4((to ^ ((ch & 7) << 4)) + (ch >> 3) * C::kSpan, hmul2(w[0], s), hmul2(w[1], s), hmul2(w[2], s),
+                           hmul2(w[3], s));
             }
           }
           fence_proxy_async_smem();
@@ -986,12 +1011,12 @@ int launch(const dflash_paged_cache& cache, const PagedAttnArgs& a, int type, vo
   k.rec = l.rec;
   const long long most = (long long)a.max_rows * a.group;
   const long long rts = (most + kRows - 1) / kRows;
-  if (rts * a.batch.B > 1 << 30) return DFLASH_ERR_SHAPE;
   k.rts = (int)rts;
   k.part_rows = part_rows(a.group, a.max_rows);
   // What an item costs beside its tiles, for the cut of the line (queries, their factors,
-  // the first references, the end): of 1 / 4 / 8 / 16 tiles ragged blocks take 223 / 172 /
-  // 147 / 149 us, blocks of 8 149 / 149 / 147 / 154, prompt chunks alike.
+  // the first references, the end): of 4 / 8 tiles ragged blocks take 170 / 145 us,
+  // with 1 / 16, when that was tried, 223 / 149; blocks of 8 with 16 154 for 147; prompt
+  // chunks alike.
   k.seg_cost = 8;
   k.k_pages = static_cast<const uint8_t*>(cache.k_pages);
   k.v_pages = static_cast<const uint8_t*>(cache.v_pages);

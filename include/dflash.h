@@ -59,7 +59,7 @@
  * host, and may be captured into a CUDA graph.
  *
  * Workspace.  draft_block, ctx_append, probs, verify and the target-side calls
- * (paged_append, paged_gather, paged_attention, logits_adjust) take a caller-owned
+ * (paged_append, paged_append_rope, paged_gather, paged_attention, logits_adjust) take a caller-owned
  * device workspace of at least the size the matching *_workspace_bytes
  * function returns, 256-byte aligned, ZERO-FILLED BEFORE ITS FIRST USE.  The
  * library leaves the workspace's counter region zeroed after every call, so
@@ -552,19 +552,20 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  *             is launched
  *   scale     finite and > 0;  causal 0 or 1;  window >= 0, 0 = none
  * n_q_heads is a multiple of n_kv_heads, at most 65,535.  With R = max_rows *
- * n_q_heads / n_kv_heads, R and B * ceil(R / 256) are at most 2^30, and
+ * n_q_heads / n_kv_heads, R and B * ceil(R / 256) (E2M1: / 128) are at most 2^30, and
  * (max_pages * page_size / 128 + 16) * n_kv_heads is below 2^31.  Cache rows that no row of a request
  * sees (behind its length, before its window, in pages it does not list) may
  * hold anything, NaN included.  A visible row that is not finite makes the
  * outputs of that request and KV head undefined, no other's.
  * Precision: statistics and sums are float32.  Weights are rounded to bf16 over a
- * BF16 cache, to fp16 over the others, where one that is below 2^-25 of the row's
+ * BF16 cache, to fp16 over the others, where (F16, E4M3) one that is below 2^-25 of the row's
  * largest (E4M3: times the value scales) keeps fewer bits, the last at 2^-35.
  * bf16 values of any finite size do; what adds less than 2^-96 to an output (2^-64
  * for value scales of E4M3 and E2M1) may be lost.  Over E2M1 the queries become
  * fp16 times a power of two per row (2^-39 of a row's largest may be lost), keys
- * and values fp16 times one per row (2^-36 of a row's largest scale); the largest
- * weight that is followed is that of weight times value scale, as over E4M3. */
+ * and values fp16 times one per row (2^-34 of a row's largest scale); a weight below
+ * 2^-18 of the row's largest, times the power of two of its value row, keeps fewer
+ * bits, the last at 2^-28.  Scores beyond float32's range are undefined. */
 size_t dflash_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim,
                                               int max_rows);
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_batch* batch,

@@ -54,6 +54,12 @@ def test_attention_refusals_of_a_cache_in_4_bits(L):
         assert call(c=cache4(**bad)) == code, bad
     assert call(n=need - 1) == -7 and call(n_q=9) == -2 and call(t=2) == -1
     assert call(max_rows=0) == 0
+    # B * ceil(R / 128) items: 2^30 of them and no more
+    many = dict(rows=1 << 30, max_pages=1, table_stride=1)
+    x = rows(row_stride=1024)
+    for B, code in ((128, -7), (129, -2)):
+        assert L.dflash_paged_attention(ref(cache4()), ref(batch(B=B, **many)), 0, 2, ref(x), ref(x), None, 1 << 30, 0.1, 1, 0, None,
+                                        0, None) == code
     maps = dfl.dflash_paged_maps()
     assert L.dflash_paged_cache_maps(ref(cache4()), ref(maps)) == 0
     assert call(c=cache4(maps=ctypes.addressof(maps)), max_rows=0) == 0
