@@ -43,15 +43,16 @@
 // Tensor memory: S, 256 columns; O, 128; K0 | K1, head_dim / 2 each.
 //
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16):
-//   32 requests, blocks of 8, context 8,192: 142 us for 341 MB, 2.4 TB/s, 0.36 of the
-//     measured copy (a bf16 cache takes 172, E4M3 177).  The tensor cores are at work
+//   32 requests, blocks of 8, context 8,192: 138 us for 341 MB, 2.5 TB/s, 0.37 of the
+//     measured copy (with L2 flushed 145, a bf16 cache 193, E4M3 182).  The tensor cores are at work
 //     for 0.65 of the time, waiting for operands most of it: a product of 48 columns
 //     (16 keys or values deep) alone takes 49 clocks where K comes from tensor memory
 //     and 72 where V comes from shared memory, nearly twice as long beside the widening
 //     and the weights, which keep shared memory busy; issue slots 51 %;
-//   16 blocks of 16, context 512 to 131,072: 140 us, alike (E4M3 196);
-//   prompt chunk, 2 x 2,048 rows, context up to 16,384: 1,485 us, 0.70 PFLOP/s (bf16
-//     909, E4M3 1,622).  Tensor cores 28 % of their rate and busy throughout, shared
+//   16 blocks of 16, context 512 to 131,072: 139 us, alike (flushed 143, bf16 150,
+//     E4M3 158);
+//   prompt chunk, 2 x 2,048 rows, context up to 16,384: 1,489 us, 0.70 PFLOP/s (bf16
+//     748, E4M3 1,266).  Tensor cores 28 % of their rate and busy throughout, shared
 //     memory 50 %, issue slots 53 %; without references that grow it would be 1,208:
 //     each time one does the tile is held up for about 2,000 clocks;
 //   one token, context 1,000: latency, 12 us.
