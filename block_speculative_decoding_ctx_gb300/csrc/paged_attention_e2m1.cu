@@ -60,7 +60,7 @@
 // All waits are bounded.  When one gives up, the softmax warps run on to the end of
 // their segment without waiting (their barriers stay matched, results are void,
 // the status word says so) and the CTA ends as usual.
-#include "paged_line.cuh"
+#include "paged_e2m1.cuh"
 
 namespace dfl {
 namespace {
@@ -91,11 +91,7 @@ constexpr float kRenewWeight = 6.0f;
 // off the weights again, stay finite.
 constexpr int kLeastK = 13, kLeastV = 127 - 64, kMost = 253;
 
-struct KernelArgs : LineArgs {
-  const uint8_t *k_pages, *v_pages;
-  long long k_stride, v_stride;
-  int bf16;
-  int slots;
+struct KernelArgs : E2m1Args {
   int spans;  // of 64 rows (columns of P, rows of Q)
 };
 
@@ -148,21 +144,6 @@ __device__ __forceinline__ uint32_t s_col(bool alt, uint32_t tile) {
   return alt ? (tile & 3u) * kAltRows : (tile & 1u) * kRows;
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ bool any_of(int id, int threads, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((uint32_t)p)
-      : "memory");
-  return r != 0;
-}
 // Eight columns, waited for.
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
@@ -181,26 +162,9 @@ __device__ __forceinline__ void max_shared_if(bool p, int* at, int v) {
 // A float's bits as an integer of the same order, and back; what no score has.
 __device__ __forceinline__ int ordered(int bits) { return bits ^ ((bits >> 31) & 0x7FFFFFFF); }
 constexpr int kNone = (int)0x80000000;
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void st_shared_x4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 __device__ __forceinline__ void st_shared(uint32_t at, uint32_t a) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // A record: codes and scales as words.
 template <int HD>
 struct Record {
@@ -856,22 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
           w = __ldg(reinterpret_cast<const uint4*>(
               a.q + ((size_t)(it.s0 + tok) * a.q_row + (size_t)(s.head * a.group + g) * a.q_head + ch * 8) * 2));
         }
-        uint32_t v[4] = {w.x, w.y, w.z, w.w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
-#pragma unroll
-        for (int o = kCh / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m = max(m & 0xFFFFu, m >> 16);
-        const float top = k.bf16 ? unpack16<true>(m).x : unpack16<false>(m).x;
-        const int e = max((int)(__float_as_uint(top) >> 23), 15);  // a row that is not finite becomes NaN
-        const float f = e < 255 ? __uint_as_float((uint32_t)(268 - e) << 23) : __uint_as_float(0x7FC00000u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 y = k.bf16 ? unpack16<true>(v[i]) : unpack16<false>(v[i]);
-          v[i] = pack16<false>(y.x * f, y.y * f);
-        }
-        *reinterpret_cast<uint4*>(q_s + (ch >> 3) * q_span + swz(r, (ch & 7) * 8)) = make_uint4(v[0], v[1], v[2], v[3]);
+        int e;
+        w = widen_q<kCh>(w, k.bf16, &e);
+        *reinterpret_cast<uint4*>(q_s + (ch >> 3) * q_span + swz(r, (ch & 7) * 8)) = w;
         if (ch == 0) {
           // columns without a row: weights of zero
           const bool real = r < it.rows;
@@ -879,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
             const int own = alt ? r : r - w * mine;
             if (own < 0 || own >= mine) continue;
             float* cs = reinterpret_cast<float*>(&c->col[w][own >> 1]) + (own & 1);
-            cs[0] = real ? a.scale_log2 * __uint_as_float((uint32_t)(min(e, 254) - 14) << 23) : 0.0f;
+            cs[0] = real ? q_factor(e, a.scale_log2) : 0.0f;
             cs[2] = real ? kUnseen : -1000.0f;
           }
           const int packed = it.row0 + (real ? r : 0), tok = packed / a.group, g = packed - tok * a.group;
@@ -989,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
 // -------------------------------------------------------------------- host
 
 template <int HD>
-int launch(const dflash_paged_cache& cache, const PagedAttnArgs& a, int type, void* ws, cudaStream_t s) {
+int launch(KernelArgs& k, cudaStream_t s) {
   using C = Cfg<HD>;
   auto kern = paged_attention_e2m1_kernel<HD>;
   int dev = 0, sms = 0;
@@ -1004,43 +955,42 @@ int launch(const dflash_paged_cache& cache, const PagedAttnArgs& a, int type, vo
     if (attr.numRegs != kRegsLaunch) return DFLASH_ERR_UNSUPPORTED;  // the softmax's share would never come free
     if (dev < 64) known[dev].store(sms);
   }
-  KernelArgs k;
-  k.a = a;
-  const Layout l = layout(ws, a.group, HD, a.max_rows);
-  k.part = l.part;
-  k.ml = l.ml;
-  k.rec = l.rec;
-  const long long most = (long long)a.max_rows * a.group;
-  const long long rts = (most + kRows - 1) / kRows;
-  k.rts = (int)rts;
-  k.part_rows = part_rows(a.group, a.max_rows);
+  const int most = k.a.max_rows * k.a.group;  // at most kRows
+  k.rts = 1;
   // What an item costs beside its tiles, for the cut of the line (queries, their factors,
   // the first references, the end): of 4 / 8 tiles ragged blocks take 170 / 145 us,
-  // with 1 / 16, when that was tried, 223 / 149; blocks of 8 with 16 154 for 147; prompt
-  // chunks alike.
+  // with 1 / 16, when that was tried, 223 / 149; blocks of 8 with 16 154 for 147.
   k.seg_cost = 8;
-  k.k_pages = static_cast<const uint8_t*>(cache.k_pages);
-  k.v_pages = static_cast<const uint8_t*>(cache.v_pages);
-  k.k_stride = cache.k_page_stride;
-  k.v_stride = cache.v_page_stride;
-  k.bf16 = type == DFLASH_TYPE_BF16;
   k.spans = most > 64 ? 2 : 1;
   const int fixed = C::kWideAll + 2 * k.spans * C::kSpan + k.spans * 64 * 128 * (HD / 64) + kCtrlBytes;
   k.slots = min(kMaxSlots, (kSmem - fixed) / C::kSlot);
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   int rc;
   if ((rc = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmem, s, k))) return rc;
-  const int y = (int)min((long long)kJoinBlocks, most);
+  const int y = min(kJoinBlocks, most);
   const LineArgs& line = k;
-  return type == DFLASH_TYPE_BF16 ? launch_pdl(paged_join_kernel<HD, true>, dim3(grid, y), dim3(256), 0, s, line)
-                                  : launch_pdl(paged_join_kernel<HD, false>, dim3(grid, y), dim3(256), 0, s, line);
+  return k.bf16 ? launch_pdl(paged_join_kernel<HD, true>, dim3(grid, y), dim3(256), 0, s, line)
+                : launch_pdl(paged_join_kernel<HD, false>, dim3(grid, y), dim3(256), 0, s, line);
 }
 
 }  // namespace
 
 int launch_paged_attention_e2m1(const dflash_paged_cache& c, const PagedAttnArgs& a, int type, void* ws,
                                 cudaStream_t s) {
-  return c.head_dim == 128 ? launch<128>(c, a, type, ws, s) : launch<64>(c, a, type, ws, s);
+  KernelArgs k;
+  k.a = a;
+  const Layout l = layout(ws, a.group, c.head_dim, a.max_rows);
+  k.part = l.part;
+  k.ml = l.ml;
+  k.rec = l.rec;
+  k.part_rows = part_rows(a.group, a.max_rows);
+  k.k_pages = static_cast<const uint8_t*>(c.k_pages);
+  k.v_pages = static_cast<const uint8_t*>(c.v_pages);
+  k.k_stride = c.k_page_stride;
+  k.v_stride = c.v_page_stride;
+  k.bf16 = type == DFLASH_TYPE_BF16;
+  if ((long long)a.max_rows * a.group > kRows) return launch_paged_attention_e2m1_rows(k, c.head_dim, s);
+  return c.head_dim == 128 ? launch<128>(k, s) : launch<64>(k, s);
 }
 
 }  // namespace dfl
