@@ -34,7 +34,8 @@ namespace {
 using namespace line;
 
 constexpr int kThreads = 640;
-// Registers: of the softmax warpgroups, of the others, and what a thread is launched with.
+// Registers: of the softmax warpgroups, of the others, and what a thread is launched with
+// (softmax 144 / 152 / 160: prompt chunk 928 / 920 / 926 us).
 constexpr int kRegsSoftmax = 152, kRegsOthers = 56, kRegsLaunch = 96;
 static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOthers <= kThreads * kRegsLaunch, "the block's registers");
 constexpr int kMT = 128, kItemRows = 2 * kMT;
@@ -45,9 +46,10 @@ constexpr int kWides = 3;      // widened halves of K, and of V
 constexpr uint32_t kColO = 256;
 constexpr int kScaleExp = 12;  // of 32 keys' largest scale
 constexpr float kUnscale = 0x1p-12f;
-// The largest weight, and what a reference makes of a tile's largest, log2 (as in
-// paged_attention_e2m1.cu).
-constexpr float kMaxWeight = 15.0f, kFreshWeight = 4.0f;
+// Weights, log2: the largest there may be, and what a reference that grows makes of its
+// job's largest, so that the last place of a weight is 2^-32 of that (2^4 / 2^8 / 2^11:
+// prompt chunk 920 / 936 / 952 us).
+constexpr float kMaxWeight = 15.0f, kFreshWeight = 8.0f;
 constexpr int kLeastK = 13, kLeastV = 127 - 64, kMost = 253;
 
 struct Seg : line::Seg {
@@ -668,7 +670,9 @@ int launch(E2m1Args& k, cudaStream_t s) {
   }
   const long long most = (long long)k.a.max_rows * k.a.group;
   k.rts = (int)((most + kItemRows - 1) / kItemRows);
-  k.seg_cost = 4;
+  // What an item costs beside its tiles, for the cut of the line: of 2 / 4 / 8 tiles
+  // prompt chunks take 922 / 920 / 907 us.
+  k.seg_cost = 8;
   k.slots = C::kSlots;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   int rc;

@@ -565,7 +565,9 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  * fp16 times a power of two per row (2^-39 of a row's largest may be lost), keys
  * and values fp16 times one per row (2^-34 of a row's largest scale); a weight below
  * 2^-18 of the row's largest, times the power of two of its value row, keeps fewer
- * bits, the last at 2^-28.  Scores beyond float32's range are undefined. */
+ * bits, the last at 2^-28.  With R above 128 that power is one for 32 neighbouring
+ * positions (2^-34 of the largest scale among them may be lost), and the last bit of a
+ * weight is at 2^-32.  Scores beyond float32's range are undefined. */
 size_t dflash_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim,
                                               int max_rows);
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_batch* batch,

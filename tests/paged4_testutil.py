@@ -82,8 +82,9 @@ def pack_fast(x):
     return np.concatenate([c[..., 0::2] | (c[..., 1::2] << 4), two], -1)
 
 
-def reference(p, q, causal, window, scale, only=None):
+def reference(p, q, causal, window, scale, only=None, max_rows=None):
     """out, lse and the bounds on their errors (see bound)."""
+    together = (max_rows or max(p.rows)) * q.shape[1] // p.n_kv > 128
     kp, vp = p.host()
     q64 = to64(q)
     n, n_q, hd = q64.shape
@@ -98,8 +99,10 @@ def reference(p, q, causal, window, scale, only=None):
         v = e2m1.sequence(vp, p.table_np[b], length, p.page)
         at = np.arange(length)
         vs = np.abs(e2m1.split(vp[p.table_np[b][at // p.page], :, at % p.page])[1]).max(-1)      # [length, heads]
+        if together:            # of 32 neighbouring positions the largest
+            vs = np.repeat([vs[i:i + 32].max(0) for i in range(0, length, 32)], 32, 0)[:length]
         power = 2.0 ** np.maximum(np.floor(np.log2(np.maximum(vs, 2.0 ** -140))), -64)
-        ks = np.abs(e2m1.split(kp[p.table_np[b][at // p.page], :, at % p.page])[1]).max(-1)
+        ks = np.abs(e2m1.split(kp[p.table_np[b][at // p.page], :, at % p.page])[1]).max(-1)      # (their largest counts)
         pos = np.arange(length - (s1 - s0), length)[:, None]
         hide = np.zeros((s1 - s0, length), dtype=bool)
         if causal:
@@ -122,7 +125,7 @@ def reference(p, q, causal, window, scale, only=None):
             out[s0:s1, h] = w @ v[:, g]
             lse[s0:s1, h] = np.where(seen, m + np.log(np.where(seen, tot, 1)), -np.inf)
             mean = w @ np.abs(v[:, g])
-            few = (w * power[None, :, g]).max(1)
+            few = (w * power[None, :, g]).max(1) * (2.0 ** -4 if together else 1.0)
             bo, bl = bound(out[s0:s1, h], lse[s0:s1, h], mean, size, most, few, w @ vs[:, g], length, hd, p.dtype)
             b_out[s0:s1, h] = np.where(seen[:, None], bo, 0)
             b_lse[s0:s1, h] = np.where(seen, bl, 0)
@@ -149,7 +152,8 @@ def bound(out, lse, mean, size, most, few, mean_scale, n, hd, dtype):
                 log2 terms: 6 e (Z + 130); a softmax mean is then off by 2 d A;
       weights   rounded to fp16: 2^-11 A, and an absolute 2^-25 where the row's
                 largest weight times its value row's power (few) is at least 2^4:
-                2^-29 n few times what a value has beside its power, 12;
+                2^-29 n few times what a value has beside its power, 12 (above 128
+                packed rows 2^8 and the power of 32 neighbours: few is given so);
       sums      n additions of either product, 2 e each, twice; rescaling and
                 merging of partial results: 32 e A;
       output    rounded once: u |out|, or 2^-25 where fp16 is subnormal."""
@@ -174,9 +178,9 @@ def run(p, q, out=None, lse=True, max_rows=None, ws=None, **kw):
     return out, lse_t, dfl.dflash_read_status(ws)
 
 
-def check(p, q, out, lse, causal=True, window=0, scale=None, only=None):
+def check(p, q, out, lse, causal=True, window=0, scale=None, only=None, max_rows=None):
     scale = q.shape[2] ** -0.5 if scale is None else scale
-    want, want_l, b_out, b_lse = reference(p, q, causal, window, scale, only)
+    want, want_l, b_out, b_lse = reference(p, q, causal, window, scale, only, max_rows)
     rows = np.zeros(q.shape[0], dtype=bool)
     for b in range(len(p.lens)):
         if only is None or b in only:

@@ -145,6 +145,8 @@ CASES = [
     ([260], [260], 4, 4, 64, 32),
     ([2000, 33], [16, 1], 16, 2, 64, 128),                  # 128 packed rows, and 8
     ([5, 3000], [5, 30], 6, 3, 128, 16),
+    ([800, 300, 64, 1, 700], [129, 300, 2, 1, 0], 2, 2, 128, 32),   # items of 129, 256 and 44, 2 and 1 rows
+    ([1500, 90], [400, 90], 5, 1, 64, 128),
 ]
 
 
@@ -198,7 +200,7 @@ def test_items_cut_between_ctas(n_q, lens, rows):
 
 
 @pytest.mark.parametrize("dtype", [BF, F16])
-@pytest.mark.parametrize("rows", [2, 40])
+@pytest.mark.parametrize("rows", [2, 40, 200])
 def test_tail_behind_a_dominant_key(dtype, rows):
     """One key takes nine tenths of every row; its values are tiny, so that the
     others, 2^-15 of its weight each, are the output."""
@@ -229,6 +231,13 @@ def test_scores_that_grow_and_magnitudes_of_any_size():
     q = rows_tensor(30, 6, hd, BF, 4)
     out, lse, _ = run(p, q)
     check(p, q, out, lse)
+    # more rows share a power with 32 positions: sizes that differ less
+    v = rng.standard_normal((n, 2, hd)).astype(np.float32) * np.exp2(rng.integers(-8, 8, (n, 2, 1))).astype(np.float32)
+    v = torch.from_numpy(v).to(BF).float().numpy()
+    many = Paged4([n], [300], 2, hd, 32, BF, values=[[k], [v]])
+    q = rows_tensor(300, 6, hd, BF, 4)
+    out, lse, _ = run(many, q)
+    check(many, q, out, lse)
     big = Paged4([n], [9], 2, hd, 32, BF, values=[[k * 2.0 ** 50], [v * 2.0 ** 60]])
     q = rows_tensor(9, 6, hd, BF, 4) * 2.0 ** -50
     out, lse, _ = run(big, q)
@@ -239,11 +248,12 @@ def test_scores_that_grow_and_magnitudes_of_any_size():
     check(small, q, out, lse)
 
 
-def test_rows_do_not_reach_into_one_another():
+@pytest.mark.parametrize("n", [20, 60])
+def test_rows_do_not_reach_into_one_another(n):
     """A row that is not finite, one of huge values and one of zeros among others
     of its item; a cache row that is not finite voids its head only."""
-    p = Paged4([500, 400], [20, 20], 2, 128, 64, BF, seed=8)
-    q = rows_tensor(40, 10, 128, BF, 4)
+    p = Paged4([500, 400], [n, n], 2, 128, 64, BF, seed=8)
+    q = rows_tensor(2 * n, 10, 128, BF, 4)
     clean, lse0, _ = run(p, q)
     check(p, q, clean, lse0)
     q2 = q.clone()
@@ -252,7 +262,7 @@ def test_rows_do_not_reach_into_one_another():
     q2[5, 0] = 1e30
     q2[6, 7] = 0
     out, lse, _ = run(p, q2)
-    same = torch.ones(40, 10, dtype=torch.bool, device="cuda")
+    same = torch.ones(2 * n, 10, dtype=torch.bool, device="cuda")
     for r, h in ((3, 2), (4, 1), (5, 0), (6, 7)):
         same[r, h] = False
     assert torch.equal(out[same], clean[same]) and torch.equal(lse[same], lse0[same])
@@ -261,8 +271,8 @@ def test_rows_do_not_reach_into_one_another():
     pid = int(p.table_np[0, 2])
     pages[pid, 1, 7, 64:66] = 0xFF                       # NaN scale of one block of V, KV head 1, position 135
     out, lse, _ = run(p, q)
-    assert torch.equal(out[20:], clean[20:]) and torch.equal(out[:20, :5], clean[:20, :5])
-    assert torch.equal(lse[:20, :5], lse0[:20, :5])
+    assert torch.equal(out[n:], clean[n:]) and torch.equal(out[:n, :5], clean[:n, :5])
+    assert torch.equal(lse[:n, :5], lse0[:n, :5])
 
 
 def test_bad_pages_read_as_zeros_and_requests_that_do_not_fit_stay():
@@ -310,14 +320,15 @@ def test_lengths_in_between_and_max_rows_above_the_batchs():
     a = run(p, q)
     b = run(p, q, max_rows=200)
     check(p, q, *a[:2])
-    check(p, q, *b[:2])
+    check(p, q, *b[:2], max_rows=200)
 
 
-def test_streams_threads_and_a_captured_graph():
-    p = Paged4([3000, 400, 77], [8, 8, 8], 2, 128, 64, BF, seed=9)
-    q = rows_tensor(24, 10, 128, BF, 4)
+@pytest.mark.parametrize("rows", [8, 40])
+def test_streams_threads_and_a_captured_graph(rows):
+    p = Paged4([3000, 400, 77], [rows] * 3, 2, 128, 64, BF, seed=9)
+    q = rows_tensor(3 * rows, 10, 128, BF, 4)
     want, lse, _ = run(p, q)
-    need = dfl.dflash_paged_attention_workspace_bytes(10, 2, 128, 8)
+    need = dfl.dflash_paged_attention_workspace_bytes(10, 2, 128, rows)
     got = []
 
     def other(i):
@@ -327,7 +338,7 @@ def test_streams_threads_and_a_captured_graph():
         s.wait_stream(torch.cuda.default_stream())
         out = torch.empty_like(q)
         for _ in range(5):
-            dfl.dflash_paged_attention(p.cache, q, out, *p.batch, 8, ws, stream=s)
+            dfl.dflash_paged_attention(p.cache, q, out, *p.batch, rows, ws, stream=s)
         s.synchronize()
         got.append(out)
     threads = [threading.Thread(target=other, args=(i,)) for i in range(3)]
@@ -340,8 +351,8 @@ def test_streams_threads_and_a_captured_graph():
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        dfl.dflash_paged_attention(p.cache, q, out, *p.batch, 8, ws)
-    for n in (3000, 2500, 3):
+        dfl.dflash_paged_attention(p.cache, q, out, *p.batch, rows, ws)
+    for n in (3000, 2500, 3, 0):
         p.kv_len[0] = n
         out.zero_()
         graph.replay()
