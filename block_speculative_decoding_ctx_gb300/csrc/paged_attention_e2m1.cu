@@ -12,7 +12,9 @@
 // positions or a single token costs the softmax what its rows are, not 128, and all
 // its threads have keys; and the widened K goes from the codes straight to tensor
 // memory as an operand, a row to a lane, without a trip through shared memory, which
-// is the busiest part here.
+// is the busiest part here.  Calls with more than 128 packed rows to a request go to
+// paged_attention_e2m1_rows.cu (from 65 on it would take ragged blocks of 16, 80 rows,
+// from 143 to 162 us).
 //
 // Values.  A code times its scale has 10 significant bits.  A row's scales are
 // brought to [2^12, 2^13) by a power of two of the row's largest, so that the
@@ -23,8 +25,8 @@
 // value row, so that the tail behind a dominant key with small values keeps its
 // places: weights are fp16 up to 2^15, 2^4 at least for the largest when a reference
 // is set, and end at 2^-24, so their last place is 2^-28 of the largest.  (References
-// at 2^11 / 2^8 / 2^4 / 2^0: blocks of 8 155 / 150 / 145 / 141 us, prompt chunk 1,673 /
-// 1,571 / 1,487 / 1,434; the lower, the rarer they grow, and the more of a long tail is
+// at 2^11 / 2^8 / 2^4 / 2^0: blocks of 8 155 / 150 / 145 / 141 us, ragged blocks 158 /
+// 152 / 145 / 139; the lower, the rarer they grow, and the more of a long tail is
 // rounded away: 2^-28 of 131,072 keys is 2^-11 of the largest, 2^-24 would be 2^-7.)
 //
 // Roles (640 threads, a persistent CTA on its part of the line, see paged_line.cuh;
@@ -44,17 +46,17 @@
 //
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16):
 //   32 requests, blocks of 8, context 8,192: 138 us for 341 MB, 2.5 TB/s, 0.37 of the
-//     measured copy (with L2 flushed 145, a bf16 cache 193, E4M3 182).  The tensor cores are at work
-//     for 0.65 of the time, waiting for operands most of it: a product of 48 columns
-//     (16 keys or values deep) alone takes 49 clocks where K comes from tensor memory
-//     and 72 where V comes from shared memory, nearly twice as long beside the widening
-//     and the weights, which keep shared memory busy; issue slots 51 %;
+//     measured copy (with L2 flushed 145; a bf16 cache 193, E4M3 182).  The products'
+//     operands: in a timeline of a CTA the issuer is never without a product to issue, and a
+//     tile's take 1,850 clocks, 750 for the scores and 1,100 for the values.  Alone a
+//     product (16 deep, of up to 64 columns) takes 49 clocks where K comes from tensor
+//     memory and 72 where V comes from shared memory, 970 a tile; beside them the widening
+//     and the weights keep shared memory busy, 0.6 of its cycles in all.  Tensor cores
+//     16 % of their rate, issue slots 51 %;
 //   16 blocks of 16, context 512 to 131,072: 139 us, alike (flushed 143, bf16 150,
 //     E4M3 158);
-//   prompt chunk, 2 x 2,048 rows, context up to 16,384: 1,489 us, 0.70 PFLOP/s (bf16
-//     748, E4M3 1,266).  Tensor cores 28 % of their rate and busy throughout, shared
-//     memory 50 %, issue slots 53 %; without references that grow it would be 1,208:
-//     each time one does the tile is held up for about 2,000 clocks;
+//   without references that grow these two would take 131 and 127: each time one does
+//     its stream is held up for about 2,000 clocks;
 //   one token, context 1,000: latency, 12 us.
 //
 // All waits are bounded.  When one gives up, the softmax warps run on to the end of
@@ -69,7 +71,7 @@ using namespace line;
 
 constexpr int kThreads = 640;
 // Registers: of the softmax warpgroups, of the others, and what a thread is launched with
-// (softmax 136 / 144 / 152 / 160: prompt chunk 1,554 / 1,513 / 1,485 / 1,544 us).
+// (softmax 144 / 152 / 160: ragged blocks 145 / 143 / 147 us, blocks of 8 alike).
 constexpr int kRegsSoftmax = 152, kRegsOthers = 56, kRegsLaunch = 96;
 static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOthers <= kThreads * kRegsLaunch, "the block's registers");
 constexpr int kRows = 128;     // of an item at most
@@ -84,7 +86,8 @@ constexpr float kUnseen = 0x1p100f;  // minus the reference of a column that has
 // tile's largest.
 constexpr float kMaxWeight = 15.0f, kFreshWeight = 4.0f;
 // A weight that makes its column's reference grow once some other column's has to: all
-// that are about to do so at once (with 15 prompt chunk 1,567 us for 1,487, blocks alike).
+// that are about to do so at once (when prompt chunks ran here, 1,487 us for the 1,567
+// with 15; blocks alike).
 constexpr float kRenewWeight = 6.0f;
 // Exponents (biased) that rows of K and V are scaled by: so that the factors stay
 // normal numbers.  Of V 2^-64 at least: the sums l, in which that power is taken
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
           __syncwarp();
         };
         // Whatever is ready goes next: in a fixed order either waits for what the other's
-        // operands wait for (prompt chunk 1,927 us for 1,581, when that was tried).
+        // operands wait for (blocks of 8 160 us for 147, when that was tried).
         const int buffers = alt ? 4 : 2;  // of S
         int ns = 0, nv = 0;               // scores and values issued
         unsigned long long since = 0;
