@@ -30,7 +30,7 @@
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16): prompt chunk, 2 x
 // 2,048 rows, context 8,192 to 16,384, 922 us, 1.13 PFLOP/s, 0.58 of the measured burst
 // (a bf16 cache 746, E4M3 1,253).  Tensor cores 49 % of their rate, issue slots 59 % (632 M
-// instructions, a third of them widening), shared memory 0.73 of its cycles: no unit is
+// instructions), shared memory 0.73 of its cycles: no unit is
 // at its end, the chain scores, weights, values of either stream is what is left.
 //
 // All waits are bounded, as in paged_attention_e2m1.cu.
