@@ -11,7 +11,7 @@
 // sines and cosines once for all heads: P times w_j / (2 pi) in 2^-64ths of a
 // turn is a product of integers modulo 2^64, exact for any position; what is left
 // of it beside the nearest quarter turn is at most an eighth of a turn and becomes
-// a float32.
+// two float32s.
 //   Then a thread moves 16 values of one (row, head of q, k or v) at a time, two
 // such pieces on their way: two runs of 8 values, for a rotated row of layout
 // HALF the two whose values are each other's pairs (values 8 l and rotary_dim / 2
@@ -20,8 +20,8 @@
 // both, and one shuffle finds its largest magnitude.
 //
 // Measured on GB300 (40 query and 8 KV heads of 128), bytes at the measured copy's rate
-// in brackets: prompts rotated into a 16-bit cache, queries beside them (782 MB) 129 us
-// [0.91]; prompts into 4 bits (237 MB) 64 us [0.56], which instructions bound (62 % of the
+// in brackets: prompts rotated into a 16-bit cache, queries beside them (782 MB) 131 us
+// [0.90]; prompts into 4 bits (237 MB) 64 us [0.56], which instructions bound (62 % of the
 // issue slots, 250 a warp for 16 values a thread, like the E4M3 append's); a step's 256
 // rows 10 us, the host's launch.
 #include "paged_rows.cuh"
@@ -37,16 +37,41 @@ constexpr int kMaxRows = 32;   // of a block
 // 133 us; 1,024 with another form of the loop 162 for 154).
 constexpr int kMostUnits = 512;
 
-// Sine and cosine of `turns` 2^-64ths of a turn, times f.
+// Cosine and sine of `turns` 2^-64ths of a turn, times f, each rounded about once: what
+// they turn is rounded into 4 bits next, and a value that falls on the other side of a
+// code's border is a whole step off (with sincospif, 1.8e-5 of the 16-bit results differ for
+// 1.4e-5, and rotated prompts take 133 us for 135).  Beside the nearest quarter turn, the
+// angle is p + e, p a float32 of at most pi / 4 and e its rest; Taylor's series of sine to
+// p^11 and of cosine to p^10 (2^-36 and 2^-33 are left out), added to their first terms last.
 __device__ __forceinline__ float2 cos_sin(unsigned long long turns, float f) {
   const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62);
   const long long rest = (long long)(turns - ((unsigned long long)quarter << 62));
-  const float half_turns = (float)(int)(rest >> 32) * 0x1p-31f;
-  float s, c;
-  sincospif(half_turns, &s, &c);
+  const float h = (float)(int)(rest >> 32);
+  const float low = (float)(rest - ((long long)(int)h << 32));
+  constexpr double kTurn = 6.283185307179586 / 4294967296.0;  // 2^-32 of a turn
+  constexpr float kHi = (float)kTurn, kLo = (float)(kTurn - (double)kHi), kLow = (float)(kTurn / 4294967296.0);
+  const float p = h * kHi, e = fmaf(h, kHi, -p) + fmaf(h, kLo, low * kLow);
+  const float t = p * p, t_rest = fmaf(p, p, -t);
+  float s3 = fmaf(t, -1.0f / 39916800.0f, 1.0f / 362880.0f);  // (sine / p - 1) / t
+  s3 = fmaf(t, fmaf(t, fmaf(t, s3, -1.0f / 5040.0f), 1.0f / 120.0f), -1.0f / 6.0f);
+  float c4 = fmaf(t, -1.0f / 3628800.0f, 1.0f / 40320.0f);  // (cosine - 1 + t / 2) / t^2
+  c4 = fmaf(t, fmaf(t, c4, -1.0f / 720.0f), 1.0f / 24.0f);
+  const float w = fmaf(t, -0.5f, 1.0f), w_rest = fmaf(t, -0.5f, 1.0f - w);  // 1 - t / 2
+  const float s_rest = fmaf(p * t, s3, e * fmaf(t * t, c4, w));
+  const float c_rest = w_rest + fmaf(t * t, c4, fmaf(-0.5f, t_rest, -e * fmaf(p * t, s3, p)));
+  const float s = fmaf(p, f, s_rest * f), c = fmaf(w, f, c_rest * f);
   const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
   // quarter 0: (c, s)  1: (-s, c)  2: (-c, -s)  3: (s, -c)
-  return make_float2(quarter == 1 || quarter == 2 ? -x * f : x * f, quarter >= 2 ? -y * f : y * f);
+  return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter >= 2 ? -y : y);
+}
+// x c - y s and y c + x s.  (Adding the rounded product's rounding back, Kahan's difference
+// of products, makes 1.2e-5 of the 16-bit results other than the exact ones' rounding for
+// 1.4e-5, and rotated prompts take 143 us for 135.)
+__device__ __forceinline__ void turn2(float2& x, float2& y, float2 c, float2 s) {
+  const float2 ns = make_float2(-s.x, -s.y);
+  const float2 a = fma2(x, c, mul2(y, ns)), b = fma2(y, c, mul2(x, s));
+  x = a;
+  y = b;
 }
 
 struct Piece {
@@ -135,15 +160,16 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float4 cs = *reinterpret_cast<const float4*>(t + p.c0 + 2 * e);
-            const float2 x = f[e], y = f[4 + e];
-            f[e] = make_float2(x.x * cs.x - y.x * cs.y, x.y * cs.z - y.y * cs.w);
-            f[4 + e] = make_float2(y.x * cs.x + x.x * cs.y, y.y * cs.z + x.y * cs.w);
+            turn2(f[e], f[4 + e], make_float2(cs.x, cs.z), make_float2(cs.y, cs.w));
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 cs = t[(e < 4 ? p.c0 : p.c1) / 2 + (e & 3)], x = f[e];
-            f[e] = make_float2(x.x * cs.x - x.y * cs.y, x.y * cs.x + x.x * cs.y);
+          for (int e = 0; e < 8; e += 2) {
+            const float4 cs = *reinterpret_cast<const float4*>(t + (e < 4 ? p.c0 : p.c1) / 2 + (e & 3));
+            float2 x = make_float2(f[e].x, f[e + 1].x), y = make_float2(f[e].y, f[e + 1].y);
+            turn2(x, y, make_float2(cs.x, cs.z), make_float2(cs.y, cs.w));
+            f[e] = make_float2(x.x, y.x);
+            f[e + 1] = make_float2(x.y, y.y);
           }
         }
       }
