@@ -20,21 +20,22 @@
 // both, and one shuffle finds its largest magnitude.
 //
 // Measured on GB300 (40 query and 8 KV heads of 128), bytes at the measured copy's rate
-// in brackets: prompts rotated into a 16-bit cache, queries beside them (782 MB) 131 us
-// [0.90]; prompts into 4 bits (237 MB) 64 us [0.56], which instructions bound (62 % of the
-// issue slots, 250 a warp for 16 values a thread, like the E4M3 append's); a step's 256
-// rows 10 us, the host's launch.
+// in brackets: prompts rotated into a 16-bit cache, queries beside them (782 MB) 125 us
+// [0.93]; prompts into 4 bits (237 MB) 57 us [0.62]: latency of the loads beside the
+// instructions (59 % of the issue slots, 190 a warp for 16 values a thread; 64 us with
+// 250, before a thread's pieces shared their place); a step's 256 rows 10 us, the host's
+// launch.
 #include "paged_rows.cuh"
 
 namespace dfl {
 namespace {
 
-constexpr int kThreads = 256;  // (128: rotated prompts 145 us for 133, prompts into 4 bits 73 for 65)
-// Pieces of a thread on their way (1 / 2 / 3: rotated prompts 145 / 133 / 147 us).
+constexpr int kThreads = 256;  // (128: rotated prompts 133 us for 131, prompts into 4 bits 59 for 57)
+// Pieces of a thread on their way (1 / 2 / 3: rotated prompts 135 / 131 / 137 us).
 constexpr int kPieces = 2;
 constexpr int kMaxRows = 32;   // of a block
-// (row, head) of a block, as far as that is no single row (256 / 512: rotated prompts 139 /
-// 133 us; 1,024 with another form of the loop 162 for 154).
+// (row, head) of a block, as far as that is no single row (256 / 512 / 1,024: rotated prompts
+// 133 / 131 / 137 us, prompts into 4 bits 61 / 57 / 57).
 constexpr int kMostUnits = 512;
 
 // Cosine and sine of `turns` 2^-64ths of a turn, times f, each rounded about once: what
@@ -74,6 +75,24 @@ __device__ __forceinline__ void turn2(float2& x, float2& y, float2 c, float2 s) 
   y = b;
 }
 
+// Where a row goes.
+struct Spot {
+  uint8_t* page[2];  // of K and of V, or null: nowhere
+  int id, at;        // the page's, and row of a head there
+  int pos;           // below 0: none, or no row of a request's
+};
+
+// The larger magnitudes of two pairs, under signs of no meaning; NaN where either is.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF16)
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 struct Piece {
   int row, slot;        // of the block; head of q, then k, then v
   int c0, c1;           // first columns of its two runs
@@ -88,22 +107,26 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
   constexpr bool E4M3 = FORMAT == DFLASH_CACHE_E4M3, E2M1 = FORMAT == DFLASH_CACHE_E2M1;
   constexpr int kLanes = HD / 16;              // threads per (row, head)
   constexpr int kUnits = kThreads / kLanes;    // (row, head) at once
-  __shared__ Place places[kMaxRows];
+  // A thread's pieces: without rotation the same row and head of k and of v, so that one
+  // place serves both, else any.
+  constexpr uint32_t kStep = ROPE ? kUnits : 0, kTurn = ROPE ? kUnits * kPieces : kUnits;
+  static_assert(ROPE || kPieces == 2, "of k and of v");
+  __shared__ Spot spots[kMaxRows];
   __shared__ Found found;
   __shared__ float2 turn_s[ROPE ? kMaxRows : 1][64];  // cosine and sine
   const PagedMoveArgs& m = a.m;
   const int n0 = blockIdx.x * rows, lane = threadIdx.x % kLanes;
   const int half = a.rope.rotary_dim / 2;      // pairs
   const int n_q = ROPE ? a.n_q : 0;
-  const uint32_t per_row = n_q + 2u * m.n_kv;
+  const uint32_t per_row = ROPE ? n_q + 2u * m.n_kv : m.n_kv;
   look_through<kThreads>(m.batch, n0, m.status, &found);
   const int mine = max(0, min(rows, found.end - n0));
   const uint32_t units = mine * per_row;
 
-  auto piece = [&](uint32_t u) {
+  auto piece = [&](uint32_t u, int i) {
     Piece p;
-    p.row = (int)__umulhi(u, magic);  // u / per_row
-    p.slot = (int)(u - p.row * per_row);
+    p.row = (int)__umulhi(ROPE ? u : 2 * u, magic);  // u / per_row (launch_rope)
+    p.slot = (int)(u - p.row * per_row) + (ROPE ? 0 : i * m.n_kv);
     const size_t n = n0 + p.row;
     p.turned = ROPE && p.slot < n_q + m.n_kv && lane * 8 < half;
     p.c0 = p.turned ? lane * 8 : lane * 16;
@@ -111,49 +134,59 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
     if (p.slot < n_q) {
       p.x = a.q + (n * a.q_row + (size_t)p.slot * a.q_head) * 2;
     } else {
-      const int side = p.slot >= n_q + m.n_kv, head = p.slot - n_q - side * m.n_kv;
+      const int side = ROPE ? p.slot >= n_q + m.n_kv : i, head = p.slot - n_q - side * m.n_kv;
       p.x = m.x[side] + (n * m.row_stride[side] + (size_t)head * m.head_stride[side]) * 2;
     }
     return p;
   };
   uint4 w[kPieces][2] = {};
-  auto load_rows = [&](uint32_t u0) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint32_t u = u0 + i * kUnits;
-      if (u < units) {
-        const Piece p = piece(u);
-        w[i][0] = *reinterpret_cast<const uint4*>(p.x + p.c0 * 2);
-        w[i][1] = *reinterpret_cast<const uint4*>(p.x + p.c1 * 2);
-      }
+  auto load_row = [&](uint32_t u0, int i) {
+    const uint32_t u = u0 + i * kStep;
+    if (u < units) {
+      const Piece p = piece(u, i);
+      w[i][0] = *reinterpret_cast<const uint4*>(p.x + p.c0 * 2);
+      w[i][1] = *reinterpret_cast<const uint4*>(p.x + p.c1 * 2);
     }
   };
   // the first rows are on their way while places and angles are made
-  load_rows(threadIdx.x / kLanes);
-  if ((int)threadIdx.x < mine) places[threadIdx.x] = find_row(m.batch, found, n0 + threadIdx.x, m.status);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) load_row(threadIdx.x / kLanes, i);
+  if ((int)threadIdx.x < mine) {
+    const Place pl = find_row(m.batch, found, n0 + threadIdx.x, m.status);
+    Spot spot;
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+      spot.page[side] = pl.there ? m.pages[side] + (size_t)pl.page * m.page_stride[side] * (E4M3 || E2M1 ? 1 : 2) : nullptr;
+    spot.id = (int)pl.page;
+    spot.at = pl.at;
+    spot.pos = pl.owned ? pl.pos : -1;
+    spots[threadIdx.x] = spot;
+  }
   __syncthreads();
   if (ROPE) {
     for (int i = threadIdx.x; i < mine * half; i += kThreads) {
       const int row = i / half, j = i - row * half;
-      const long long pos = a.positions ? (long long)__ldg(a.positions + n0 + row) : places[row].pos;
+      const long long pos = a.positions ? (long long)__ldg(a.positions + n0 + row) : spots[row].pos;
       turn_s[row][j] = cos_sin((unsigned long long)pos * a.rope.turns[j], a.rope.factor);
     }
     __syncthreads();
   }
 
   // whole warps stay together: pieces past the last take part in the shuffles
-  const uint32_t turns = (units + kUnits * kPieces - 1) / (kUnits * kPieces);
+  const uint32_t turns = (units + kTurn - 1) / kTurn;
   for (uint32_t turn = 0; turn < turns; ++turn) {
-    const uint32_t u0 = turn * (kUnits * kPieces) + threadIdx.x / kLanes;
+    const uint32_t u0 = turn * kTurn + threadIdx.x / kLanes;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const uint32_t u = u0 + i * kUnits;
-      const Piece p = piece(min(u, units - 1));
-      const Place pl = places[p.row];
+      const uint32_t u = u0 + i * kStep;
+      const Piece p = piece(min(u, units - 1), i);
       const uint32_t v[8] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w, w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
       float2 f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = unpack16<BF16>(v[e]);
+      // the next turn's rows, as early as their registers are free (without rotation, where
+      // more is live here, this is slower: 63 us for 57; rotated prompts 131 for 135)
+      if (ROPE) load_row(u0 + kTurn, i);
       if (p.turned) {
         const float2* t = turn_s[p.row];
         if (a.rope.layout == DFLASH_ROPE_HALF) {
@@ -182,8 +215,8 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
       uint32_t m0 = 0, m1 = 0;
       if (!ROPE) {  // as they came, two at a time
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m0 = __vmaxu2(m0, v[e] & 0x7FFF7FFFu);
-        const float2 top = unpack16<BF16>(m0);
+        for (int e = 0; e < 8; ++e) m0 = max_abs<BF16>(m0, v[e]);
+        const float2 top = unpack16<BF16>(m0 & 0x7FFF7FFFu);
         m0 = m1 = max(__float_as_uint(top.x), __float_as_uint(top.y));
       } else if (E4M3 || E2M1) {
 #pragma unroll
@@ -204,16 +237,16 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
       }
       if (u >= units) continue;
       if (p.slot < n_q) {
-        if (!pl.owned || pl.pos < 0) continue;
+        if (spots[p.row].pos < 0) continue;
         uint8_t* q = a.q_out + ((size_t)(n0 + p.row) * a.o_row + (size_t)p.slot * a.o_head) * 2;
         *reinterpret_cast<uint4*>(q + p.c0 * 2) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(q + p.c1 * 2) = make_uint4(o[4], o[5], o[6], o[7]);
         continue;
       }
-      if (!pl.there) continue;
-      const int side = p.slot >= n_q + m.n_kv, head = p.slot - n_q - side * m.n_kv;
-      const size_t row = ((size_t)head << m.batch.page_shift) + pl.at;
-      uint8_t* page = m.pages[side] + (size_t)pl.page * m.page_stride[side] * (E4M3 || E2M1 ? 1 : 2);
+      const int side = ROPE ? p.slot >= n_q + m.n_kv : i, head = p.slot - n_q - side * m.n_kv;
+      uint8_t* const page = spots[p.row].page[side];
+      if (!page) continue;
+      const uint32_t row = ((uint32_t)head << m.batch.page_shift) + spots[p.row].at;  // below 2^19
       if (E2M1) {
         uint8_t* rec = page + row * e2m1_record(HD);
         auto scale = [](uint32_t top) {
@@ -224,9 +257,9 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
           return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : s == 0.0f ? 1.0f : s;
         };
         auto codes = [&](const float2* x, float s) {
-          const float y = __frcp_rn(s);
+          const float y = __frcp_rn(s), y_rest = fmaf(-s, y, 1.0f) * y;
           uint32_t c = 0;
-          if (quotients_small(s)) {
+          if (quotients_small(s) || (!ROPE && s > 0x1p100f)) {  // (there y_rest has few bits)
 #pragma unroll 1
             for (int e = 0; e < 4; ++e) {
               const float2 q = quotients_slow(e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3], s);
@@ -235,7 +268,13 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
             return c;
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c |= e2m1x2(quotients(x[e], s, y)) << (8 * e);
+          for (int e = 0; e < 4; ++e) {
+            // 16-bit values lie on a border between codes or 2^-14 of themselves from it, and
+            // x times the reciprocal to 48 bits is the border where x / s is (-0 becomes 0)
+            const float2 q = ROPE ? quotients(x[e], s, y)
+                                  : fma2(x[e], make_float2(y, y), fma2(x[e], make_float2(y_rest, y_rest), make_float2(0.0f, 0.0f)));
+            c |= e2m1x2(q) << (8 * e);
+          }
           return c;
         };
         const float s0 = scale(m0), s1 = ROPE ? scale(m1) : s0;
@@ -261,24 +300,30 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
                                           __NV_SATFINITE, __NV_E4M3);
         *reinterpret_cast<uint2*>(page + row * HD + p.c0) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         *reinterpret_cast<uint2*>(page + row * HD + p.c1) = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
-        if (lane == 0) m.scale[side][(((size_t)pl.page * m.n_kv) << m.batch.page_shift) + row] = s;
+        if (lane == 0) m.scale[side][(((size_t)spots[p.row].id * m.n_kv) << m.batch.page_shift) + row] = s;
       } else {
         *reinterpret_cast<uint4*>(page + (row * HD + p.c0) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(page + (row * HD + p.c1) * 2) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
-    if (turn + 1 < turns) load_rows(u0 + kUnits * kPieces);
+    if (!ROPE) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) load_row(u0 + kTurn, i);
+    }
   }
 }
 
 template <int HD, int FORMAT, bool BF16, bool ROPE>
 int launch_rope(const PagedRopeArgs& a, cudaStream_t s) {
-  const long long each = a.m.batch.rows / 608;  // 4 blocks for each of 152 SMs come first
+  const long long each = ceil_div(a.m.batch.rows, 608);  // 4 blocks for each of 152 SMs come first
   const int per_row = a.n_q + 2 * a.m.n_kv;
   const int most = min(kMaxRows, max(1, kMostUnits / per_row));
-  const int rows = (int)min((long long)most, max(1ll, each));
+  // ... and what is more comes in equal shares (prompts into 4 bits 57 us, 59 with blocks of `most`)
+  const long long waves = max(1ll, (each + most - 1) / most);
+  const int rows = (int)max(1ll, (each + waves - 1) / waves);
   const int grid = max(1, ceil_div(a.m.batch.rows, rows));
-  // u / per_row = u * magic / 2^32 for u < rows * per_row: 0 for a single row, else u and
+  // u / per_row = u * magic / 2^32 for u < rows * per_row (without rotation twice a pair's
+  // number): 0 for a single row, else u and
   // per_row are at most kMostUnits
   const uint32_t magic = rows == 1 ? 0u : (uint32_t)(((1ull << 32) + per_row - 1) / per_row);
   return launch_pdl(paged_rope_kernel<HD, FORMAT, BF16, ROPE>, dim3(grid), dim3(kThreads), 0, s, a, rows, magic);

@@ -95,6 +95,33 @@ def test_values_that_round_oddly(dtype):
         assert torch.equal(got.signbit()[~w.isnan()], w.signbit()[~w.isnan()])
 
 
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_borders_under_every_scale(dtype):
+    """Blocks of every significand that a largest value has, with the values next to each
+    border between two codes and on it, for exponents over the type's range: codes and
+    scales as the oracle's, bit for bit."""
+    hd = 128
+    exps = [-132, -110, -101, -100, -99, -60, 0, 60, 99, 100, 101, 102, 103, 120, 127] if dtype is BF else [-20, -10, 0, 15]
+    bits = 7 if dtype is BF else 10
+    mant = 1 + np.arange(0, 1 << bits, 1 if dtype is BF else 5) / (1 << bits)
+    top = torch.from_numpy(np.outer(2.0 ** np.array(exps), mant).reshape(-1)).to(dtype)
+    n = top.numel()
+    scale = e2m1.split(e2m1.pack(np.repeat(top.float().numpy()[:, None], 16, -1)))[1].astype(np.float64)  # [n, 1]
+    on = torch.from_numpy(np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * scale).to(dtype)  # where representable
+    near = torch.cat([on, (on.view(torch.int16) + 1).view(dtype), (on.view(torch.int16) - 1).clamp_min(0).view(dtype),
+                      on[:, :5] * 0.5, on[:, 2:] * 0.25], 1)                                     # [n, 31]
+    near = torch.cat([near, -near], 1)[:, :60].minimum(top[:, None]).maximum(-top[:, None])
+    x = torch.stack([torch.cat([top[:, None], near[:, 15 * b:15 * b + 15]], 1) for b in (0, 1, 2, 3)] * 2, 1)
+    x = x.reshape(n, 1, hd)
+    p = Paged4([n], [n], 1, hd, 16, dtype, garbage=False)
+    dfl.dflash_paged_append(p.cache, x.cuda(), x.flip(0).cuda(), *p.batch, dfl.workspace(dfl.dflash_paged_workspace_bytes()))
+    for side, rows in ((0, x), (1, x.flip(0))):
+        got = p.host()[side][p.table_np[0, np.arange(n) // 16], :, np.arange(n) % 16]
+        want = e2m1.split(e2m1.pack(rows.float().numpy()))
+        np.testing.assert_array_equal(e2m1.split(got)[1], want[1])
+        np.testing.assert_array_equal(e2m1.split(got)[0], want[0])
+
+
 def test_pages_that_are_none_and_requests_that_do_not_fit():
     lens, rows = [40, 33, 50], [20, 10, 30]
     p = Paged4(lens, rows, 2, 64, 16, BF, garbage=False)
