@@ -21,7 +21,8 @@
 //
 // Measured on GB300 (40 query and 8 KV heads of 128), bytes at the measured copy's rate
 // in brackets: prompts rotated into a 16-bit cache, queries beside them (782 MB) 125 us
-// [0.93]; prompts into 4 bits (237 MB) 57 us [0.62]: latency of the loads beside the
+// [0.93], into E4M3 (728 MB) 151 us [0.72], into 4 bits (705 MB) 133 us [0.79]; prompts
+// into 4 bits as they come (237 MB) 57 us [0.62]: latency of the loads beside the
 // instructions (59 % of the issue slots, 190 a warp for 16 values a thread; 64 us with
 // 250, before a thread's pieces shared their place); a step's 256 rows 10 us, the host's
 // launch.
@@ -91,6 +92,15 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
   else
     asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// Scales for which quotients() is not made come to a size where it is, and their values
+// along: the quotient stays.
+__device__ __forceinline__ void raise(float2* x, float& s) {
+  if (!quotients_small(s)) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], make_float2(0x1p100f, 0x1p100f));
+  s *= 0x1p100f;
 }
 
 struct Piece {
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
         for (int e = 0; e < 8; ++e) m0 = max_abs<BF16>(m0, v[e]);
         const float2 top = unpack16<BF16>(m0 & 0x7FFF7FFFu);
         m0 = m1 = max(__float_as_uint(top.x), __float_as_uint(top.y));
-      } else if (E4M3 || E2M1) {
+      } else if ((E4M3 || E2M1) && __any_sync(0xffffffffu, p.slot >= n_q)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           m0 = max(m0, max(__float_as_uint(f[e].x) & 0x7FFFFFFFu, __float_as_uint(f[e].y) & 0x7FFFFFFFu));
@@ -256,10 +266,11 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
           const float s = __bfloat162float(__float2bfloat16_rn(by6));
           return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : s == 0.0f ? 1.0f : s;
         };
-        auto codes = [&](const float2* x, float s) {
+        auto codes = [&](float2* x, float s) {
+          if (ROPE) raise(x, s);
           const float y = __frcp_rn(s), y_rest = fmaf(-s, y, 1.0f) * y;
           uint32_t c = 0;
-          if (quotients_small(s) || (!ROPE && s > 0x1p100f)) {  // (there y_rest has few bits)
+          if (!ROPE && (quotients_small(s) || s > 0x1p100f)) {  // (there y_rest has few bits)
 #pragma unroll 1
             for (int e = 0; e < 4; ++e) {
               const float2 q = quotients_slow(e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3], s);
@@ -291,13 +302,15 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
         if (p.c1 % 16 == 0) scales[p.c1 / 16] = (uint16_t)(__float_as_uint(s1) >> 16);
       } else if (E4M3) {
         const bool finite = m0 < 0x7F800000u;
-        const float s = !finite ? __uint_as_float(0x7FC00000u) : m0 ? __fdiv_rn(__uint_as_float(m0), 448.0f) : 1.0f;
-        const float y = __fdiv_rn(1.0f, s);
+        const float by448 = __fdiv_rn(__uint_as_float(m0), 448.0f);  // 0 of rotated values below 2^-141, too
+        const float s = !finite ? __uint_as_float(0x7FC00000u) : by448 == 0.0f ? 1.0f : by448;
+        float up = s;  // of the lower values; the upper ones' is the same
+        raise(f + 4, up);
+        raise(f, up = s);
+        const float y = __fdiv_rn(1.0f, up);
         uint32_t c[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          c[e] = __nv_cvt_float2_to_fp8x2(quotients_small(s) ? quotients_slow(f[e], s) : quotients(f[e], s, y),
-                                          __NV_SATFINITE, __NV_E4M3);
+        for (int e = 0; e < 8; ++e) c[e] = __nv_cvt_float2_to_fp8x2(quotients(f[e], up, y), __NV_SATFINITE, __NV_E4M3);
         *reinterpret_cast<uint2*>(page + row * HD + p.c0) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         *reinterpret_cast<uint2*>(page + row * HD + p.c1) = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
         if (lane == 0) m.scale[side][(((size_t)spots[p.row].id * m.n_kv) << m.batch.page_shift) + row] = s;

@@ -380,7 +380,7 @@ int dflash_quantize_e4m3(const void* w, int rows, int cols, void* codes, float* 
  *   BF16, F16  the rows as they are;
  *   E4M3       8-bit codes (as DFLASH_WEIGHTS_E4M3) with one float32 scale
  *              per (page, KV head, row): value = code * scale,
- *              scale = max|row| / 448 (1 for a row of zeros; NaN for a row
+ *              scale = max|row| / 448 (1 where that is 0; NaN for a row
  *              that holds a NaN or an infinity, which then reads back as NaN),
  *              code = value / scale rounded to nearest, ties to even.
  *   E2M1       4-bit codes (1 sign, 2 exponent bits with bias 1, 1 mantissa bit:

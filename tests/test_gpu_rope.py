@@ -150,6 +150,39 @@ def test_position_zero_and_factor_one_are_append(fmt):
     assert torch.equal(q, q_out)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_keys_of_any_size(fmt):
+    """At position 0 with factor 1 nothing turns: rows of every size from bfloat16's
+    smallest on get the codes and scales that append gives them.  A factor that takes them
+    where a scale would be 0 makes zeros of them, under scales of 1."""
+    n, n_kv, hd = 512, 2, 128
+    rng = np.random.default_rng(3)
+    size = 2.0 ** np.linspace(-133, 127, n)
+    x = rng.uniform(0.3, 1.0, (n, n_kv, hd)) * rng.choice([-1.0, 1.0], (n, n_kv, hd)) * size[:, None, None]
+    x[:, :, ::37] = 0
+    x = torch.from_numpy(x.clip(-3e38, 3e38)).to(BF)
+    x[x == 0] = 0                                        # no -0
+    k, zero = x.cuda(), torch.zeros(n, dtype=torch.int64, device="cuda")
+    ws = dfl.workspace(dfl.dflash_paged_workspace_bytes())
+    freq = dfl.dflash_rope_frequencies(hd, 1e6)
+    p, q = (make(fmt, [n], [n], n_kv, hd, 16, BF) for _ in range(2))
+    dfl.dflash_paged_append(p.cache, k, k.flip(0), *p.batch, ws)
+    dfl.dflash_paged_append_rope(q.cache, k, k.flip(0), *q.batch, dfl.dflash_rope_init(freq), ws, positions=zero)
+    assert all(torch.equal(p.pages[i].view(torch.uint8), q.pages[i].view(torch.uint8)) for i in range(2))
+    if fmt == "e4m3":
+        assert all(torch.equal(p.scale[i], q.scale[i]) for i in range(2))
+    k = torch.full_like(k, 2.0 ** -133)
+    k[:, :, 5::9] = 0
+    back = [torch.full_like(k, 7.0) for _ in range(2)]
+    dfl.dflash_paged_append_rope(q.cache, k, k, *q.batch, dfl.dflash_rope_init(freq, factor=2.0 ** -12), ws, positions=zero)
+    dfl.dflash_paged_gather(q.cache, *back, *q.batch, ws)
+    assert (back[0] == 0).all()
+    # values as they came: 2^-133 / 448 is a float32, 2^-133 / 6 below half of bfloat16's smallest, 2^-133
+    assert torch.equal(back[1], k if fmt == "e4m3" else torch.zeros_like(k))
+    if fmt == "e4m3":
+        assert (q.scale[0][q.table_np[0].tolist()] == 1).all()
+
+
 def test_in_place_slices_and_strides():
     """Queries turned in place, and slices of one projection's output."""
     lens, rows, hd, n_kv, n_q = [100, 30], [20, 30], 64, 2, 6
