@@ -555,9 +555,9 @@ def dflash_paged_gather(cache, k, v, row_start, kv_len, page_table, ws, stream=N
 def dflash_rope_frequencies(rotary_dim, theta, stretch=1.0, trained=0.0, slow=1.0, fast=4.0):
     """Radians per position of every pair, a list of rotary_dim / 2 floats."""
     _c_ints("rotary_dim", rotary_dim)
-    f = (ctypes.c_double * max(1, rotary_dim // 2))()
+    f = (ctypes.c_double * 64)()  # the largest rotary_dim's
     _check(lib().dflash_rope_frequencies(rotary_dim, theta, stretch, trained, slow, fast, f), "dflash_rope_frequencies")
-    return list(f)
+    return f[:rotary_dim // 2]
 
 
 def dflash_rope_init(frequencies, layout=DFLASH_ROPE_HALF, factor=1.0):

@@ -118,7 +118,7 @@ def test_frequencies_follow_the_formula(L):
         for kw in (dict(), dict(stretch=8.0), dict(stretch=4.0, trained=8192.0), dict(stretch=0.5, trained=1e6, slow=-2.0, fast=32.0)):
             got = dfl.dflash_rope_frequencies(n, 5e5, **kw)
             np.testing.assert_allclose(got, rotary.frequencies(n, 5e5, **kw), rtol=1e-14)
-    for bad, code in ((dict(rotary_dim=16), "SHAPE"), (dict(rotary_dim=160), "SHAPE"), (dict(rotary_dim=-32), "SHAPE"),
+    for bad, code in ((dict(rotary_dim=16), "SHAPE"), (dict(rotary_dim=(1 << 31) - 32), "SHAPE"), (dict(rotary_dim=160), "SHAPE"), (dict(rotary_dim=-32), "SHAPE"),
                       (dict(theta=0.0), "ARG"), (dict(theta=math.inf), "ARG"), (dict(stretch=0.0), "ARG"),
                       (dict(stretch=math.nan), "ARG"), (dict(trained=-1.0), "ARG"), (dict(trained=8.0, slow=4.0), "ARG"),
                       (dict(trained=8.0, slow=math.nan), "ARG"), (dict(trained=8.0, fast=math.inf), "ARG")):
