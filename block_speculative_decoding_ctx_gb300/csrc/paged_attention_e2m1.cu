@@ -53,7 +53,7 @@
 //     memory and 72 where V comes from shared memory, 970 a tile; beside them the widening
 //     and the weights keep shared memory busy, 0.6 of its cycles in all.  Tensor cores
 //     16 % of their rate, issue slots 51 %;
-//   16 blocks of 16, context 512 to 131,072: 139 us, alike (flushed 143, bf16 150,
+//   16 blocks of 16, context 512 to 131,072: 137 us, alike (flushed 143, bf16 150,
 //     E4M3 158);
 //   without references that grow these two would take 131 and 127: each time one does
 //     its stream is held up for about 2,000 clocks;

@@ -28,7 +28,7 @@
 // Tensor memory: S of stream 0 | 1, 2 x 64 columns each, O of stream 0 | 1, 128 each.
 //
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16): prompt chunk, 2 x
-// 2,048 rows, context 8,192 to 16,384, 922 us, 1.13 PFLOP/s, 0.58 of the measured burst
+// 2,048 rows, context 8,192 to 16,384, 929 us, 1.12 PFLOP/s, 0.57 of the measured burst
 // (a bf16 cache 746, E4M3 1,253).  Tensor cores 49 % of their rate, issue slots 59 % (632 M
 // instructions), shared memory 0.73 of its cycles: no unit is
 // at its end, the chain scores, weights, values of either stream is what is left.
