@@ -197,27 +197,23 @@ __device__ __forceinline__ void read_record(Record<HD>& r, const uint8_t* p, boo
   }
 }
 template <int HD>
-__device__ __forceinline__ void read_scales(Record<HD>& r, const uint8_t* p) {
+__device__ __forceinline__ void read_scales(uint32_t (&scale)[HD / 32], const uint8_t* p) {
   if (HD == 128) {
     const uint4 w = *reinterpret_cast<const uint4*>(p + HD / 2);
-    r.scale[0] = w.x;
-    r.scale[1] = w.y;
-    r.scale[HD / 64] = w.z;
-    r.scale[HD / 32 - 1] = w.w;
+    scale[0] = w.x;
+    scale[1] = w.y;
+    scale[HD / 64] = w.z;
+    scale[HD / 32 - 1] = w.w;
   } else {
     const uint2 w = *reinterpret_cast<const uint2*>(p + HD / 2);
-    r.scale[0] = w.x;
-    r.scale[HD / 32 - 1] = w.y;
+    scale[0] = w.x;
+    scale[HD / 32 - 1] = w.y;
   }
 }
-// The biased exponent of the largest scale.
+// The biased exponent of a record's largest scale, within limits.
 template <int HD>
-__device__ __forceinline__ int largest_exponent(const Record<HD>& r, int least) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < HD / 32; ++i) m = __vmaxu2(m, r.scale[i] & 0x7FFF7FFFu);
-  const int e = (int)(max(m & 0xFFFFu, m >> 16) >> 7);
-  return min(max(e, least), kMost);
+__device__ __forceinline__ int largest_exponent(Record<HD>& r, const uint8_t* p, int least) {
+  return min(max((int)(largest_scale<HD>(r.scale, p) >> 7), least), kMost);
 }
 // Scale i of the record, brought to the row's power of two, as a pair of fp16.
 template <int HD>
@@ -730,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
         Record<HD> x;
         if (of_v) {
           read_record<HD>(x, from + kKT * C::kRec, in_v);
-          const float f = __uint_as_float((uint32_t)(254 + kScaleExp - largest_exponent<HD>(x, kLeastV)) << 23);
+          const float f = __uint_as_float((uint32_t)(254 + kScaleExp - largest_exponent<HD>(x, from + kKT * C::kRec, kLeastV)) << 23);
           ok = warp_wait_on(&c->pv_done[i], before, stop, a.status);
           if (!ok) break;
           // (128-byte swizzle: chunk c of row r lies at c ^ r % 8)
@@ -755,15 +751,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_kernel(const
           }
         } else {
           // V's exponents are wanted with the scores
-          uint32_t ev = 127;
+          int ev = 0;
           if (in_v) {
-            read_scales<HD>(x, from + kKT * C::kRec);
-            ev = largest_exponent<HD>(x, kLeastV);
+            uint32_t scale[HD / 32];
+            read_scales<HD>(scale, from + kKT * C::kRec);
+            ev = (int)(largest_scale<HD>(scale, from + kKT * C::kRec) >> 7);
           }
+          if (__any_sync(0xffffffffu, ev == 0)) {
+            const int top = (int)__reduce_max_sync(0xffffffffu, (unsigned)ev);
+            if (ev == 0) ev = top ? top - kZeroBelow : kZeroV;
+          }
+          ev = min(max(ev, kLeastV), kMost);
           read_record<HD>(x, from, in && !((c->bad[0][slot] >> (r >> shift)) & 1u));
-          const uint32_t ek = largest_exponent<HD>(x, kLeastK);
-          const float f = __uint_as_float((254 + kScaleExp - ek) << 23);
-          c->exponent[T & 7u][r] = ek | (ev << 16);
+          const int ek = largest_exponent<HD>(x, from, kLeastK);
+          const float f = __uint_as_float((uint32_t)(254 + kScaleExp - ek) << 23);
+          c->exponent[T & 7u][r] = (uint32_t)ek | ((uint32_t)ev << 16);
           ok = warp_wait_on(&c->k_empty[i], before, stop, a.status);
           if (!ok) break;
           tc_fence_after();

@@ -111,13 +111,9 @@ __device__ __forceinline__ int row_exponent(const uint8_t* rec, bool there, uint
     scale[0] = w.x;
     scale[HD / 32 - 1] = w.y;
   }
-  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < HD / 32; ++i) {
-    scale[i] = there ? scale[i] : 0u;  // zeros make any codes zeros
-    m = __vmaxu2(m, scale[i] & 0x7FFF7FFFu);
-  }
-  return (int)(max(m & 0xFFFFu, m >> 16) >> 7);
+  for (int i = 0; i < HD / 32; ++i) scale[i] = there ? scale[i] : 0u;  // zeros make any codes zeros
+  return (int)(largest_scale<HD>(scale, rec) >> 7);
 }
 // Half of a record's codes as fp16 over 2^(e - kScaleExp), into a row of a widened half (`to`: the
 // address of its first chunk under the 128-byte swizzle).
@@ -436,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_e2m1_rows_kernel(
         const uint8_t* const rec = ring_s + slot * C::kSlot + at * C::kRec;
         uint32_t scale[HD / 32];
         int ev = row_exponent<HD>(rec + kKT * C::kRec, there, scale);
-        ev = min(max((int)__reduce_max_sync(0xffffffffu, (unsigned)ev), kLeastV), kMost);
+        ev = (int)__reduce_max_sync(0xffffffffu, (unsigned)ev);
+        ev = ev ? min(max(ev, kLeastV), kMost) : kZeroV;
         int e = ev;
         if (!of_v) {
           e = row_exponent<HD>(rec, there, scale);

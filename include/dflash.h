@@ -567,7 +567,10 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  * 2^-18 of the row's largest, times the power of two of its value row, keeps fewer
  * bits, the last at 2^-28.  With R above 128 that power is one for 32 neighbouring
  * positions (2^-34 of the largest scale among them may be lost), and the last bit of a
- * weight is at 2^-32.  Scores beyond float32's range are undefined. */
+ * weight is at 2^-32.  Scales of 1 in blocks of zeros count for none of this: a row of
+ * zeros has 2^-32 of its neighbours' power (R above 128: the same one), at least 2^-64.
+ * What lies 2^-126 below a row's largest weight times power is left out of its sums, too.
+ * Scores beyond float32's range are undefined. */
 size_t dflash_paged_attention_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim,
                                               int max_rows);
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_batch* batch,
