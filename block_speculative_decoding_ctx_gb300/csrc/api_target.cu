@@ -187,6 +187,7 @@ int dflash_rope_frequencies(int rotary_dim, double theta, double stretch, double
     return DFLASH_ERR_ARG;
   if (trained > 0.0 && !(slow < fast && std::isfinite(slow) && std::isfinite(fast) && std::isfinite(fast - slow)))
     return DFLASH_ERR_ARG;
+  double f[64];
   for (int j = 0; j < rotary_dim / 2; ++j) {
     const double w = std::pow(theta, -2.0 * j / rotary_dim);
     double g = 0.0;
@@ -194,8 +195,10 @@ int dflash_rope_frequencies(int rotary_dim, double theta, double stretch, double
       g = (trained * w / 6.283185307179586 - slow) / (fast - slow);
       g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
     }
-    frequencies[j] = g * w + (1.0 - g) * w / stretch;
+    f[j] = g * w + (1.0 - g) * w / stretch;
+    if (!std::isfinite(f[j])) return DFLASH_ERR_ARG;
   }
+  std::memcpy(frequencies, f, rotary_dim / 2 * sizeof(double));
   return DFLASH_OK;
 }
 

@@ -505,7 +505,8 @@ typedef struct dflash_rope {
  *     stay, slow ones are stretched (B. Peng et al., "YaRN: Efficient context
  *     window extension of large language models", 2023, section 3.2).
  * rotary_dim a multiple of 32 from 32 to 128; theta > 0; stretch > 0; trained
- * >= 0; slow < fast where trained > 0; all finite. */
+ * >= 0; slow < fast where trained > 0; all finite, the frequencies too
+ * (DFLASH_ERR_ARG, with none of them written). */
 int dflash_rope_frequencies(int rotary_dim, double theta, double stretch, double trained, double slow,
                             double fast, double* frequencies);
 
