@@ -9,6 +9,7 @@ object.  No cmake, no torch extension machinery.
 import concurrent.futures
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -20,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdflash.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xptxas", "-v", "-Xcompiler", "-fPIC,-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 
 
@@ -36,8 +37,27 @@ def _headers():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _log(obj):
+    return obj[:-2] + ".ptxas"
+
+
+def registers(unit):
+    """Registers of a thread at launch, as ptxas gave them to each kernel of a built unit:
+    {mangled name: registers}.  A kernel that moves registers between its warps counts on
+    their number and is refused at launch with any other."""
+    out, name = {}, None
+    with open(_log(os.path.join(BUILD, unit + ".o"))) as f:
+        for line in f:
+            m = re.search(r"Function properties for (\S+)", line)
+            name = m.group(1) if m else name
+            m = re.search(r"Used (\d+) registers", line)
+            if m and name:
+                out[name], name = int(m.group(1)), None
+    return out
+
+
 def _stale(src, obj, hdr_mtime):
-    if not os.path.exists(obj):
+    if not os.path.exists(obj) or not os.path.exists(_log(obj)):
         return True
     t = os.path.getmtime(obj)
     return os.path.getmtime(src) > t or hdr_mtime > t
@@ -66,6 +86,9 @@ def build(verbose=False, extra_flags=()):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+        if "-c" in cmd:
+            with open(_log(cmd[-1]), "w") as f:
+                f.write(r.stderr)
         return r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
