@@ -553,7 +553,10 @@ def dflash_paged_gather(cache, k, v, row_start, kv_len, page_table, ws, stream=N
 
 
 def dflash_rope_frequencies(rotary_dim, theta, stretch=1.0, trained=0.0, slow=1.0, fast=4.0):
-    """Radians per position of every pair, a list of rotary_dim / 2 floats."""
+    """Radians per position of every pair, a list of rotary_dim / 2 floats.
+    With trained > 0 (scaling by parts) slow and fast are the model's, as theta
+    is; the defaults are no model's in particular (the paper that the header
+    cites has slow=1, fast=32)."""
     _c_ints("rotary_dim", rotary_dim)
     f = (ctypes.c_double * 64)()  # the largest rotary_dim's
     _check(lib().dflash_rope_frequencies(rotary_dim, theta, stretch, trained, slow, fast, f), "dflash_rope_frequencies")
@@ -608,7 +611,8 @@ def dflash_paged_attention_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_
 def dflash_paged_attention(cache, q, out, row_start, kv_len, page_table, max_rows, ws, lse=None,
                            scale=None, causal=True, window=0, stream=None):
     """q, out [rows, n_q_heads, head_dim]; lse float32 [rows, n_q_heads] or
-    None; scale None: 1 / sqrt(head_dim)."""
+    None; scale None: 1 / sqrt(head_dim).  max_rows: the largest request's new
+    rows; over a cache in 4 bits a bound far above them costs time."""
     index, hd = cache.index, cache._rows[1]
     shape = q.shape
     if out.shape != shape or q.dtype is not out.dtype or len(shape) != 3 or shape[2] != hd:

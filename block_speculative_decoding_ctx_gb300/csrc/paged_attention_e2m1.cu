@@ -13,12 +13,11 @@
 // its threads have keys; and the widened K goes from the codes straight to tensor
 // memory as an operand, a row to a lane, without a trip through shared memory, which
 // is the busiest part here.  Calls with more than 128 packed rows to a request go to
-// paged_attention_e2m1_rows.cu (from 65 on it would take ragged blocks of 16, 80 rows,
-// from 143 to 162 us).
+// paged_attention_e2m1_rows.cu (launch_paged_attention_e2m1 below).
 //
 // Values.  A code times its scale has 10 significant bits.  A row's scales are
 // brought to [2^12, 2^13) by a power of two of the row's largest, so that the
-// products are fp16 values, exact but for 2^-36 of the largest scale; the power comes
+// products are fp16 values, exact but for 2^-34 of the largest scale; the power comes
 // back in float32, for K as a factor of the scores, for V added to the exponent of
 // the weights.  Queries become fp16 times a power of two per row.
 //   What a row's reference follows is the largest of weight times the power of its
@@ -45,18 +44,21 @@
 // Tensor memory: S, 256 columns; O, 128; K0 | K1, head_dim / 2 each.
 //
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16):
-//   32 requests, blocks of 8, context 8,192: 138 us for 341 MB, 2.5 TB/s, 0.37 of the
-//     measured copy (with L2 flushed 145; a bf16 cache 193, E4M3 182).  The products'
+//   32 requests, blocks of 8, context 8,192: 143 us for 341 MB, 2.4 TB/s, 0.36 of the
+//     measured copy (with L2 flushed 149; a bf16 cache 193, E4M3 182).  The products'
 //     operands: in a timeline of a CTA the issuer is never without a product to issue, and a
 //     tile's take 1,850 clocks, 750 for the scores and 1,100 for the values.  Alone a
 //     product (16 deep, of up to 64 columns) takes 49 clocks where K comes from tensor
 //     memory and 72 where V comes from shared memory, 970 a tile; beside them the widening
 //     and the weights keep shared memory busy, 0.6 of its cycles in all.  Tensor cores
-//     16 % of their rate, issue slots 51 %;
-//   16 blocks of 16, context 512 to 131,072: 137 us, alike (flushed 143, bf16 150,
-//     E4M3 158);
-//   without references that grow these two would take 131 and 127: each time one does
-//     its stream is held up for about 2,000 clocks;
+//     16 % of their rate, issue slots 52 %;
+//   16 blocks of 16, context 512 to 131,072: 140 us (flushed 147, bf16 150, E4M3 158).
+//     74 key tiles an SM take some 3,400 clocks each, where the products alone take
+//     1,528: above 64 rows both warpgroups share a tile and S has two buffers, so that
+//     tiles go through the chain scores, weights, values nearly one after another, and
+//     80 rows take 96 columns;
+//   without references that grow these two took 131 and 127 where they took 138 and 137:
+//     each time one does its stream is held up for about 2,000 clocks;
 //   one token, context 1,000: latency, 12 us.
 //
 // All waits are bounded.  When one gives up, the softmax warps run on to the end of
@@ -994,6 +996,13 @@ int launch_paged_attention_e2m1(const dflash_paged_cache& c, const PagedAttnArgs
   k.k_stride = c.k_page_stride;
   k.v_stride = c.v_page_stride;
   k.bf16 = type == DFLASH_TYPE_BF16;
+  // By the bound max_rows, for what a request really has is on the device.  With 5 query
+  // heads to a KV head over 8,192 keys: 16 requests of 25 rows (125 packed) take 141 us here
+  // and 140 there, of 20 137 and 133; ragged blocks of 16 (80) 140 and 160, blocks of 8 (40)
+  // 143 and 213, 32 single tokens 108 and 198.  So a max_rows above 128 packed rows costs a
+  // call of few rows up to that much.  (A max_rows above 64 of them, 121 for the tokens: the
+  // room for weights is taken from the slots.)  31 tokens beside a chunk of 2,048 rows
+  // take 624 us in one call, 105 and 384 in two.
   if ((long long)a.max_rows * a.group > kRows) return launch_paged_attention_e2m1_rows(k, c.head_dim, s);
   return c.head_dim == 128 ? launch<128>(k, s) : launch<64>(k, s);
 }

@@ -28,10 +28,14 @@
 // Tensor memory: S of stream 0 | 1, 2 x 64 columns each, O of stream 0 | 1, 128 each.
 //
 // What bounds it, measured on GB300 (8 KV heads of 128, groups of 5, bf16): prompt chunk, 2 x
-// 2,048 rows, context 8,192 to 16,384, 929 us, 1.12 PFLOP/s, 0.57 of the measured burst
-// (a bf16 cache 746, E4M3 1,253).  Tensor cores 49 % of their rate, issue slots 59 % (632 M
-// instructions), shared memory 0.73 of its cycles: no unit is
-// at its end, the chain scores, weights, values of either stream is what is left.
+// 2,048 rows, context 8,192 to 16,384, 948 us, 1.10 PFLOP/s, 0.56 of the measured burst
+// (a bf16 cache 746, E4M3 1,253).  The products as they are issued: a score product of 64
+// keys with both operands in shared memory takes 80 clocks, for half the work of one of 128
+// keys in 112; a job's 8 of them and 4 of the values (79 each) 956, a tile of both streams
+// 3,824.  62,272 tiles of items are 410 an SM, 1.57 M of the kernel's 1.75 M cycles.  The
+// tensor cores count 48 % of their rate, since the operands' reads are no work; issue slots
+// 59 % (643 M instructions), shared memory 0.73 of its cycles.  Scores of 128 keys at once
+// would take 3,056 clocks a tile, queries in tensor memory 2,848; neither is built.
 //
 // All waits are bounded, as in paged_attention_e2m1.cu.
 #include "paged_e2m1.cuh"

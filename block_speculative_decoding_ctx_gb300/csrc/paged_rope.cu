@@ -19,30 +19,35 @@
 // 16 values (E2M1) is two lanes' lower runs, two lanes' upper runs or one lane's
 // both, and one shuffle finds its largest magnitude.
 //
-// Measured on GB300 (40 query and 8 KV heads of 128), bytes at the measured copy's rate
-// in brackets: prompts rotated into a 16-bit cache, queries beside them (782 MB) 125 us
-// [0.93], into E4M3 (728 MB) 151 us [0.72], into 4 bits (705 MB) 133 us [0.79]; prompts
-// into 4 bits as they come (237 MB) 57 us [0.62]: latency of the loads beside the
-// instructions (59 % of the issue slots, 190 a warp for 16 values a thread; 64 us with
-// 250, before a thread's pieces shared their place); a step's 256 rows 10 us, the host's
-// launch.
+// Measured on GB300 (40 query and 8 KV heads of 128), calls back to back, bytes at the
+// measured copy's rate in brackets: prompts rotated into a 16-bit cache, queries beside
+// them (782 MB) 125 us [0.93], into E4M3 (728 MB) 151 us [0.72], into 4 bits (705 MB) 134
+// us [0.79]; prompts into 4 bits as they come (237 MB) 50 us [0.70], 57 with L2 flushed
+// [0.62].  The last one's loads are asked for only after the turn before has stored all
+// (54 % of the issue slots, 194 instructions a warp for 16 values a thread).  The rotated,
+// quantised ones have more alive than the 64 registers that four blocks an SM leave a
+// thread: 8 bytes stored and 48 loaded again into E4M3, 28 and 60 into 4 bits (the fp16
+// append into 4 bits without rotation 28 and 40, the others none).  A step's 256 rows 11 to
+// 13 us, the host's launch.  The sweeps below are of this code, in the same four cases.
 #include "paged_rows.cuh"
 
 namespace dfl {
 namespace {
 
-constexpr int kThreads = 256;  // (128: rotated prompts 133 us for 131, prompts into 4 bits 59 for 57)
-// Pieces of a thread on their way (1 / 2 / 3: rotated prompts 135 / 131 / 137 us).
+constexpr int kThreads = 256;  // (128: 133 / 160 / 133 / 56 us)
+// Pieces of a thread on their way (with rotation, 1 / 2 / 3: 130 / 125 / 132 us, into E4M3
+// 148 / 151 / 193, into 4 bits 123 / 134 / 159: one count for all).
 constexpr int kPieces = 2;
 constexpr int kMaxRows = 32;   // of a block
 // (row, head) of a block, as far as that is no single row (256 / 512 / 1,024: rotated prompts
-// 133 / 131 / 137 us, prompts into 4 bits 61 / 57 / 57).
+// 129 / 125 / 132 us, into E4M3 156 / 151 / 151, into 4 bits 139 / 134 / 135, prompts into 4
+// bits as they come 54 / 50 / 50).
 constexpr int kMostUnits = 512;
 
 // Cosine and sine of `turns` 2^-64ths of a turn, times f, each rounded about once: what
 // they turn is rounded into 4 bits next, and a value that falls on the other side of a
 // code's border is a whole step off (with sincospif, 1.8e-5 of the 16-bit results differ for
-// 1.4e-5, and rotated prompts take 133 us for 135).  Beside the nearest quarter turn, the
+// 1.4e-5, as fast).  Beside the nearest quarter turn, the
 // angle is p + e, p a float32 of at most pi / 4 and e its rest; Taylor's series of sine to
 // p^11 and of cosine to p^10 (2^-36 and 2^-33 are left out), added to their first terms last.
 __device__ __forceinline__ float2 cos_sin(unsigned long long turns, float f) {
@@ -68,7 +73,7 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long turns, float f) {
 }
 // x c - y s and y c + x s.  (Adding the rounded product's rounding back, Kahan's difference
 // of products, makes 1.2e-5 of the 16-bit results other than the exact ones' rounding for
-// 1.4e-5, and rotated prompts take 143 us for 135.)
+// 1.4e-5, and rotated prompts take 132 us for 125, into 4 bits 146 for 134.)
 __device__ __forceinline__ void turn2(float2& x, float2& y, float2 c, float2 s) {
   const float2 ns = make_float2(-s.x, -s.y);
   const float2 a = fma2(x, c, mul2(y, ns)), b = fma2(y, c, mul2(x, s));
@@ -194,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, 4) paged_rope_kernel(const PagedRope
       float2 f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = unpack16<BF16>(v[e]);
-      // the next turn's rows, as early as their registers are free (without rotation, where
-      // more is live here, this is slower: 63 us for 57; rotated prompts 131 for 135)
+      // the next turn's rows, as early as their registers are free (rotated prompts 125 us for
+      // 130, into E4M3 151 for 170; without rotation, where more is live here, 57 for 50)
       if (ROPE) load_row(u0 + kTurn, i);
       if (p.turned) {
         const float2* t = turn_s[p.row];
@@ -331,7 +336,7 @@ int launch_rope(const PagedRopeArgs& a, cudaStream_t s) {
   const long long each = ceil_div(a.m.batch.rows, 608);  // 4 blocks for each of 152 SMs come first
   const int per_row = a.n_q + 2 * a.m.n_kv;
   const int most = min(kMaxRows, max(1, kMostUnits / per_row));
-  // ... and what is more comes in equal shares (prompts into 4 bits 57 us, 59 with blocks of `most`)
+  // ... and what is more comes in equal shares (prompts into 4 bits 50 us, 52 with blocks of `most`)
   const long long waves = max(1ll, (each + most - 1) / most);
   const int rows = (int)max(1ll, (each + waves - 1) / waves);
   const int grid = max(1, ceil_div(a.m.batch.rows, rows));

@@ -503,7 +503,10 @@ typedef struct dflash_rope {
  *     context that the model was trained on; with g = (r - slow) / (fast - slow)
  *     cut to [0, 1] its frequency is g w_j + (1 - g) w_j / stretch: fast pairs
  *     stay, slow ones are stretched (B. Peng et al., "YaRN: Efficient context
- *     window extension of large language models", 2023, section 3.2).
+ *     window extension of large language models", 2023, section 3.2).  slow and
+ *     fast belong to the model as theta does: the paper's own models have 1 and 32,
+ *     others have other values, and some blend by a pair's number instead of r;
+ *     their frequencies go to dflash_rope_init as they are.
  * rotary_dim a multiple of 32 from 32 to 128; theta > 0; stretch > 0; trained
  * >= 0; slow < fast where trained > 0; all finite, the frequencies too
  * (DFLASH_ERR_ARG, with none of them written). */
@@ -550,7 +553,10 @@ int dflash_paged_gather(const dflash_paged_cache* cache, const dflash_paged_batc
  *   type      DFLASH_TYPE_BF16 or _F16: q and out; a 16-bit cache has the same
  *   lse       float32 [rows, n_q_heads] or NULL
  *   max_rows  no request has more new rows than this; at most `rows`; 0: nothing
- *             is launched
+ *             is launched.  It is also what the kernel over an E2M1 cache is chosen
+ *             by (R below, above 128 or not), and with it the rounding: a bound far
+ *             above what the requests have costs time (32 single tokens over 8,192
+ *             keys, 5 query heads to a KV head: 108 us with 1, 198 from 26 on)
  *   scale     finite and > 0;  causal 0 or 1;  window >= 0, 0 = none
  * n_q_heads is a multiple of n_kv_heads, at most 65,535.  With R = max_rows *
  * n_q_heads / n_kv_heads, R and B * ceil(R / 256) (E2M1: / 128) are at most 2^30, and
